@@ -110,7 +110,9 @@ ZS3_API const char* zs3_last_error(void);
  * own start and end timestamps into start_event / stop_event (hipEvent_t,
  * created by the caller, either may be NULL), as hipExtLaunchKernel does; no
  * extra commands are enqueued.  The setting applies to exactly one launch
- * (calls that launch two kernels time the first).  Always returns ZS3_OK. */
+ * (calls that launch two kernels time the first).  The calls of
+ * zs3_lowbit.h do not take part: they leave the setting for the next other
+ * launch.  Always returns ZS3_OK. */
 ZS3_API zs3_status zs3_time_next_launch(void* start_event, void* stop_event);
 
 /* ------------------------------------------------------------- layout

@@ -30,6 +30,9 @@ Modules:
   pin ``zero3`` (a second, differently structured derivation).
 * ``coordinator`` -- the trace-driven fetch/release coordinator as a
   step-by-step simulation (imported as ``oracle.coordinator``).
+* ``lowbit`` -- AdamW over a tensor with 32- or 8-bit states, and the 4-bit
+  wire of the coalesced gather and reduce-scatter (imported as
+  ``oracle.lowbit``).
 
 Parity status of each function is stated in its docstring; every function
 has an independent pin.  (The decoupled weight-decay branch of

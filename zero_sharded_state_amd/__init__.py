@@ -1,7 +1,7 @@
 """Python binding of libzs3, the ZeRO-3 shard-step library for MI355X.
 
 Argument marshalling only: every function below has the name of a C entry
-point in ``include/zs3.h`` and forwards to it through ctypes.  Device
+point in ``include/zs3.h`` or ``include/zs3_lowbit.h`` and forwards to it through ctypes.  Device
 buffers may be given as torch tensors (their data pointers are passed) or as
 raw integer device addresses; ``stream`` may be a ``torch.cuda.Stream``, a
 raw ``hipStream_t`` integer, or ``None`` for torch's current stream.  A
@@ -12,6 +12,7 @@ built, the first call raises ``RuntimeError`` -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import List, Optional, Sequence, Tuple
 
@@ -29,6 +30,7 @@ ZS3_ENOMEM = -8
 
 ZS3_FP16 = 1
 ZS3_BF16 = 2
+ZS3_FP32 = 3
 ZS3_PACK = 1
 ZS3_UNPACK = 2
 ZS3_REDUCE = 4
@@ -38,7 +40,10 @@ ZS3_TRACE_INVALID, ZS3_TRACE_RECORD, ZS3_TRACE_COMPLETE = 0, 1, 2
 ZS3_PARAM_NOT_AVAILABLE, ZS3_PARAM_INFLIGHT, ZS3_PARAM_AVAILABLE = 0, 1, 2
 ZS3_GATHER_CURRENT, ZS3_GATHER_PREFETCH = 0, 1
 
-DTYPES = {"fp16": ZS3_FP16, "bf16": ZS3_BF16}
+ZS3_EXP_AVG, ZS3_EXP_AVG_SQ = 1, 2
+ZS3_ROUND_NEAREST, ZS3_ROUND_STOCHASTIC = 0, 1
+
+DTYPES = {"fp16": ZS3_FP16, "bf16": ZS3_BF16, "fp32": ZS3_FP32}
 
 # Every exported symbol of include/zs3.h.
 EXPORTS = (
@@ -53,6 +58,12 @@ EXPORTS = (
     "zs3_coord_fetch", "zs3_coord_release",
     "zs3_coord_release_all", "zs3_coord_reset_step", "zs3_coord_info", "zs3_coord_param_status",
     "zs3_coord_trace_signature",
+)
+
+# And of include/zs3_lowbit.h.
+EXPORTS_LOWBIT = (
+    "zs3_adamw_tensors", "zs3_moment8_bytes", "zs3_moment8_read", "zs3_mx4_sizes", "zs3_gather_coalesced_mx4",
+    "zs3_reduce_scatter_coalesced_mx4",
 )
 
 
@@ -79,6 +90,30 @@ class zs3_adam_params(ctypes.Structure):
         ("eps", ctypes.c_double),
         ("weight_decay", ctypes.c_double),
         ("step", ctypes.c_int64),
+    ]
+
+
+class zs3_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("numel", ctypes.c_int64),
+        ("id", ctypes.c_int64),
+        ("master", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("param", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p),
+        ("lr_scale", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+    ]
+
+
+class zs3_moment8(ctypes.Structure):
+    _fields_ = [
+        ("numel", ctypes.c_int64),
+        ("moment", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("kind", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -136,6 +171,16 @@ _SIGNATURES = {
     "zs3_coord_info": (_c_i32, [_c_p, _p_i32, _p_i64, _p_i32, _p_i32]),
     "zs3_coord_param_status": (_c_i32, [_c_p, _c_i64, _p_i32]),
     "zs3_coord_trace_signature": (_c_i32, [_c_p, _p_u64, _p_u64, _p_i32]),
+    "zs3_adamw_tensors": (_c_i32, [_c_i32, _c_i32, _c_i32, _c_i32, ctypes.POINTER(zs3_adamw_tensor), _c_p, _c_p,
+                                   ctypes.POINTER(zs3_adam_params), ctypes.c_uint64, _c_p]),
+    "zs3_moment8_bytes": (_c_i32, [_c_i64, _p_i64]),
+    "zs3_moment8_read": (_c_i32, [_c_i32, _c_i32, ctypes.POINTER(zs3_moment8), _c_p]),
+    "zs3_mx4_sizes": (_c_i32, [_c_p, _c_i32, _p_i64, _p_i64, _p_i64]),
+    "zs3_gather_coalesced_mx4": (_c_i32, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _p_i64, _c_p, _c_p,
+                                          ctypes.POINTER(_c_p), _c_p, _p_i64, _c_p]),
+    "zs3_reduce_scatter_coalesced_mx4": (_c_i32, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _p_i64, ctypes.POINTER(_c_p),
+                                                  _c_p, ctypes.POINTER(_c_p), _c_p, _c_p, _c_i32, ctypes.c_uint64,
+                                                  _c_p]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -166,9 +211,9 @@ def _check(status: int) -> None:
 def _ptr(x) -> Optional[int]:
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    return int(x.data_ptr())
+    if hasattr(x, "data_ptr"):
+        return int(x.data_ptr())
+    return operator.index(x)       # an address: any integer type
 
 
 def _stream(s) -> Optional[int]:
@@ -400,6 +445,85 @@ def zs3_init_master(layout: int, rank: int, dtype, begin: int, end: int, shard_f
                     exp_avg_sq=None, stream=None) -> None:
     _check(lib().zs3_init_master(layout, rank, _dtype(dtype), int(begin), int(end), _ptr(shard_flat), _ptr(master),
                                  _ptr(exp_avg), _ptr(exp_avg_sq), _stream(stream)))
+
+
+# ------------------------------------------------- AdamW over a tensor list
+
+def zs3_adamw_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
+    """The list that ``zs3_adamw_tensors`` steps: one dict a tensor with numel,
+    id, master, grad, exp_avg, exp_avg_sq and, where they differ from these,
+    param=None, lr_scale=1.0, weight_decay=0.0.  It holds addresses only: a
+    caller keeps it for as long as its buffers stay where they are."""
+    out = (zs3_adamw_tensor * max(1, len(tensors)))()
+    for o, t in zip(out, tensors):
+        o.numel, o.id = int(t["numel"]), int(t["id"])
+        o.master, o.grad, o.param = _ptr(t["master"]), _ptr(t["grad"]), _ptr(t.get("param"))
+        o.exp_avg, o.exp_avg_sq = _ptr(t["exp_avg"]), _ptr(t["exp_avg_sq"])
+        o.lr_scale, o.weight_decay = float(t.get("lr_scale", 1.0)), float(t.get("weight_decay", 0.0))
+    out.count = len(tensors)
+    return out
+
+
+def zs3_adamw_tensors(dtype, grad_dtype, state_bits: int, tensors, scale, nonfinite, hp, seed: int = 0,
+                      stream=None) -> None:
+    """``tensors``: what ``zs3_adamw_tensor_list`` gives, or the dicts."""
+    arr = tensors if isinstance(tensors, ctypes.Array) else zs3_adamw_tensor_list(tensors)
+    p = _hp(hp)
+    _check(lib().zs3_adamw_tensors(_dtype(dtype), _dtype(grad_dtype), int(state_bits), arr.count, arr, _ptr(scale),
+                                   _ptr(nonfinite), ctypes.byref(p), int(seed), _stream(stream)))
+
+
+def zs3_moment8_bytes(numel: int) -> int:
+    b = ctypes.c_int64()
+    _check(lib().zs3_moment8_bytes(int(numel), ctypes.byref(b)))
+    return b.value
+
+
+def zs3_moment8_list(moments: Sequence[dict]) -> ctypes.Array:
+    """The list that ``zs3_moment8_read`` reads: one dict a moment with numel,
+    kind, moment and out."""
+    out = (zs3_moment8 * max(1, len(moments)))()
+    for o, t in zip(out, moments):
+        o.numel, o.kind, o.moment, o.out = int(t["numel"]), int(t["kind"]), _ptr(t["moment"]), _ptr(t["out"])
+    out.count = len(moments)
+    return out
+
+
+def zs3_moment8_read(out_dtype, moments, stream=None) -> None:
+    """``moments``: what ``zs3_moment8_list`` gives, or the dicts."""
+    arr = moments if isinstance(moments, ctypes.Array) else zs3_moment8_list(moments)
+    _check(lib().zs3_moment8_read(_dtype(out_dtype), arr.count, arr, _stream(stream)))
+
+
+# ------------------------------------------------------------ the 4-bit wire
+
+def zs3_mx4_sizes(layout: int, ds_ids: Sequence[int]) -> Tuple[int, int]:
+    """(blocks, bytes) of a bucket's chunk."""
+    a, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().zs3_mx4_sizes(layout, len(ds_ids), _i64s(ds_ids), ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+def zs3_gather_coalesced_mx4(layout: int, rank: int, dtype, mode: int, ds_ids: Sequence[int], shard_flat=None,
+                             own_chunk=None, rank_chunks: Optional[Sequence] = None, full_flat=None,
+                             stream=None) -> List[int]:
+    n = len(ds_ids)
+    offs = (ctypes.c_int64 * max(1, n))()
+    chunks = _ptrs(rank_chunks) if rank_chunks is not None else None
+    _check(lib().zs3_gather_coalesced_mx4(layout, rank, _dtype(dtype), mode, n, _i64s(ds_ids), _ptr(shard_flat),
+                                          _ptr(own_chunk), chunks, _ptr(full_flat), offs, _stream(stream)))
+    return list(offs[:n])
+
+
+def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, ds_ids: Sequence[int],
+                                     grads: Optional[Sequence] = None, send=None,
+                                     recv_chunks: Optional[Sequence] = None, grad_flat=None, partials=None,
+                                     rounding: int = ZS3_ROUND_NEAREST, seed: int = 0, stream=None) -> None:
+    g = _ptrs(grads) if grads is not None else None
+    r = _ptrs(recv_chunks) if recv_chunks is not None else None
+    _check(lib().zs3_reduce_scatter_coalesced_mx4(layout, rank, _dtype(dtype), mode, len(ds_ids), _i64s(ds_ids), g,
+                                                  _ptr(send), r, _ptr(grad_flat), _ptr(partials), int(rounding),
+                                                  int(seed), _stream(stream)))
 
 
 # ------------------------------------------------------------- coordinator

@@ -1,0 +1,787 @@
+// HIP kernels of the low-bit operators for gfx950 (MI355X): AdamW over a list
+// of tensors (states in 32 or 8 bits), and quantising, widening and averaging
+// on the 4-bit wire.
+//
+// All of it streams through HBM once, so the rules are those of the other
+// kernels of this library: whole-line loads and stores, each byte touched
+// once, enough of it in flight.  What is particular here:
+//  - a block of 32 elements shares a power-of-two scale, so dividing by the
+//    scale is exact and the codes depend on the value alone;
+//  - a block lies in neighbouring lanes (8 lanes of 4 elements, or 4 lanes of
+//    8), and its largest magnitude is found with lane permutations (DPP) in
+//    registers, with no LDS and no barrier;
+//  - gfx950's scaled conversions do the rounding: cvt_scalef32_pk_fp4_f32 (to
+//    nearest even), cvt_scalef32_sr_pk_fp4_f32 and cvt_scalef32_sr_fp8_f32
+//    (stochastic: rounded up where the discarded fraction plus the random
+//    word, read as a fraction, reaches one);
+//  - loads and stores carry the alignment that the data has (2 bytes for
+//    16-bit views at odd offsets): global memory instructions of this target
+//    take any alignment, so there is one path for all of them.
+//
+// Floating point: compiled with -ffp-contract=off, so every fp32 expression is
+// the sequence of operations it spells.
+
+#include <hip/hip_runtime.h>
+
+#include "lowbit.hpp"
+#include "zs3_internal.hpp"
+
+namespace zs3 {
+namespace {
+
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u2h __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u4h __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------------ 16 bits
+
+template <int D>
+__device__ __forceinline__ float widen(uint32_t h) {
+    if constexpr (D == kFP16) return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(h)));
+    else return __uint_as_float(h << 16);
+}
+
+// Round to nearest, ties to even; NaN stays NaN.
+template <int D>
+__device__ __forceinline__ uint32_t narrow(float f) {
+    if constexpr (D == kFP16) {
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+    } else {
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+    }
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+    return narrow<D>(a) | (narrow<D>(b) << 16);
+}
+
+// ------------------------------------------------------- lanes of a block
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
+    const uint32_t y = static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xf, 0xf, true));
+    return x > y ? x : y;
+}
+constexpr int kDppXor1 = 0xB1;          // quad_perm [1,0,3,2]
+constexpr int kDppXor2 = 0x4E;          // quad_perm [2,3,0,1]
+constexpr int kDppHalfMirror = 0x141;   // lane i of 8 <-> lane 7 - i
+
+__device__ __forceinline__ uint32_t max4lanes(uint32_t x) { return max_dpp<kDppXor2>(max_dpp<kDppXor1>(x)); }
+__device__ __forceinline__ uint32_t max8lanes(uint32_t x) { return max_dpp<kDppHalfMirror>(max4lanes(x)); }
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t mag(float f) { return __float_as_uint(f) & 0x7fffffffu; }
+
+constexpr uint32_t kInf = 0x7f800000u;
+
+// The scale byte for a block whose largest magnitude has the bits `top`
+// (comparing magnitudes as integers puts NaN above infinity above the
+// rest).  `carry` is added so that mantissas past the format's largest
+// carry into the exponent; emax is the exponent of the format's largest.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top, uint32_t carry, int emax, int highest) {
+    int s = static_cast<int>((top + carry) >> 23) - emax;
+    s = s < 1 ? 1 : s;
+    s = s > highest ? highest : s;
+    return top >= kInf ? 255u : static_cast<uint32_t>(s);
+}
+
+// The scale as a float: byte 255 gives infinity, which with the codes that
+// such a block holds reads back as a value that is not finite.
+__device__ __forceinline__ float scale_of(uint32_t s) { return __uint_as_float(s << 23); }
+
+// ---------------------------------------------------------- random words
+
+// A counter hash: two multiply-xorshift rounds over a Weyl sequence.  The
+// 32-bit multiplies take four issue slots each, and consecutive elements
+// share the first as an addition.
+constexpr uint32_t kWeyl = 0x9E3779B1u;
+__device__ __forceinline__ uint32_t weyl(int64_t i, uint32_t key0) {
+    return static_cast<uint32_t>(i) * kWeyl + key0 + static_cast<uint32_t>(static_cast<uint64_t>(i) >> 32) * 0x85157AF5u;
+}
+__device__ __forceinline__ uint32_t random_word(uint32_t x, uint32_t key1) {
+    x ^= x >> 16;
+    x *= 0x761BCE4Bu;
+    x ^= (x >> 15) ^ key1;
+    x *= 0xA0D73955u;
+    return x ^ (x >> 16);
+}
+
+// The list's tensor that tile b belongs to: each lane compares one prefix
+// and the wave counts them, one load where a search would make six.
+template <class PLAN>
+__device__ __forceinline__ int find_tensor(const PLAN& p, int32_t b, int lane) {
+    if (p.n == 1) return 0;
+    const bool past = lane < p.n && p.first_tile[lane + 1] <= b;
+    return __builtin_amdgcn_readfirstlane(__builtin_popcountll(__ballot(past)));
+}
+
+// --------------------------------------------------------- AdamW, 32 bits
+// Per element (one IEEE operation each, as the flat Adam step computes it):
+//   g = grad * scale;  w -= (lr*wd) * w;  m = b1*m + (1-b1)*g;
+//   v = b2*v + (1-b2)*(g*g);
+//   w -= lr * ((m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps));  param = round16(w)
+
+template <int G>
+struct Grad4 {
+    u2h h;
+    __device__ void load(const void* p, int64_t e) {
+        h = __builtin_nontemporal_load(reinterpret_cast<const u2h*>(static_cast<const uint16_t*>(p) + e));
+    }
+    __device__ float get(int q) const { return widen<G>((q & 1) ? h[q >> 1] >> 16 : h[q >> 1] & 0xffffu); }
+};
+template <>
+struct Grad4<3> {
+    f4 f;
+    __device__ void load(const void* p, int64_t e) {
+        f = __builtin_nontemporal_load(reinterpret_cast<const f4*>(static_cast<const float*>(p) + e));
+    }
+    __device__ float get(int q) const { return f[q]; }
+};
+template <int G>
+__device__ __forceinline__ float grad1(const void* p, int64_t e) {
+    if constexpr (G == 3) return static_cast<const float*>(p)[e];
+    else return widen<G>(static_cast<const uint16_t*>(p)[e]);
+}
+
+__device__ __forceinline__ void adamw32_1(float& w, float& m, float& v, float g, float lr, float lrwd,
+                                          const StepConsts& c) {
+    if (lrwd != 0.0f) w = w - lrwd * w;
+    m = c.b1 * m + c.omb1 * g;
+    v = c.b2 * v + c.omb2 * (g * g);
+    const float mh = m / c.bc1;
+    const float vh = v / c.bc2;
+    const float den = __builtin_sqrtf(vh) + c.eps;
+    w = w - lr * (mh / den);
+}
+
+template <int D, int G>
+__device__ __forceinline__ void adamw32_tile(const StepTensor& t, int64_t e0, int lane, float scale, bool skip,
+                                             const StepConsts& c) {
+    float* m32 = static_cast<float*>(t.exp_avg);
+    float* v32 = static_cast<float*>(t.exp_avg_sq);
+    if (e0 + 256 * kStepRuns <= t.numel) {
+        f4 W[kStepRuns], M[kStepRuns], V[kStepRuns];
+        Grad4<G> gr[kStepRuns];
+#pragma unroll
+        for (int k = 0; k < kStepRuns; ++k) {
+            const int64_t e = e0 + 256 * k + 4 * lane;
+            W[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(t.master + e));
+            M[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(m32 + e));
+            V[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(v32 + e));
+            gr[k].load(t.grad, e);
+        }
+        if (skip) return;
+#pragma unroll
+        for (int k = 0; k < kStepRuns; ++k) {
+            const int64_t e = e0 + 256 * k + 4 * lane;
+            float w[4], m[4], v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                w[q] = W[k][q];
+                m[q] = M[k][q];
+                v[q] = V[k][q];
+                adamw32_1(w[q], m[q], v[q], gr[k].get(q) * scale, t.lr, t.lrwd, c);
+            }
+            __builtin_nontemporal_store(f4{w[0], w[1], w[2], w[3]}, reinterpret_cast<f4*>(t.master + e));
+            __builtin_nontemporal_store(f4{m[0], m[1], m[2], m[3]}, reinterpret_cast<f4*>(m32 + e));
+            __builtin_nontemporal_store(f4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f4*>(v32 + e));
+            if (t.param != nullptr)
+                __builtin_nontemporal_store(u2h{narrow2<D>(w[0], w[1]), narrow2<D>(w[2], w[3])},
+                                            reinterpret_cast<u2h*>(t.param + e));
+        }
+        return;
+    }
+    if (skip) return;
+    for (int k = 0; k < 4 * kStepRuns; ++k) {
+        const int64_t e = e0 + 64 * k + lane;
+        if (e >= t.numel) break;
+        float w = t.master[e], m = m32[e], v = v32[e];
+        adamw32_1(w, m, v, grad1<G>(t.grad, e) * scale, t.lr, t.lrwd, c);
+        t.master[e] = w;
+        m32[e] = m;
+        v32[e] = v;
+        if (t.param != nullptr) t.param[e] = static_cast<uint16_t>(narrow<D>(w));
+    }
+}
+
+// ---------------------------------------------------------- AdamW, 8 bits
+// First moment: e4m3 codes, second: unsigned codes of 4 exponent and 4
+// mantissa bits (bias 7; it is never negative, and the sign's bit buys half
+// the spacing, which the running mean of a beta2 near 1 needs).  Both round
+// stochastically, since a mean that moves by a thousandth of itself a step
+// would stand still when rounded to the nearest of 8 or 16 values a binade.
+// The update itself uses the new moments before they are rounded.
+
+constexpr uint32_t kCarryM = 0x1fffffu;    // mantissas past 1.75 (448 = 1.75 * 2^8)
+constexpr uint32_t kCarryV = 0x07ffffu;    // mantissas past 1.9375 (496 = 1.9375 * 2^8)
+
+// A code c's value is the float with the bits c << 19 (exponents from -127 on,
+// subnormal where the code is) times 2^120, times the scale.
+__device__ __forceinline__ float decode_v(uint32_t c, uint32_t s) {
+    return __builtin_ldexpf(__uint_as_float(c << 19), static_cast<int>(s) - 7);
+}
+__device__ __forceinline__ uint32_t encode_v(float v, uint32_t s, uint32_t word) {
+    const uint32_t t = __float_as_uint(__builtin_ldexpf(v, 7 - static_cast<int>(s)));
+    const uint32_t c = (t + ((word & 0xffffu) << 3)) >> 19;
+    return umax(c, umin(__float_as_uint(v), 1u));     // what is not zero never becomes zero
+}
+
+template <int D, int G>
+__device__ __forceinline__ void adamw8_tile(const StepTensor& t, int64_t e0, int lane, float scale, bool skip,
+                                            const StepConsts& c) {
+    uint8_t* m8 = static_cast<uint8_t*>(t.exp_avg);
+    uint8_t* v8 = static_cast<uint8_t*>(t.exp_avg_sq);
+    const int64_t scales = (t.numel + kMxBlock - 1) / kMxBlock * kMxBlock;
+    f4 W[kStepRuns];
+    Grad4<G> gr[kStepRuns];
+    uint32_t MC[kStepRuns], VC[kStepRuns], MS[kStepRuns], VS[kStepRuns];
+    const bool whole = e0 + 256 * kStepRuns <= t.numel;
+    if (whole) {
+#pragma unroll
+        for (int k = 0; k < kStepRuns; ++k) {
+            const int64_t e = e0 + 256 * k + 4 * lane;
+            W[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(t.master + e));
+            gr[k].load(t.grad, e);
+            MC[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(m8 + e));
+            VC[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(v8 + e));
+            MS[k] = m8[scales + (e >> 5)];
+            VS[k] = v8[scales + (e >> 5)];
+        }
+        if (skip) return;
+    }
+    if (skip) return;
+#pragma unroll
+    for (int k = 0; k < kStepRuns; ++k) {
+        const int64_t e = e0 + 256 * k + 4 * lane;
+        const int left = whole ? 4 : (t.numel - e >= 4 ? 4 : (t.numel > e ? static_cast<int>(t.numel - e) : 0));
+        float w[4] = {}, g[4] = {};
+        uint32_t mc = 0, vc = 0, ms = 0, vs = 0;
+        if (whole) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                w[q] = W[k][q];
+                g[q] = gr[k].get(q) * scale;
+            }
+            mc = MC[k];
+            vc = VC[k];
+            ms = MS[k];
+            vs = VS[k];
+        } else if (left > 0) {
+            // codes are padded to whole blocks: the four are there
+            mc = *reinterpret_cast<const uint32_t*>(m8 + e);
+            vc = *reinterpret_cast<const uint32_t*>(v8 + e);
+            ms = m8[scales + (e >> 5)];
+            vs = v8[scales + (e >> 5)];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q < left) {
+                    w[q] = t.master[e + q];
+                    g[q] = grad1<G>(t.grad, e + q) * scale;
+                }
+            }
+        }
+        const f2 m01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mc, scale_of(ms), false);
+        const f2 m23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mc, scale_of(ms), true);
+        float m[4] = {m01.x, m01.y, m23.x, m23.y}, v[4];
+        uint32_t mtop = 0, vtop = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] = decode_v((vc >> (8 * q)) & 0xffu, vs);
+            w[q] = w[q] - t.lrwd * w[q];
+            m[q] = c.b1 * m[q] + c.omb1 * g[q];
+            v[q] = c.b2 * v[q] + c.omb2 * (g[q] * g[q]);
+            // two of the formula's divisions are by constants of the step and
+            // taken as products with their reciprocals; root and quotient
+            // within one ulp (the rounding of w covers it: lr times it is
+            // added to a weight that is far larger)
+            const float den = __builtin_amdgcn_sqrtf(v[q]) * c.rsqrt_bc2 + c.eps;
+            w[q] = w[q] - (t.lr * m[q]) * __builtin_amdgcn_rcpf(den);
+            if (q >= left) m[q] = v[q] = 0.0f;         // padding of the last block
+            mtop = umax(mtop, mag(m[q]));
+            vtop = umax(vtop, mag(v[q]));
+        }
+        mtop = max8lanes(mtop);
+        vtop = max8lanes(vtop);
+        const uint32_t msn = scale_byte(mtop, kCarryM, 8, 254), vsn = scale_byte(vtop, kCarryV, 8, 254);
+        const uint32_t x0 = weyl(e, t.key0);
+        uint32_t word[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) word[q] = random_word(x0 + static_cast<uint32_t>(q) * kWeyl, t.key1);
+        const float sc = scale_of(msn);
+        uint32_t mo = 0;
+        mo = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(mo, m[0], word[0], sc, 0);
+        mo = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(mo, m[1], word[1], sc, 1);
+        mo = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(mo, m[2], word[2], sc, 2);
+        mo = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(mo, m[3], word[3], sc, 3);
+        uint32_t vo = encode_v(v[0], vsn, word[0]) | encode_v(v[1], vsn, word[1]) << 8 |
+                      encode_v(v[2], vsn, word[2]) << 16 | encode_v(v[3], vsn, word[3]) << 24;
+        if (msn == 255u) mo = 0x7f7f7f7fu;
+        if (vsn == 255u) vo = 0xffffffffu;
+        if (left == 4) {
+            __builtin_nontemporal_store(f4{w[0], w[1], w[2], w[3]}, reinterpret_cast<f4*>(t.master + e));
+            if (t.param != nullptr)
+                __builtin_nontemporal_store(u2h{narrow2<D>(w[0], w[1]), narrow2<D>(w[2], w[3])},
+                                            reinterpret_cast<u2h*>(t.param + e));
+            __builtin_nontemporal_store(mo, reinterpret_cast<uint32_t*>(m8 + e));
+            __builtin_nontemporal_store(vo, reinterpret_cast<uint32_t*>(v8 + e));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                if (q < left) {
+                    t.master[e + q] = w[q];
+                    if (t.param != nullptr) t.param[e + q] = static_cast<uint16_t>(narrow<D>(w[q]));
+                    m8[e + q] = static_cast<uint8_t>(mo >> (8 * q));
+                    v8[e + q] = static_cast<uint8_t>(vo >> (8 * q));
+                }
+            }
+        }
+        if (left > 0 && (lane & 7) == 0) {
+            m8[scales + (e >> 5)] = static_cast<uint8_t>(msn);
+            v8[scales + (e >> 5)] = static_cast<uint8_t>(vsn);
+        }
+    }
+}
+
+template <int D, int G, int BITS>
+__global__ __launch_bounds__(kLbBlock) void k_adamw(const StepPlan plan, const StepConsts c,
+                                                    const float* __restrict__ scale_p,
+                                                    const int32_t* __restrict__ nonfinite_p) {
+    const int32_t flag = nonfinite_p != nullptr ? *nonfinite_p : 0;
+    const float scale = scale_p != nullptr ? *scale_p : 1.0f;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int s = find_tensor(plan, b, lane);
+    const StepTensor t = plan.t[s];
+    const int64_t e0 = int64_t(b - plan.first_tile[s]) * kStepTile + int64_t(wave) * 256 * kStepRuns;
+    if (e0 >= t.numel) return;
+    if constexpr (BITS == 32) adamw32_tile<D, G>(t, e0, lane, scale, flag != 0, c);
+    else adamw8_tile<D, G>(t, e0, lane, scale, flag != 0, c);
+}
+
+// ------------------------------------------------------ 8-bit moments read
+// 1 + 1/32 bytes in, 2 or 4 out an element; both codes are exact in bf16.
+
+template <bool F32>
+__global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int s = find_tensor(plan, b, lane);
+    const ReadTensor t = plan.t[s];
+    const int64_t e0 = int64_t(b - plan.first_tile[s]) * kReadTile + int64_t(wave) * 256 * kReadRuns;
+    const int64_t scales = (t.numel + kMxBlock - 1) / kMxBlock * kMxBlock;
+    uint32_t C[kReadRuns], S[kReadRuns];
+#pragma unroll
+    for (int k = 0; k < kReadRuns; ++k) {
+        const int64_t e = e0 + 256 * k + 4 * lane;
+        C[k] = S[k] = 0;
+        if (e < t.numel) {
+            C[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(t.moment + e));
+            S[k] = t.moment[scales + (e >> 5)];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kReadRuns; ++k) {
+        const int64_t e = e0 + 256 * k + 4 * lane;
+        float x[4];
+        if (t.second != 0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = decode_v((C[k] >> (8 * q)) & 0xffu, S[k]);
+        } else {
+            const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(C[k], scale_of(S[k]), false);
+            const f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(C[k], scale_of(S[k]), true);
+            x[0] = a.x;
+            x[1] = a.y;
+            x[2] = d.x;
+            x[3] = d.y;
+        }
+        if (e + 4 <= t.numel) {
+            if constexpr (F32)
+                __builtin_nontemporal_store(f4{x[0], x[1], x[2], x[3]},
+                                            reinterpret_cast<f4*>(static_cast<float*>(t.out) + e));
+            else
+                __builtin_nontemporal_store(u2h{narrow2<kBF16>(x[0], x[1]), narrow2<kBF16>(x[2], x[3])},
+                                            reinterpret_cast<u2h*>(static_cast<uint16_t*>(t.out) + e));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                if (e + q < t.numel) {
+                    if constexpr (F32) static_cast<float*>(t.out)[e + q] = x[q];
+                    else static_cast<uint16_t*>(t.out)[e + q] = static_cast<uint16_t>(narrow<kBF16>(x[q]));
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------- the 4-bit wire
+
+// The largest scale whose largest code, 6, is still finite in 16 bits; a
+// block with magnitudes past 7 of it (fp16: from 57344 on) is held there.
+template <int D>
+constexpr int kMxHighest = D == kFP16 ? 140 : 252;
+
+// 8 elements of 16 bits from `p`, the first `left` of them there (zeros after).
+__device__ __forceinline__ u4 load8(const uint16_t* p, int64_t left) {
+    if (left >= 8) return __builtin_nontemporal_load(reinterpret_cast<const u4h*>(p));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 7; ++q)
+        if (q < left) w[q >> 1] |= static_cast<uint32_t>(p[q]) << (16 * (q & 1));
+    return u4{w[0], w[1], w[2], w[3]};
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int64_t left, u4 x) {
+    if (left >= 8) {
+        __builtin_nontemporal_store(x, reinterpret_cast<u4h*>(p));
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 7; ++q)
+        if (q < left) p[q] = static_cast<uint16_t>(x[q >> 1] >> (16 * (q & 1)));
+}
+
+// The scale byte of the block of which this lane holds 8 elements (its three
+// neighbours of the quad the others).  Magnitudes of 16-bit values compare
+// as integers, two to a word.
+template <int D, bool SR>
+__device__ __forceinline__ uint32_t mx_scale(u4 x) {
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        hi = umax(hi, x[q] & 0x7fff0000u);
+        lo = umax(lo, x[q] & 0x7fffu);
+    }
+    const uint32_t top16 = max4lanes(umax(hi >> 16, lo));
+    // ties at 7 * 2^e would round to 8: to nearest, the scale doubles from
+    // there on; stochastically from past 6 on, since 6 is the last code
+    return scale_byte(mag(widen<D>(top16)), SR ? 0x3fffffu : 0x200000u, 2, kMxHighest<D>);
+}
+
+// Codes of 8 elements.  `pair`: the index of the first two in the send
+// buffer; the second of a pair rounds by the first's word rotated by one bit.
+template <int D, bool SR>
+__device__ __forceinline__ uint32_t mx_encode(u4 x, uint32_t s, int64_t pair, uint32_t key0, uint32_t key1) {
+    const float sc = scale_of(s);
+    uint32_t out = 0;
+    if constexpr (SR) {
+        const uint32_t x0 = weyl(pair, key0);
+        const f2 a = {widen<D>(x[0] & 0xffffu), widen<D>(x[0] >> 16)}, b = {widen<D>(x[1] & 0xffffu), widen<D>(x[1] >> 16)};
+        const f2 c = {widen<D>(x[2] & 0xffffu), widen<D>(x[2] >> 16)}, d = {widen<D>(x[3] & 0xffffu), widen<D>(x[3] >> 16)};
+        // byte 0 of each conversion: the compiler does not keep the other bytes
+        // of this one's destination, so the four are joined by permutes
+        const uint32_t ra = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, a, random_word(x0, key1), sc, 0);
+        const uint32_t rb = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, b, random_word(x0 + kWeyl, key1), sc, 0);
+        const uint32_t rc = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, c, random_word(x0 + 2 * kWeyl, key1), sc, 0);
+        const uint32_t rd = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, d, random_word(x0 + 3 * kWeyl, key1), sc, 0);
+        out = __builtin_amdgcn_perm(rb, ra, 0x0c0c0400u) | __builtin_amdgcn_perm(rd, rc, 0x04000c0cu);
+    } else {
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, widen<D>(x[0] & 0xffffu), widen<D>(x[0] >> 16), sc, 0);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, widen<D>(x[1] & 0xffffu), widen<D>(x[1] >> 16), sc, 1);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, widen<D>(x[2] & 0xffffu), widen<D>(x[2] >> 16), sc, 2);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, widen<D>(x[3] & 0xffffu), widen<D>(x[3] >> 16), sc, 3);
+    }
+    return s == 255u ? 0u : out;
+}
+
+template <int I>
+__device__ __forceinline__ f2 mx_pair(uint32_t codes, float sc) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, sc, I);
+}
+
+// The 16-bit values of 8 codes (exact: a scale is chosen from 16-bit values).
+template <int D>
+__device__ __forceinline__ u4 mx_decode(uint32_t codes, uint32_t s) {
+    u4 r;
+    const float sc = scale_of(s);
+    if constexpr (D == kFP16) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, sc, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, sc, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, sc, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, sc, 3));
+    } else {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, sc, 3));
+    }
+    constexpr uint32_t nan2 = D == kFP16 ? 0x7e007e00u : 0x7fc07fc0u;
+    if (s == 255u) r = u4{nan2, nan2, nan2, nan2};
+    return r;
+}
+
+__device__ __forceinline__ uint8_t* chunk_of(const MxPlan& p, int v) {
+    return p.base != nullptr ? p.base + v * p.stride : p.chunk[v - p.v0];
+}
+
+// Tile x of a parameter's partition, rank y: the own rank's part is quantised
+// from the shard into the own chunk (pack) and written, as the values that
+// the codes stand for, into the parameter's view like every other rank's
+// (unpack), so that all ranks see the same parameters.
+template <int D, int MODE>
+__global__ __launch_bounds__(kLbBlock) void k_mx4_gather(const MxPlan plan) {
+    const int t = threadIdx.x;
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int s = find_tensor(plan, b, t & 63);
+    const MxParam p = plan.p[s];
+    const int v = plan.v0 + static_cast<int>(blockIdx.y);
+    const int64_t tile0 = int64_t(b - plan.first_tile[s]) * kMxTile;
+    const int64_t lo = v * p.ps;
+    int64_t real = p.numel - lo;
+    real = real < 0 ? 0 : real > p.ps ? p.ps : real;
+    const int64_t codes_end = (p.ps + kMxBlock - 1) / kMxBlock * kMxBlock;
+    if (v == plan.rank && (MODE & kMxPack) != 0) {
+        u4 x[kMxVecs];
+#pragma unroll
+        for (int u = 0; u < kMxVecs; ++u) {
+            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
+            x[u] = u4{0, 0, 0, 0};
+            if (k < real) x[u] = load8(p.src + k, real - k);
+        }
+#pragma unroll
+        for (int u = 0; u < kMxVecs; ++u) {
+            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
+            const uint32_t sc = mx_scale<D, false>(x[u]);
+            const uint32_t codes = mx_encode<D, false>(x[u], sc, 0, 0, 0);
+            if (k < codes_end) {
+                *reinterpret_cast<uint32_t*>(plan.own + 16 * p.block0 + k / 2) = codes;
+                if ((t & 3) == 0) plan.own[16 * plan.blocks + p.block0 + k / 32] = static_cast<uint8_t>(sc);
+                if constexpr ((MODE & kMxUnpack) != 0) {
+                    if (k < real) store8(p.dst + lo + k, real - k, mx_decode<D>(codes, sc));
+                }
+            }
+        }
+    } else if constexpr ((MODE & kMxUnpack) != 0) {
+        if (tile0 >= real) return;
+        const uint8_t* chunk = chunk_of(plan, v);
+        uint32_t C[kMxVecs], S[kMxVecs];
+#pragma unroll
+        for (int u = 0; u < kMxVecs; ++u) {
+            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
+            C[u] = S[u] = 0;
+            if (k < real) {
+                C[u] = *reinterpret_cast<const uint32_t*>(chunk + 16 * p.block0 + k / 2);
+                S[u] = chunk[16 * plan.blocks + p.block0 + k / 32];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kMxVecs; ++u) {
+            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
+            if (k < real) store8(p.dst + lo + k, real - k, mx_decode<D>(C[u], S[u]));
+        }
+    }
+}
+
+// Tile x of a parameter's partition for destination y.
+template <int D, bool SR>
+__global__ __launch_bounds__(kLbBlock) void k_mx4_send(const MxPlan plan, uint32_t key0, uint32_t key1) {
+    const int t = threadIdx.x;
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int s = find_tensor(plan, b, t & 63);
+    const MxParam p = plan.p[s];
+    const int d = plan.v0 + static_cast<int>(blockIdx.y);
+    const int64_t tile0 = int64_t(b - plan.first_tile[s]) * kMxTile;
+    int64_t real = p.numel - d * p.ps;
+    real = real < 0 ? 0 : real > p.ps ? p.ps : real;
+    const int64_t codes_end = (p.ps + kMxBlock - 1) / kMxBlock * kMxBlock;
+    const uint16_t* src = p.src + d * p.ps;
+    uint8_t* chunk = chunk_of(plan, d);
+    const int64_t pair0 = (d * plan.blocks + p.block0) * (kMxBlock / 2);
+    u4 x[kMxVecs];
+#pragma unroll
+    for (int u = 0; u < kMxVecs; ++u) {
+        const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
+        x[u] = u4{0, 0, 0, 0};
+        if (k < real) x[u] = load8(src + k, real - k);
+    }
+#pragma unroll
+    for (int u = 0; u < kMxVecs; ++u) {
+        const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
+        const uint32_t sc = mx_scale<D, SR>(x[u]);
+        const uint32_t codes = mx_encode<D, SR>(x[u], sc, pair0 + k / 2, key0, key1);
+        if (k < codes_end) {
+            *reinterpret_cast<uint32_t*>(chunk + 16 * p.block0 + k / 2) = codes;
+            if ((t & 3) == 0) chunk[16 * plan.blocks + p.block0 + k / 32] = static_cast<uint8_t>(sc);
+        }
+    }
+}
+
+// The owner's average of N received chunks: fp32 sums in rank order from +0,
+// one fp32 division, rounded to 16 bits; padding positions 0.  A wave covers
+// the 1024 elements of one norm slot.
+constexpr int kMxBatch = 8;     // chunks whose loads are in flight together
+
+template <int D, bool NORM>
+__global__ __launch_bounds__(kLbBlock) void k_mx4_reduce(const MxPlan plan, double* __restrict__ partials) {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int s = find_tensor(plan, b, lane);
+    const MxParam p = plan.p[s];
+    const int64_t tile = b - plan.first_tile[s];
+    const int64_t k0 = tile * kMxReduceTile + int64_t(wave) * 1024;
+    int64_t real = p.numel - plan.rank * p.ps;
+    real = real < 0 ? 0 : real > p.ps ? p.ps : real;
+    double ss = 0.0;
+    if (k0 < p.ps) {
+        float acc[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[u][e] = 0.0f;
+        for (int vb = 0; vb < plan.world; vb += kMxBatch) {
+            uint32_t C[kMxBatch][2], S[kMxBatch][2];
+#pragma unroll
+            for (int j = 0; j < kMxBatch; ++j) {
+                if (vb + j < plan.world) {
+                    const uint8_t* chunk = chunk_of(plan, vb + j);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int64_t k = k0 + 512 * u + 8 * lane;
+                        C[j][u] = S[j][u] = 0;
+                        if (k < real) {
+                            C[j][u] = *reinterpret_cast<const uint32_t*>(chunk + 16 * p.block0 + k / 2);
+                            S[j][u] = chunk[16 * plan.blocks + p.block0 + k / 32];
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kMxBatch; ++j) {
+                if (vb + j < plan.world) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float sc = S[j][u] == 255u ? __builtin_nanf("") : scale_of(S[j][u]);
+                        const f2 a = mx_pair<0>(C[j][u], sc), bb = mx_pair<1>(C[j][u], sc);
+                        const f2 cc = mx_pair<2>(C[j][u], sc), d = mx_pair<3>(C[j][u], sc);
+                        acc[u][0] += a.x;
+                        acc[u][1] += a.y;
+                        acc[u][2] += bb.x;
+                        acc[u][3] += bb.y;
+                        acc[u][4] += cc.x;
+                        acc[u][5] += cc.y;
+                        acc[u][6] += d.x;
+                        acc[u][7] += d.y;
+                        if (S[j][u] == 255u) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) acc[u][e] = __builtin_nanf("");
+                        }
+                    }
+                }
+            }
+        }
+        const float n = static_cast<float>(plan.world);
+        const bool pow2 = (plan.world & (plan.world - 1)) == 0;
+        const float inv = 1.0f / n;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t k = k0 + 512 * u + 8 * lane;
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float mean = pow2 ? acc[u][e] * inv : acc[u][e] / n;
+                h[e] = k + e < real ? narrow<D>(mean) : 0u;
+                if constexpr (NORM) {
+                    const double y = widen<D>(h[e]);
+                    ss += y * y;
+                }
+            }
+            const u4 x = {h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+            if (k < p.ps) store8(p.dst + k, p.ps - k, x);
+        }
+    }
+    if constexpr (NORM) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) ss += __shfl_xor(ss, o, 64);
+        if (lane == 0) partials[p.slot + tile * 4 + wave] = ss;
+    }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- launchers
+
+// LDS that the 32-bit step reserves and never uses: two workgroups a CU, as
+// the flat Adam step, whose streams it has.
+constexpr unsigned kStepLdsReserve = 56 * 1024;
+
+template <int D, int G>
+static void adamw_launch(int32_t bits, const StepPlan& plan, const StepConsts& c, const float* scale,
+                         const int32_t* nonfinite, hipStream_t stream) {
+    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]));
+    if (bits == 32)
+        hipLaunchKernelGGL((k_adamw<D, G, 32>), g, dim3(kLbBlock), kStepLdsReserve, stream, plan, c, scale, nonfinite);
+    else
+        hipLaunchKernelGGL((k_adamw<D, G, 8>), g, dim3(kLbBlock), 0, stream, plan, c, scale, nonfinite);
+}
+
+hipError_t launch_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state_bits, const StepPlan& plan,
+                                const StepConsts& c, const float* scale, const int32_t* nonfinite,
+                                hipStream_t stream) {
+    if (plan.n <= 0) return hipSuccess;
+    if (dtype == kFP16) {
+        if (grad_dtype == 3) adamw_launch<kFP16, 3>(state_bits, plan, c, scale, nonfinite, stream);
+        else if (grad_dtype == kFP16) adamw_launch<kFP16, kFP16>(state_bits, plan, c, scale, nonfinite, stream);
+        else adamw_launch<kFP16, kBF16>(state_bits, plan, c, scale, nonfinite, stream);
+    } else {
+        if (grad_dtype == 3) adamw_launch<kBF16, 3>(state_bits, plan, c, scale, nonfinite, stream);
+        else if (grad_dtype == kFP16) adamw_launch<kBF16, kFP16>(state_bits, plan, c, scale, nonfinite, stream);
+        else adamw_launch<kBF16, kBF16>(state_bits, plan, c, scale, nonfinite, stream);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_moment8_read(bool fp32_out, const ReadPlan& plan, hipStream_t stream) {
+    if (plan.n <= 0) return hipSuccess;
+    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]));
+    if (fp32_out) hipLaunchKernelGGL(k_moment8_read<true>, g, dim3(kLbBlock), 0, stream, plan);
+    else hipLaunchKernelGGL(k_moment8_read<false>, g, dim3(kLbBlock), 0, stream, plan);
+    return hipGetLastError();
+}
+
+template <int D>
+static void mx4_gather_launch(int32_t mode, dim3 g, const MxPlan& plan, hipStream_t stream) {
+    if (mode == kMxPack) hipLaunchKernelGGL((k_mx4_gather<D, kMxPack>), g, dim3(kLbBlock), 0, stream, plan);
+    else if (mode == kMxUnpack) hipLaunchKernelGGL((k_mx4_gather<D, kMxUnpack>), g, dim3(kLbBlock), 0, stream, plan);
+    else hipLaunchKernelGGL((k_mx4_gather<D, kMxPack | kMxUnpack>), g, dim3(kLbBlock), 0, stream, plan);
+}
+
+hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, const MxPlan& plan, int32_t n_ranks, hipStream_t stream) {
+    if (plan.n <= 0 || n_ranks <= 0) return hipSuccess;
+    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]), static_cast<uint32_t>(n_ranks));
+    if (dtype == kFP16) mx4_gather_launch<kFP16>(mode, g, plan, stream);
+    else mx4_gather_launch<kBF16>(mode, g, plan, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_send(int32_t dtype, bool stochastic, uint32_t key0, uint32_t key1, const MxPlan& plan,
+                           int32_t n_ranks, hipStream_t stream) {
+    if (plan.n <= 0 || n_ranks <= 0) return hipSuccess;
+    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]), static_cast<uint32_t>(n_ranks)), b(kLbBlock);
+    if (dtype == kFP16) {
+        if (stochastic) hipLaunchKernelGGL((k_mx4_send<kFP16, true>), g, b, 0, stream, plan, key0, key1);
+        else hipLaunchKernelGGL((k_mx4_send<kFP16, false>), g, b, 0, stream, plan, key0, key1);
+    } else {
+        if (stochastic) hipLaunchKernelGGL((k_mx4_send<kBF16, true>), g, b, 0, stream, plan, key0, key1);
+        else hipLaunchKernelGGL((k_mx4_send<kBF16, false>), g, b, 0, stream, plan, key0, key1);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_reduce(int32_t dtype, const MxPlan& plan, double* partials, hipStream_t stream) {
+    if (plan.n <= 0) return hipSuccess;
+    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n])), b(kLbBlock);
+    if (dtype == kFP16) {
+        if (partials != nullptr) hipLaunchKernelGGL((k_mx4_reduce<kFP16, true>), g, b, 0, stream, plan, partials);
+        else hipLaunchKernelGGL((k_mx4_reduce<kFP16, false>), g, b, 0, stream, plan, partials);
+    } else {
+        if (partials != nullptr) hipLaunchKernelGGL((k_mx4_reduce<kBF16, true>), g, b, 0, stream, plan, partials);
+        else hipLaunchKernelGGL((k_mx4_reduce<kBF16, false>), g, b, 0, stream, plan, partials);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace zs3

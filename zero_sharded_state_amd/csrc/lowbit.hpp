@@ -1,0 +1,116 @@
+// Internal declarations of the low-bit operators: AdamW over a list of
+// tensors with 32- or 8-bit states, and the 4-bit wire of the coalesced
+// gather and reduce-scatter.  Every call's description travels in the kernel
+// arguments (under 4 KB, the work of longer requests split over launches),
+// so nothing is allocated, uploaded or cached: a call may be captured into a
+// graph the first time it is made, and calls share no state.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+
+namespace zs3 {
+
+constexpr int kLbBlock = 256;              // threads of a workgroup (4 waves of 64)
+constexpr int64_t kMxBlock = 32;           // elements that share a scale byte
+
+// ------------------------------------------------ AdamW over a tensor list
+
+constexpr int kStepTensors = 48;           // tensors of one launch
+constexpr int kStepRuns = 2;               // runs of 256 elements of a wave
+constexpr int64_t kStepTile = int64_t(kLbBlock) * 4 * kStepRuns;   // elements of a workgroup
+
+struct StepTensor {
+    int64_t numel;
+    float* master;
+    const void* grad;
+    uint16_t* param;        // may be null
+    void* exp_avg;
+    void* exp_avg_sq;
+    float lr;               // 8-bit states: lr / (1 - beta1^t)
+    float lrwd;
+    uint32_t key0, key1;    // of the tensor's random words
+};
+
+struct StepPlan {
+    int32_t n;
+    int32_t first_tile[kStepTensors + 1];
+    StepTensor t[kStepTensors];
+};
+static_assert(sizeof(StepPlan) <= 3584, "the plan has to fit the kernel arguments");
+
+struct StepConsts {
+    float b1, b2, omb1, omb2, bc1, bc2, eps;
+    float rsqrt_bc2;        // 8-bit states: 1 / sqrt(1 - beta2^t)
+};
+
+hipError_t launch_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state_bits, const StepPlan& plan,
+                                const StepConsts& c, const float* scale, const int32_t* nonfinite,
+                                hipStream_t stream);
+
+// ------------------------------------------------------ 8-bit moments read
+
+constexpr int kReadTensors = 64;
+constexpr int kReadRuns = 4;
+constexpr int64_t kReadTile = int64_t(kLbBlock) * 4 * kReadRuns;
+
+struct ReadTensor {
+    int64_t numel;
+    const uint8_t* moment;
+    void* out;
+    int64_t second;         // 0: first moment (e4m3), 1: second (unsigned, 4 + 4 bits)
+};
+
+struct ReadPlan {
+    int32_t n;
+    int32_t first_tile[kReadTensors + 1];
+    ReadTensor t[kReadTensors];
+};
+
+hipError_t launch_moment8_read(bool fp32_out, const ReadPlan& plan, hipStream_t stream);
+
+// ---------------------------------------------------------- the 4-bit wire
+
+constexpr int kMxParams = 24;              // parameters of one launch
+constexpr int kMxRanks = 256;              // chunk pointers of one launch
+constexpr int kMxVecs = 4;                 // groups of 8 elements of a thread (gather, send)
+constexpr int64_t kMxTile = int64_t(kLbBlock) * 8 * kMxVecs;
+constexpr int64_t kMxReduceTile = int64_t(kLbBlock) * 8 * 2;       // a wave covers one norm slot's 1024 elements
+
+// One parameter of a bucket.
+struct MxParam {
+    int64_t numel;
+    int64_t ps;
+    int64_t block0;         // first block of its partition in every chunk
+    const uint16_t* src;    // gather: its own shard part; send: its whole gradient
+    uint16_t* dst;          // gather: its full view; reduce: its part of the flat gradient
+    int64_t slot;           // reduce: its first norm slot
+};
+
+// Chunk v is at chunk[v], or at base + v * stride where base is set.
+struct MxPlan {
+    int32_t n;
+    int32_t first_tile[kMxParams + 1];
+    int32_t rank;           // whose shard `src` is (gather), whose partition is reduced (reduce)
+    int32_t world;
+    int32_t v0;             // first rank that chunk[] holds
+    int64_t blocks;         // blocks of a chunk
+    uint8_t* base;
+    int64_t stride;
+    uint8_t* own;           // gather: the own chunk to write
+    MxParam p[kMxParams];
+    uint8_t* chunk[kMxRanks];
+};
+static_assert(sizeof(MxPlan) <= 3584, "the plan has to fit the kernel arguments");
+
+enum MxMode : int32_t { kMxPack = 1, kMxUnpack = 2 };
+
+// ranks [v0, v0 + n_ranks): pack (the own rank's chunk) and/or unpack.
+hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, const MxPlan& plan, int32_t n_ranks, hipStream_t stream);
+// destinations [v0, v0 + n_ranks): quantise every destination's partitions.
+hipError_t launch_mx4_send(int32_t dtype, bool stochastic, uint32_t key0, uint32_t key1, const MxPlan& plan,
+                           int32_t n_ranks, hipStream_t stream);
+hipError_t launch_mx4_reduce(int32_t dtype, const MxPlan& plan, double* partials, hipStream_t stream);
+
+}  // namespace zs3

@@ -23,6 +23,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lowbit.hpp"
 #include "zs3_internal.hpp"
 
@@ -708,14 +710,20 @@ __global__ __launch_bounds__(kLbBlock) void k_mx4_reduce(const MxPlan plan, doub
 // the flat Adam step, whose streams it has.
 constexpr unsigned kStepLdsReserve = 56 * 1024;
 
+// Launches without the copies of a plan that a call by value makes.
+template <typename... A>
+static hipError_t launch(void (*kernel)(A...), dim3 grid, unsigned shm, hipStream_t stream,
+                         const std::remove_const_t<A>&... args) {
+    void* list[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kLbBlock), list, shm, stream);
+}
+
 template <int D, int G>
-static void adamw_launch(int32_t bits, const StepPlan& plan, const StepConsts& c, const float* scale,
-                         const int32_t* nonfinite, hipStream_t stream) {
+static hipError_t adamw_launch(int32_t bits, const StepPlan& plan, const StepConsts& c, const float* scale,
+                               const int32_t* nonfinite, hipStream_t stream) {
     const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]));
-    if (bits == 32)
-        hipLaunchKernelGGL((k_adamw<D, G, 32>), g, dim3(kLbBlock), kStepLdsReserve, stream, plan, c, scale, nonfinite);
-    else
-        hipLaunchKernelGGL((k_adamw<D, G, 8>), g, dim3(kLbBlock), 0, stream, plan, c, scale, nonfinite);
+    if (bits == 32) return launch(k_adamw<D, G, 32>, g, kStepLdsReserve, stream, plan, c, scale, nonfinite);
+    return launch(k_adamw<D, G, 8>, g, 0, stream, plan, c, scale, nonfinite);
 }
 
 hipError_t launch_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state_bits, const StepPlan& plan,
@@ -723,65 +731,48 @@ hipError_t launch_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state
                                 hipStream_t stream) {
     if (plan.n <= 0) return hipSuccess;
     if (dtype == kFP16) {
-        if (grad_dtype == 3) adamw_launch<kFP16, 3>(state_bits, plan, c, scale, nonfinite, stream);
-        else if (grad_dtype == kFP16) adamw_launch<kFP16, kFP16>(state_bits, plan, c, scale, nonfinite, stream);
-        else adamw_launch<kFP16, kBF16>(state_bits, plan, c, scale, nonfinite, stream);
-    } else {
-        if (grad_dtype == 3) adamw_launch<kBF16, 3>(state_bits, plan, c, scale, nonfinite, stream);
-        else if (grad_dtype == kFP16) adamw_launch<kBF16, kFP16>(state_bits, plan, c, scale, nonfinite, stream);
-        else adamw_launch<kBF16, kBF16>(state_bits, plan, c, scale, nonfinite, stream);
+        if (grad_dtype == 3) return adamw_launch<kFP16, 3>(state_bits, plan, c, scale, nonfinite, stream);
+        if (grad_dtype == kFP16) return adamw_launch<kFP16, kFP16>(state_bits, plan, c, scale, nonfinite, stream);
+        return adamw_launch<kFP16, kBF16>(state_bits, plan, c, scale, nonfinite, stream);
     }
-    return hipGetLastError();
+    if (grad_dtype == 3) return adamw_launch<kBF16, 3>(state_bits, plan, c, scale, nonfinite, stream);
+    if (grad_dtype == kFP16) return adamw_launch<kBF16, kFP16>(state_bits, plan, c, scale, nonfinite, stream);
+    return adamw_launch<kBF16, kBF16>(state_bits, plan, c, scale, nonfinite, stream);
 }
 
 hipError_t launch_moment8_read(bool fp32_out, const ReadPlan& plan, hipStream_t stream) {
     if (plan.n <= 0) return hipSuccess;
     const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]));
-    if (fp32_out) hipLaunchKernelGGL(k_moment8_read<true>, g, dim3(kLbBlock), 0, stream, plan);
-    else hipLaunchKernelGGL(k_moment8_read<false>, g, dim3(kLbBlock), 0, stream, plan);
-    return hipGetLastError();
+    return launch(fp32_out ? k_moment8_read<true> : k_moment8_read<false>, g, 0, stream, plan);
 }
 
 template <int D>
-static void mx4_gather_launch(int32_t mode, dim3 g, const MxPlan& plan, hipStream_t stream) {
-    if (mode == kMxPack) hipLaunchKernelGGL((k_mx4_gather<D, kMxPack>), g, dim3(kLbBlock), 0, stream, plan);
-    else if (mode == kMxUnpack) hipLaunchKernelGGL((k_mx4_gather<D, kMxUnpack>), g, dim3(kLbBlock), 0, stream, plan);
-    else hipLaunchKernelGGL((k_mx4_gather<D, kMxPack | kMxUnpack>), g, dim3(kLbBlock), 0, stream, plan);
+static hipError_t mx4_gather_launch(int32_t mode, dim3 g, const MxPlan& plan, hipStream_t stream) {
+    if (mode == kMxPack) return launch(k_mx4_gather<D, kMxPack>, g, 0, stream, plan);
+    if (mode == kMxUnpack) return launch(k_mx4_gather<D, kMxUnpack>, g, 0, stream, plan);
+    return launch(k_mx4_gather<D, kMxPack | kMxUnpack>, g, 0, stream, plan);
 }
 
 hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, const MxPlan& plan, int32_t n_ranks, hipStream_t stream) {
     if (plan.n <= 0 || n_ranks <= 0) return hipSuccess;
     const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]), static_cast<uint32_t>(n_ranks));
-    if (dtype == kFP16) mx4_gather_launch<kFP16>(mode, g, plan, stream);
-    else mx4_gather_launch<kBF16>(mode, g, plan, stream);
-    return hipGetLastError();
+    return dtype == kFP16 ? mx4_gather_launch<kFP16>(mode, g, plan, stream) : mx4_gather_launch<kBF16>(mode, g, plan, stream);
 }
 
 hipError_t launch_mx4_send(int32_t dtype, bool stochastic, uint32_t key0, uint32_t key1, const MxPlan& plan,
                            int32_t n_ranks, hipStream_t stream) {
     if (plan.n <= 0 || n_ranks <= 0) return hipSuccess;
-    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]), static_cast<uint32_t>(n_ranks)), b(kLbBlock);
-    if (dtype == kFP16) {
-        if (stochastic) hipLaunchKernelGGL((k_mx4_send<kFP16, true>), g, b, 0, stream, plan, key0, key1);
-        else hipLaunchKernelGGL((k_mx4_send<kFP16, false>), g, b, 0, stream, plan, key0, key1);
-    } else {
-        if (stochastic) hipLaunchKernelGGL((k_mx4_send<kBF16, true>), g, b, 0, stream, plan, key0, key1);
-        else hipLaunchKernelGGL((k_mx4_send<kBF16, false>), g, b, 0, stream, plan, key0, key1);
-    }
-    return hipGetLastError();
+    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]), static_cast<uint32_t>(n_ranks));
+    if (dtype == kFP16) return launch(stochastic ? k_mx4_send<kFP16, true> : k_mx4_send<kFP16, false>, g, 0, stream, plan, key0, key1);
+    return launch(stochastic ? k_mx4_send<kBF16, true> : k_mx4_send<kBF16, false>, g, 0, stream, plan, key0, key1);
 }
 
 hipError_t launch_mx4_reduce(int32_t dtype, const MxPlan& plan, double* partials, hipStream_t stream) {
     if (plan.n <= 0) return hipSuccess;
-    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n])), b(kLbBlock);
-    if (dtype == kFP16) {
-        if (partials != nullptr) hipLaunchKernelGGL((k_mx4_reduce<kFP16, true>), g, b, 0, stream, plan, partials);
-        else hipLaunchKernelGGL((k_mx4_reduce<kFP16, false>), g, b, 0, stream, plan, partials);
-    } else {
-        if (partials != nullptr) hipLaunchKernelGGL((k_mx4_reduce<kBF16, true>), g, b, 0, stream, plan, partials);
-        else hipLaunchKernelGGL((k_mx4_reduce<kBF16, false>), g, b, 0, stream, plan, partials);
-    }
-    return hipGetLastError();
+    const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]));
+    const bool norm = partials != nullptr;
+    if (dtype == kFP16) return launch(norm ? k_mx4_reduce<kFP16, true> : k_mx4_reduce<kFP16, false>, g, 0, stream, plan, partials);
+    return launch(norm ? k_mx4_reduce<kBF16, true> : k_mx4_reduce<kBF16, false>, g, 0, stream, plan, partials);
 }
 
 }  // namespace zs3

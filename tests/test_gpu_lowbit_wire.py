@@ -186,6 +186,36 @@ def test_reduce(case, dtype, shift):
                     assert torch.isnan(partials).all()
 
 
+@pytest.mark.parametrize("world", [1, 2, 3, 7, 15, 37])
+def test_reduce_of_a_large_partition(world):
+    """Own parts of 2.1M elements and more take a thread two groups of elements at
+    a time, smaller ones one: both, with ranks that fill no batch of chunks."""
+    require_gpu()
+    import torch
+    note(f"mx4 large reduce N={world}")
+    own = 512 * 4096 + 4097
+    with Set(world, [own * world - 1, 333], "bf16", seed=world) as st:
+        ids = st.wire_ids
+        _, _, blocks, size = lb.bucket_places(st.L, ids)
+        # random codes and scales are as good as any
+        data = [st.rng.integers(0, 256, size).astype(np.uint8) for _ in range(min(world, 4))]
+        for d in data:
+            d[16 * blocks:17 * blocks] = st.rng.integers(100, 125, blocks)
+        data = [data[v % len(data)] for v in range(world)]
+        recv = Bytes(world, size, data=data)
+        ref = np.zeros(st.L.shard_numel, np.uint16)
+        lb.reduce4(st.L, world - 1, ids, data, "bf16", ref)
+        flat = Buf16(st.L.shard_numel)
+        slots, _ = zs.zs3_layout_norm_slots(st.h)
+        partials = torch.full((slots,), float("nan"), dtype=torch.float64, device="cuda")
+        zs.zs3_reduce_scatter_coalesced_mx4(st.h, world - 1, "bf16", REDUCE, ids, recv_chunks=recv.ptrs(), grad_flat=flat.ptr(),
+                                            partials=partials)
+        sync()
+        assert np.array_equal(flat.host(), ref)
+        want = float((oracle.to_f32(ref, "bf16").astype(np.float64) ** 2).sum())
+        assert abs(float(partials.sum()) - want) <= 1e-12 * want
+
+
 def test_norm_slots_of_some_parameters_only():
     """A bucket's slots are its parameters' own: those of persistent and of other
     parameters stay as they were, and the norm from both wires' slots is the norm

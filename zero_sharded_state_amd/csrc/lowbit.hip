@@ -113,6 +113,10 @@ __device__ __forceinline__ uint32_t random_word(uint32_t x, uint32_t key1) {
     return x ^ (x >> 16);
 }
 
+// A thread's wave, as the scalar that it is: what is computed from it stays in
+// scalar registers, and loads take a scalar address and a 32-bit offset.
+__device__ __forceinline__ int wave_of(int t) { return __builtin_amdgcn_readfirstlane(t >> 6); }
+
 // The list's tensor that tile b belongs to: each lane compares one prefix
 // and the wave counts them, one load where a search would make six.
 template <class PLAN>
@@ -355,7 +359,7 @@ __global__ __launch_bounds__(kLbBlock) void k_adamw(const StepPlan plan, const S
                                                     const int32_t* __restrict__ nonfinite_p) {
     const int32_t flag = nonfinite_p != nullptr ? *nonfinite_p : 0;
     const float scale = scale_p != nullptr ? *scale_p : 1.0f;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_of(threadIdx.x);
     const int32_t b = static_cast<int32_t>(blockIdx.x);
     const int s = find_tensor(plan, b, lane);
     const StepTensor t = plan.t[s];
@@ -370,7 +374,7 @@ __global__ __launch_bounds__(kLbBlock) void k_adamw(const StepPlan plan, const S
 
 template <bool F32>
 __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_of(threadIdx.x);
     const int32_t b = static_cast<int32_t>(blockIdx.x);
     const int s = find_tensor(plan, b, lane);
     const ReadTensor t = plan.t[s];
@@ -520,6 +524,85 @@ __device__ __forceinline__ uint8_t* chunk_of(const MxPlan& p, int v) {
     return p.base != nullptr ? p.base + v * p.stride : p.chunk[v - p.v0];
 }
 
+// What a workgroup of the gather and the send works on: elements [tile0,
+// tile0 + VECS * 2048) of the partition that rank v has of a parameter, `real`
+// of them inside the parameter and `codes` inside whole blocks.  A thread's
+// offsets in it fit 32 bits, so that addresses are a scalar and an offset.
+struct MxWork {
+    MxParam p;
+    int v;
+    int64_t tile0;
+    int real, codes;
+};
+
+template <int VECS>
+__device__ __forceinline__ MxWork mx_work(const MxPlan& plan, int lane) {
+    constexpr int kTile = static_cast<int>(mx_tile(VECS));
+    MxWork w;
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int s = find_tensor(plan, b, lane);
+    w.p = plan.p[s];
+    w.v = plan.v0 + static_cast<int>(blockIdx.y);
+    w.tile0 = int64_t(b - plan.first_tile[s]) * kTile;
+    int64_t real = w.p.numel - w.v * w.p.ps;
+    real = (real > w.p.ps ? w.p.ps : real) - w.tile0;
+    const int64_t codes = (w.p.ps + kMxBlock - 1) / kMxBlock * kMxBlock - w.tile0;
+    w.real = static_cast<int>(real < 0 ? 0 : real > kTile ? kTile : real);
+    w.codes = static_cast<int>(codes > kTile ? kTile : codes);
+    return w;
+}
+
+// Quantises a tile: src[0 .. real) to `codes` and `scales` (of the tile's
+// first block) and, with OUT, to the values the codes stand for.
+template <int D, bool SR, bool OUT, bool WHOLE, int VECS>
+__device__ __forceinline__ void mx_quantise(const MxWork& w, const uint16_t* src, uint8_t* codes, uint8_t* scales,
+                                            uint16_t* out, int64_t pair0, uint32_t key0, uint32_t key1, int t) {
+    u4 x[VECS];
+#pragma unroll
+    for (int u = 0; u < VECS; ++u) {
+        const int k = (u * kLbBlock + t) * 8;
+        if constexpr (WHOLE) {
+            x[u] = __builtin_nontemporal_load(reinterpret_cast<const u4h*>(src + k));
+        } else {
+            x[u] = u4{0, 0, 0, 0};
+            if (k < w.real) x[u] = load8(src + k, w.real - k);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < VECS; ++u) {
+        const int k = (u * kLbBlock + t) * 8;
+        const uint32_t sc = mx_scale<D, SR>(x[u]);
+        const uint32_t c = mx_encode<D, SR>(x[u], sc, pair0 + k / 2, key0, key1);
+        if (WHOLE || k < w.codes) {
+            *reinterpret_cast<uint32_t*>(codes + k / 2) = c;
+            if ((t & 3) == 0) scales[k / 32] = static_cast<uint8_t>(sc);
+            if constexpr (OUT) {
+                if (WHOLE || k < w.real) store8(out + k, WHOLE ? 8 : w.real - k, mx_decode<D>(c, sc));
+            }
+        }
+    }
+}
+
+template <int D, bool WHOLE, int VECS>
+__device__ __forceinline__ void mx_widen(const MxWork& w, const uint8_t* codes, const uint8_t* scales, uint16_t* out,
+                                         int t) {
+    uint32_t C[VECS], S[VECS];
+#pragma unroll
+    for (int u = 0; u < VECS; ++u) {
+        const int k = (u * kLbBlock + t) * 8;
+        C[u] = S[u] = 0;
+        if (WHOLE || k < w.real) {
+            C[u] = *reinterpret_cast<const uint32_t*>(codes + k / 2);
+            S[u] = scales[k / 32];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < VECS; ++u) {
+        const int k = (u * kLbBlock + t) * 8;
+        if (WHOLE || k < w.real) store8(out + k, WHOLE ? 8 : w.real - k, mx_decode<D>(C[u], S[u]));
+    }
+}
+
 // Tile x of a parameter's partition, rank y: the own rank's part is quantised
 // from the shard into the own chunk (pack) and written, as the values that
 // the codes stand for, into the parameter's view like every other rank's
@@ -527,54 +610,20 @@ __device__ __forceinline__ uint8_t* chunk_of(const MxPlan& p, int v) {
 template <int D, int MODE>
 __global__ __launch_bounds__(kLbBlock) void k_mx4_gather(const MxPlan plan) {
     const int t = threadIdx.x;
-    const int32_t b = static_cast<int32_t>(blockIdx.x);
-    const int s = find_tensor(plan, b, t & 63);
-    const MxParam p = plan.p[s];
-    const int v = plan.v0 + static_cast<int>(blockIdx.y);
-    const int64_t tile0 = int64_t(b - plan.first_tile[s]) * kMxTile;
-    const int64_t lo = v * p.ps;
-    int64_t real = p.numel - lo;
-    real = real < 0 ? 0 : real > p.ps ? p.ps : real;
-    const int64_t codes_end = (p.ps + kMxBlock - 1) / kMxBlock * kMxBlock;
-    if (v == plan.rank && (MODE & kMxPack) != 0) {
-        u4 x[kMxVecs];
-#pragma unroll
-        for (int u = 0; u < kMxVecs; ++u) {
-            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
-            x[u] = u4{0, 0, 0, 0};
-            if (k < real) x[u] = load8(p.src + k, real - k);
-        }
-#pragma unroll
-        for (int u = 0; u < kMxVecs; ++u) {
-            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
-            const uint32_t sc = mx_scale<D, false>(x[u]);
-            const uint32_t codes = mx_encode<D, false>(x[u], sc, 0, 0, 0);
-            if (k < codes_end) {
-                *reinterpret_cast<uint32_t*>(plan.own + 16 * p.block0 + k / 2) = codes;
-                if ((t & 3) == 0) plan.own[16 * plan.blocks + p.block0 + k / 32] = static_cast<uint8_t>(sc);
-                if constexpr ((MODE & kMxUnpack) != 0) {
-                    if (k < real) store8(p.dst + lo + k, real - k, mx_decode<D>(codes, sc));
-                }
-            }
-        }
-    } else if constexpr ((MODE & kMxUnpack) != 0) {
-        if (tile0 >= real) return;
-        const uint8_t* chunk = chunk_of(plan, v);
-        uint32_t C[kMxVecs], S[kMxVecs];
-#pragma unroll
-        for (int u = 0; u < kMxVecs; ++u) {
-            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
-            C[u] = S[u] = 0;
-            if (k < real) {
-                C[u] = *reinterpret_cast<const uint32_t*>(chunk + 16 * p.block0 + k / 2);
-                S[u] = chunk[16 * plan.blocks + p.block0 + k / 32];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kMxVecs; ++u) {
-            const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
-            if (k < real) store8(p.dst + lo + k, real - k, mx_decode<D>(C[u], S[u]));
-        }
+    constexpr int kTile = static_cast<int>(mx_tile(kMxGatherVecs));
+    const MxWork w = mx_work<kMxGatherVecs>(plan, t & 63);
+    uint16_t* out = w.p.dst + w.v * w.p.ps + w.tile0;
+    const int64_t codes = 16 * w.p.block0 + w.tile0 / 2, scales = 16 * plan.blocks + w.p.block0 + w.tile0 / 32;
+    constexpr bool kOut = (MODE & kMxUnpack) != 0;
+    if ((MODE & kMxPack) != 0 && w.v == plan.rank) {
+        uint8_t* c = plan.own + codes;
+        uint8_t* s = plan.own + scales;
+        if (w.real == kTile) mx_quantise<D, false, kOut, true, kMxGatherVecs>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
+        else mx_quantise<D, false, kOut, false, kMxGatherVecs>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
+    } else if constexpr (kOut) {
+        const uint8_t* chunk = chunk_of(plan, w.v);
+        if (w.real == kTile) mx_widen<D, true, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, t);
+        else mx_widen<D, false, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, t);
     }
 }
 
@@ -582,109 +631,127 @@ __global__ __launch_bounds__(kLbBlock) void k_mx4_gather(const MxPlan plan) {
 template <int D, bool SR>
 __global__ __launch_bounds__(kLbBlock) void k_mx4_send(const MxPlan plan, uint32_t key0, uint32_t key1) {
     const int t = threadIdx.x;
-    const int32_t b = static_cast<int32_t>(blockIdx.x);
-    const int s = find_tensor(plan, b, t & 63);
-    const MxParam p = plan.p[s];
-    const int d = plan.v0 + static_cast<int>(blockIdx.y);
-    const int64_t tile0 = int64_t(b - plan.first_tile[s]) * kMxTile;
-    int64_t real = p.numel - d * p.ps;
-    real = real < 0 ? 0 : real > p.ps ? p.ps : real;
-    const int64_t codes_end = (p.ps + kMxBlock - 1) / kMxBlock * kMxBlock;
-    const uint16_t* src = p.src + d * p.ps;
-    uint8_t* chunk = chunk_of(plan, d);
-    const int64_t pair0 = (d * plan.blocks + p.block0) * (kMxBlock / 2);
-    u4 x[kMxVecs];
+    constexpr int kTile = static_cast<int>(mx_tile(kMxSendVecs));
+    const MxWork w = mx_work<kMxSendVecs>(plan, t & 63);
+    const uint16_t* src = w.p.src + w.v * w.p.ps + w.tile0;
+    uint8_t* chunk = chunk_of(plan, w.v);
+    uint8_t* c = chunk + 16 * w.p.block0 + w.tile0 / 2;
+    uint8_t* s = chunk + 16 * plan.blocks + w.p.block0 + w.tile0 / 32;
+    const int64_t pair0 = (w.v * plan.blocks + w.p.block0) * (kMxBlock / 2) + w.tile0 / 2;
+    if (w.real == kTile) mx_quantise<D, SR, false, true, kMxSendVecs>(w, src, c, s, nullptr, pair0, key0, key1, t);
+    else mx_quantise<D, SR, false, false, kMxSendVecs>(w, src, c, s, nullptr, pair0, key0, key1, t);
+}
+
+// The owner's average of N received chunks: fp32 sums in rank order from +0,
+// one fp32 division, rounded to 16 bits; padding positions 0.  A wave has
+// VECS runs of 512 elements; a norm slot's 1024 are one wave's, or two waves'.
+template <int VECS>
+struct MxAcc {
+    float sum[VECS][8];
+    bool bad[VECS];         // a block with byte 255: one select an element at the end, not one a chunk
+};
+
+// Adds BATCH chunks, chunk j's codes and scales of the wave's elements at
+// codes_at(j) and scales_at(j): all loads before the first add.
+template <int BATCH, int VECS, bool WHOLE, class CHUNK>
+__device__ __forceinline__ void mx_add(MxAcc<VECS>& acc, CHUNK chunk, int v0, int64_t codes, int64_t scales, int lane,
+                                       int real) {
+    uint32_t C[BATCH][VECS], S[BATCH][VECS];
 #pragma unroll
-    for (int u = 0; u < kMxVecs; ++u) {
-        const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
-        x[u] = u4{0, 0, 0, 0};
-        if (k < real) x[u] = load8(src + k, real - k);
+    for (int j = 0; j < BATCH; ++j) {
+        const uint8_t* p = chunk(v0 + j);
+        const uint8_t* pc = p + codes;
+        const uint8_t* ps = p + scales;
+#pragma unroll
+        for (int u = 0; u < VECS; ++u) {
+            C[j][u] = S[j][u] = 0;
+            if (WHOLE || 512 * u + 8 * lane < real) {
+                C[j][u] = *reinterpret_cast<const uint32_t*>(pc + static_cast<uint32_t>(256 * u + 4 * lane));
+                S[j][u] = ps[static_cast<uint32_t>(16 * u + (lane >> 2))];
+            }
+        }
     }
 #pragma unroll
-    for (int u = 0; u < kMxVecs; ++u) {
-        const int64_t k = tile0 + (int64_t(u) * kLbBlock + t) * 8;
-        const uint32_t sc = mx_scale<D, SR>(x[u]);
-        const uint32_t codes = mx_encode<D, SR>(x[u], sc, pair0 + k / 2, key0, key1);
-        if (k < codes_end) {
-            *reinterpret_cast<uint32_t*>(chunk + 16 * p.block0 + k / 2) = codes;
-            if ((t & 3) == 0) chunk[16 * plan.blocks + p.block0 + k / 32] = static_cast<uint8_t>(sc);
+    for (int j = 0; j < BATCH; ++j) {
+#pragma unroll
+        for (int u = 0; u < VECS; ++u) {
+            const float sc = scale_of(S[j][u]);
+            const f2 a = mx_pair<0>(C[j][u], sc), b = mx_pair<1>(C[j][u], sc);
+            const f2 c = mx_pair<2>(C[j][u], sc), d = mx_pair<3>(C[j][u], sc);
+            float(&s)[8] = acc.sum[u];
+            s[0] += a.x;
+            s[1] += a.y;
+            s[2] += b.x;
+            s[3] += b.y;
+            s[4] += c.x;
+            s[5] += c.y;
+            s[6] += d.x;
+            s[7] += d.y;
+            acc.bad[u] = acc.bad[u] || S[j][u] == 255u;
         }
     }
 }
 
-// The owner's average of N received chunks: fp32 sums in rank order from +0,
-// one fp32 division, rounded to 16 bits; padding positions 0.  A wave covers
-// the 1024 elements of one norm slot.
-constexpr int kMxBatch = 8;     // chunks whose loads are in flight together
+template <int BATCH, int VECS, bool WHOLE, class CHUNK>
+__device__ __forceinline__ void mx_sum(MxAcc<VECS>& acc, CHUNK chunk, int world, int64_t codes, int64_t scales,
+                                       int lane, int real) {
+    int v = 0;
+    for (; v + BATCH <= world; v += BATCH) mx_add<BATCH, VECS, WHOLE>(acc, chunk, v, codes, scales, lane, real);
+    if constexpr (BATCH > 8)
+        for (; v + 8 <= world; v += 8) mx_add<8, VECS, WHOLE>(acc, chunk, v, codes, scales, lane, real);
+    if (v + 4 <= world) {
+        mx_add<4, VECS, WHOLE>(acc, chunk, v, codes, scales, lane, real);
+        v += 4;
+    }
+    if (v + 2 <= world) {
+        mx_add<2, VECS, WHOLE>(acc, chunk, v, codes, scales, lane, real);
+        v += 2;
+    }
+    if (v < world) mx_add<1, VECS, WHOLE>(acc, chunk, v, codes, scales, lane, real);
+}
 
-template <int D, bool NORM>
+template <int D, bool NORM, int VECS, int BATCH, bool EVEN>
 __global__ __launch_bounds__(kLbBlock) void k_mx4_reduce(const MxPlan plan, double* __restrict__ partials) {
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    constexpr int kTile = static_cast<int>(mx_tile(VECS));
+    const int t = threadIdx.x, lane = t & 63, wave = wave_of(t);
     const int32_t b = static_cast<int32_t>(blockIdx.x);
     const int s = find_tensor(plan, b, lane);
     const MxParam p = plan.p[s];
     const int64_t tile = b - plan.first_tile[s];
-    const int64_t k0 = tile * kMxReduceTile + int64_t(wave) * 1024;
-    int64_t real = p.numel - plan.rank * p.ps;
-    real = real < 0 ? 0 : real > p.ps ? p.ps : real;
+    const int64_t k0 = tile * kTile + wave * (512 * VECS);         // the wave's first
+    int64_t rl = p.numel - plan.rank * p.ps;
+    rl = (rl > p.ps ? p.ps : rl) - k0;
+    const int real = static_cast<int>(rl < 0 ? 0 : rl > 512 * VECS ? 512 * VECS : rl);
+    const int64_t tl = p.ps - k0;
+    const int total = static_cast<int>(tl < 0 ? 0 : tl > 512 * VECS ? 512 * VECS : tl);
     double ss = 0.0;
-    if (k0 < p.ps) {
-        float acc[2][8];
+    if (total > 0) {
+        const int64_t codes = 16 * p.block0 + k0 / 2, scales = 16 * plan.blocks + p.block0 + k0 / 32;
+        MxAcc<VECS> acc;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < VECS; ++u) {
+            acc.bad[u] = false;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[u][e] = 0.0f;
-        for (int vb = 0; vb < plan.world; vb += kMxBatch) {
-            uint32_t C[kMxBatch][2], S[kMxBatch][2];
-#pragma unroll
-            for (int j = 0; j < kMxBatch; ++j) {
-                if (vb + j < plan.world) {
-                    const uint8_t* chunk = chunk_of(plan, vb + j);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int64_t k = k0 + 512 * u + 8 * lane;
-                        C[j][u] = S[j][u] = 0;
-                        if (k < real) {
-                            C[j][u] = *reinterpret_cast<const uint32_t*>(chunk + 16 * p.block0 + k / 2);
-                            S[j][u] = chunk[16 * plan.blocks + p.block0 + k / 32];
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kMxBatch; ++j) {
-                if (vb + j < plan.world) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float sc = S[j][u] == 255u ? __builtin_nanf("") : scale_of(S[j][u]);
-                        const f2 a = mx_pair<0>(C[j][u], sc), bb = mx_pair<1>(C[j][u], sc);
-                        const f2 cc = mx_pair<2>(C[j][u], sc), d = mx_pair<3>(C[j][u], sc);
-                        acc[u][0] += a.x;
-                        acc[u][1] += a.y;
-                        acc[u][2] += bb.x;
-                        acc[u][3] += bb.y;
-                        acc[u][4] += cc.x;
-                        acc[u][5] += cc.y;
-                        acc[u][6] += d.x;
-                        acc[u][7] += d.y;
-                        if (S[j][u] == 255u) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) acc[u][e] = __builtin_nanf("");
-                        }
-                    }
-                }
-            }
+            for (int e = 0; e < 8; ++e) acc.sum[u][e] = 0.0f;
         }
+        const auto sum = [&](auto chunk) {
+            if (real == 512 * VECS) mx_sum<BATCH, VECS, true>(acc, chunk, plan.world, codes, scales, lane, real);
+            else mx_sum<BATCH, VECS, false>(acc, chunk, plan.world, codes, scales, lane, real);
+        };
+        if constexpr (EVEN) sum([&](int v) -> const uint8_t* { return plan.base + v * plan.stride; });
+        else sum([&](int v) -> const uint8_t* { return plan.chunk[v]; });
         const float n = static_cast<float>(plan.world);
         const bool pow2 = (plan.world & (plan.world - 1)) == 0;
         const float inv = 1.0f / n;
+        uint16_t* dst = p.dst + k0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t k = k0 + 512 * u + 8 * lane;
+        for (int u = 0; u < VECS; ++u) {
+            const int k = 512 * u + 8 * lane;
             uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float mean = pow2 ? acc[u][e] * inv : acc[u][e] / n;
+                float mean = pow2 ? acc.sum[u][e] * inv : acc.sum[u][e] / n;
+                if (acc.bad[u]) mean = __builtin_nanf("");
                 h[e] = k + e < real ? narrow<D>(mean) : 0u;
                 if constexpr (NORM) {
                     const double y = widen<D>(h[e]);
@@ -692,13 +759,20 @@ __global__ __launch_bounds__(kLbBlock) void k_mx4_reduce(const MxPlan plan, doub
                 }
             }
             const u4 x = {h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-            if (k < p.ps) store8(p.dst + k, p.ps - k, x);
+            if (k < total) store8(dst + k, total - k, x);
         }
     }
     if constexpr (NORM) {
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) ss += __shfl_xor(ss, o, 64);
-        if (lane == 0) partials[p.slot + tile * 4 + wave] = ss;
+        if constexpr (VECS == 2) {
+            if (lane == 0) partials[p.slot + tile * 4 + wave] = ss;
+        } else {
+            __shared__ double sh[kLbBlock / 64];
+            if (lane == 0) sh[wave] = ss;
+            __syncthreads();
+            if (lane == 0 && (wave & 1) == 0) partials[p.slot + tile * 2 + wave / 2] = sh[wave] + sh[wave + 1];
+        }
     }
 }
 
@@ -767,12 +841,22 @@ hipError_t launch_mx4_send(int32_t dtype, bool stochastic, uint32_t key0, uint32
     return launch(stochastic ? k_mx4_send<kBF16, true> : k_mx4_send<kBF16, false>, g, 0, stream, plan, key0, key1);
 }
 
-hipError_t launch_mx4_reduce(int32_t dtype, const MxPlan& plan, double* partials, hipStream_t stream) {
+template <int D, bool NORM>
+static hipError_t mx4_reduce_launch(bool thin, dim3 g, const MxPlan& plan, double* partials, hipStream_t stream) {
+    const bool even = plan.base != nullptr;
+    if (thin)
+        return launch(even ? k_mx4_reduce<D, NORM, 1, 32, true> : k_mx4_reduce<D, NORM, 1, 32, false>, g, 0, stream, plan, partials);
+    return launch(even ? k_mx4_reduce<D, NORM, 2, 8, true> : k_mx4_reduce<D, NORM, 2, 8, false>, g, 0, stream, plan, partials);
+}
+
+hipError_t launch_mx4_reduce(int32_t dtype, bool thin, const MxPlan& plan, double* partials, hipStream_t stream) {
     if (plan.n <= 0) return hipSuccess;
     const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]));
-    const bool norm = partials != nullptr;
-    if (dtype == kFP16) return launch(norm ? k_mx4_reduce<kFP16, true> : k_mx4_reduce<kFP16, false>, g, 0, stream, plan, partials);
-    return launch(norm ? k_mx4_reduce<kBF16, true> : k_mx4_reduce<kBF16, false>, g, 0, stream, plan, partials);
+    if (dtype == kFP16)
+        return partials != nullptr ? mx4_reduce_launch<kFP16, true>(thin, g, plan, partials, stream)
+                                   : mx4_reduce_launch<kFP16, false>(thin, g, plan, partials, stream);
+    return partials != nullptr ? mx4_reduce_launch<kBF16, true>(thin, g, plan, partials, stream)
+                               : mx4_reduce_launch<kBF16, false>(thin, g, plan, partials, stream);
 }
 
 }  // namespace zs3

@@ -74,9 +74,23 @@ hipError_t launch_moment8_read(bool fp32_out, const ReadPlan& plan, hipStream_t 
 
 constexpr int kMxParams = 24;              // parameters of one launch
 constexpr int kMxRanks = 256;              // chunk pointers of one launch
-constexpr int kMxVecs = 4;                 // groups of 8 elements of a thread (gather, send)
-constexpr int64_t kMxTile = int64_t(kLbBlock) * 8 * kMxVecs;
-constexpr int64_t kMxReduceTile = int64_t(kLbBlock) * 8 * 2;       // a wave covers one norm slot's 1024 elements
+// Groups of 8 elements of a thread.  The gather is short of stores in flight
+// and has N partitions to cut into tiles: two groups ran 30.2 us where four
+// took 32.5 on 84M elements over 64 ranks (equal over 8); the send waits for
+// its loads: four took 22.9 us where two took 23.7 on 42M over 8.
+constexpr int kMxGatherVecs = 2;
+constexpr int kMxSendVecs = 4;
+constexpr int64_t mx_tile(int vecs) { return int64_t(kLbBlock) * 8 * vecs; }
+
+// The owner's average: a thread takes two groups of 8 elements and has 8
+// chunks' loads in flight (2 x 8), or, where that leaves the chip short of
+// workgroups (fewer than two a CU), one group and 32 chunks' (1 x 32).
+// Measured: 64 ranks, 64 parameters of 1.05M (96 workgroups a launch) 34.1 us
+// against 19.7; 64 ranks, own 2.4M elements (576 workgroups) 19.5 both; 8
+// ranks, own 22M (5376) 24.2 against 30.3, since the registers of the loads
+// in flight cost resident waves, which is what hides latency once the chip is full.
+constexpr int64_t kMxThin = 512;           // workgroups of the 2 x 8 form from which it is taken
+constexpr int mx_reduce_vecs(bool thin) { return thin ? 1 : 2; }
 
 // One parameter of a bucket.
 struct MxParam {
@@ -111,6 +125,6 @@ hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, const MxPlan& plan, in
 // destinations [v0, v0 + n_ranks): quantise every destination's partitions.
 hipError_t launch_mx4_send(int32_t dtype, bool stochastic, uint32_t key0, uint32_t key1, const MxPlan& plan,
                            int32_t n_ranks, hipStream_t stream);
-hipError_t launch_mx4_reduce(int32_t dtype, const MxPlan& plan, double* partials, hipStream_t stream);
+hipError_t launch_mx4_reduce(int32_t dtype, bool thin, const MxPlan& plan, double* partials, hipStream_t stream);
 
 }  // namespace zs3

@@ -372,12 +372,13 @@ struct Chunks {
         base = reinterpret_cast<uint8_t*>(pa - a * stride);
         even = base != nullptr;
     }
-    // Puts ranks [v0, v0 + count) into a plan.
+    // Puts ranks [v0, v0 + count) into a plan: pointers where they fit (the
+    // kernels then load them as scalars), else the spacing.
     void put(MxPlan* p, int32_t v0, int32_t count) const {
         p->v0 = v0;
-        p->base = even ? base : nullptr;
+        p->base = count > kMxRanks ? base : nullptr;
         p->stride = stride;
-        if (!even)
+        if (count <= kMxRanks)
             for (int32_t v = 0; v < count; ++v) p->chunk[v] = static_cast<uint8_t*>(const_cast<void*>(list[v0 + v]));
     }
 };
@@ -409,7 +410,7 @@ zs3_status by_launch(const Bucket& b, MxPlan* plan, TILES tiles_of, FILL fill, L
 
 // Ranks of one launch: an even spacing needs no pointers, and the grid's
 // second extent is at most 65535.
-int32_t ranks_at_once(const Chunks& c) { return c.even ? 65535 : kMxRanks; }
+int32_t ranks_at_once(const Chunks& c) { return c.even && c.world > kMxRanks ? 65535 : kMxRanks; }
 
 }  // namespace
 
@@ -484,7 +485,7 @@ zs3_status zs3_gather_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_t dtype,
                 plan.stride = 0;
             }
             s = by_launch(
-                b, &plan, [](const Item& it) { return div_up(it.ps, kMxTile); },
+                b, &plan, [](const Item& it) { return div_up(it.ps, mx_tile(kMxGatherVecs)); },
                 [&](const Item& it, MxParam* p) {
                     p->src = pack ? static_cast<const uint16_t*>(shard_flat) + it.offset : nullptr;
                     p->dst = unpack ? static_cast<uint16_t*>(full_flat) + it.full0 : nullptr;
@@ -570,7 +571,7 @@ zs3_status zs3_reduce_scatter_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_
                 plan.v0 = v0;
                 const int32_t count = std::min(65535, b.world - v0);
                 s = by_launch(
-                    b, &plan, [](const Item& it) { return div_up(it.ps, kMxTile); },
+                    b, &plan, [](const Item& it) { return div_up(it.ps, mx_tile(kMxSendVecs)); },
                     [&](const Item& it, MxParam* p) { p->src = static_cast<const uint16_t*>(grads[it.request]); },
                     [&]() {
                         return launched(launch_mx4_send(dtype, rounding == ZS3_ROUND_STOCHASTIC, static_cast<uint32_t>(keys),
@@ -599,22 +600,24 @@ zs3_status zs3_reduce_scatter_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_
                     at += norm_slot_groups(ps) * kNormSlotsPerGroup;
                 }
             }
-            static_assert(kRsPiece % kMxReduceTile == 0 && kRsPiece / 1024 == kNormSlotsPerGroup,
-                          "a norm slot has to be one wave's 1024 elements");
+            static_assert(kRsPiece / 1024 == kNormSlotsPerGroup, "a norm slot has to stand for 1024 elements");
+            // a launch holds kMxParams parameters: what counts is its workgroups
+            const int64_t launches = div_up(static_cast<int64_t>(b.items.size()), kMxParams);
+            const bool thin = b.chunk_numel / mx_tile(mx_reduce_vecs(false)) < kMxThin * launches;
+            const int64_t tile = mx_tile(mx_reduce_vecs(thin));
             size_t k = 0;
             s = by_launch(
                 b, &plan,
                 // with the sums fused, tiles cover every slot that the parameter has
                 [&](const Item& it) {
-                    return partials != nullptr ? norm_slot_groups(it.ps) * (kRsPiece / kMxReduceTile)
-                                               : div_up(it.ps, kMxReduceTile);
+                    return partials != nullptr ? norm_slot_groups(it.ps) * (kRsPiece / tile) : div_up(it.ps, tile);
                 },
                 [&](const Item& it, MxParam* p) {
                     p->dst = static_cast<uint16_t*>(grad_flat) + it.offset;
                     p->slot = slot[k++];
                 },
                 [&]() {
-                    return launched(launch_mx4_reduce(dtype, plan, partials, static_cast<hipStream_t>(stream)),
+                    return launched(launch_mx4_reduce(dtype, thin, plan, partials, static_cast<hipStream_t>(stream)),
                                     "4-bit reduce kernel launch");
                 });
             if (s != ZS3_OK) return s;

@@ -34,6 +34,8 @@ namespace {
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u2h __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u2w __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t u4w __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u4h __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
@@ -140,19 +142,34 @@ __device__ __forceinline__ int line_offset(const void* p) {
     return static_cast<int>(reinterpret_cast<uintptr_t>(p) & (kLine - 1));
 }
 
-// Stores bytes [off, off + len) of `lds` to `to` (whose address modulo 128 is
-// off) in 16-byte chunks, by threads t, t + step, ...; the chunks at the ends
+// Where byte i of an array whose address modulo 128 is `off` lies in LDS: at
+// off + i, or 2 bytes on where 16-bit data would lie between words (LDS takes
+// such writes several times slower; the shift is undone on the way out).
+__device__ __forceinline__ int stage_offset(int off) { return off + (off & 2); }
+
+// Room for an array of n bytes.
+constexpr int stage_bytes(int64_t n) { return static_cast<int>(n) + kLine + 32; }
+
+// Stores an array of `len` bytes from LDS to `to`, whose address modulo 128 is
+// `off`, in 16-byte chunks, by threads t, t + step, ...; the chunks at the ends
 // by elements of T.
 template <class T>
-__device__ __forceinline__ void store_lines(uint8_t* to, const uint8_t* lds, int off, int len, int t, int step) {
-    uint8_t* base = to - off;
+__device__ __forceinline__ void store_lines(void* to, const uint8_t* lds, int off, int len, int t, int step) {
+    uint8_t* base = static_cast<uint8_t*>(to) - off;
+    const bool shifted = sizeof(T) == 2 && (off & 2) != 0;
     for (int c = 16 * t; c < off + len; c += 16 * step) {
         if (c >= off && c + 16 <= off + len) {
-            __builtin_nontemporal_store(*reinterpret_cast<const u4*>(lds + c), reinterpret_cast<u4*>(base + c));
+            u4 x = *reinterpret_cast<const u4*>(lds + c);
+            if (shifted) {
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(lds + c + 16);
+                x = u4{__builtin_amdgcn_alignbyte(x[1], x[0], 2), __builtin_amdgcn_alignbyte(x[2], x[1], 2),
+                       __builtin_amdgcn_alignbyte(x[3], x[2], 2), __builtin_amdgcn_alignbyte(y, x[3], 2)};
+            }
+            __builtin_nontemporal_store(x, reinterpret_cast<u4*>(base + c));
         } else {
-            for (int i = 0; i < 16; i += static_cast<int>(sizeof(T)))
-                if (c + i >= off && c + i < off + len)
-                    *reinterpret_cast<T*>(base + c + i) = *reinterpret_cast<const T*>(lds + c + i);
+            const uint8_t* from = lds + (shifted ? 2 : 0);
+            for (int i = c; i < c + 16; i += static_cast<int>(sizeof(T)))
+                if (i >= off && i < off + len) *reinterpret_cast<T*>(base + i) = *reinterpret_cast<const T*>(from + i);
         }
     }
 }
@@ -325,10 +342,10 @@ struct Load8 {
 };
 
 struct Stage8 {
-    alignas(16) uint8_t w[4 * kStepTile + kLine];
-    alignas(16) uint8_t p[2 * kStepTile + kLine];
-    alignas(16) uint8_t m[kStepTile + kLine];
-    alignas(16) uint8_t v[kStepTile + kLine];
+    alignas(16) uint8_t w[stage_bytes(4 * kStepTile)];
+    alignas(16) uint8_t p[stage_bytes(2 * kStepTile)];
+    alignas(16) uint8_t m[stage_bytes(kStepTile)];
+    alignas(16) uint8_t v[stage_bytes(kStepTile)];
 };
 
 template <int D, int G>
@@ -388,7 +405,7 @@ __device__ __forceinline__ void adamw8_tile(const StepTensor& t, int64_t tile0, 
             adamw8_quad(x, g, left, e, t, c);
             const int i = static_cast<int>(e - tile0);
             *reinterpret_cast<f4*>(stage.w + wo + 4 * i) = f4{x.w[0], x.w[1], x.w[2], x.w[3]};
-            *reinterpret_cast<u2h*>(stage.p + po + 2 * i) = u2h{narrow2<D>(x.w[0], x.w[1]), narrow2<D>(x.w[2], x.w[3])};
+            *reinterpret_cast<u2w*>(stage.p + stage_offset(po) + 2 * i) = u2w{narrow2<D>(x.w[0], x.w[1]), narrow2<D>(x.w[2], x.w[3])};
             *reinterpret_cast<uint32_t*>(stage.m + mo + i) = x.m;
             *reinterpret_cast<uint32_t*>(stage.v + vo + i) = x.v;
             if (left > 0 && (lane & 7) == 0) {
@@ -400,9 +417,9 @@ __device__ __forceinline__ void adamw8_tile(const StepTensor& t, int64_t tile0, 
     __syncthreads();
     const int64_t rest = t.numel - tile0;
     const int n = static_cast<int>(rest > kStepTile ? kStepTile : rest), th = wave * 64 + lane;
-    store_lines<float>(reinterpret_cast<uint8_t*>(t.master + tile0), stage.w, wo, 4 * n, th, kLbBlock);
+    store_lines<float>(t.master + tile0, stage.w, wo, 4 * n, th, kLbBlock);
     if (t.param != nullptr)
-        store_lines<uint16_t>(reinterpret_cast<uint8_t*>(t.param + tile0), stage.p, po, 2 * n, th, kLbBlock);
+        store_lines<uint16_t>(t.param + tile0, stage.p, po, 2 * n, th, kLbBlock);
     // half of the threads for each moment
     if (th < kLbBlock / 2) store_lines<uint8_t>(m8 + tile0, stage.m, mo, n, th, kLbBlock / 2);
     else store_lines<uint8_t>(v8 + tile0, stage.v, vo, n, th - kLbBlock / 2, kLbBlock / 2);
@@ -434,12 +451,16 @@ __global__ __launch_bounds__(kLbBlock) void k_adamw(const StepPlan plan, const S
 
 template <bool F32>
 __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) {
+    using T = std::conditional_t<F32, float, uint16_t>;
+    __shared__ alignas(16) uint8_t stage[stage_bytes(sizeof(T) * kReadTile)];
     const int lane = threadIdx.x & 63, wave = wave_of(threadIdx.x);
     const int32_t b = static_cast<int32_t>(blockIdx.x);
     const int s = find_tensor(plan, b, lane);
     const ReadTensor t = plan.t[s];
-    const int64_t e0 = int64_t(b - plan.first_tile[s]) * kReadTile + int64_t(wave) * 256 * kReadRuns;
+    const int64_t tile0 = int64_t(b - plan.first_tile[s]) * kReadTile, e0 = tile0 + wave * (256 * kReadRuns);
     const int64_t scales = (t.numel + kMxBlock - 1) / kMxBlock * kMxBlock;
+    T* out = static_cast<T*>(t.out) + tile0;
+    const int oo = line_offset(out);
     uint32_t C[kReadRuns], S[kReadRuns];
 #pragma unroll
     for (int k = 0; k < kReadRuns; ++k) {
@@ -452,7 +473,7 @@ __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) 
     }
 #pragma unroll
     for (int k = 0; k < kReadRuns; ++k) {
-        const int64_t e = e0 + 256 * k + 4 * lane;
+        const int i = wave * (256 * kReadRuns) + 256 * k + 4 * lane;
         float x[4];
         if (t.second != 0) {
 #pragma unroll
@@ -465,23 +486,14 @@ __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) 
             x[2] = d.x;
             x[3] = d.y;
         }
-        if (e + 4 <= t.numel) {
-            if constexpr (F32)
-                __builtin_nontemporal_store(f4{x[0], x[1], x[2], x[3]},
-                                            reinterpret_cast<f4*>(static_cast<float*>(t.out) + e));
-            else
-                __builtin_nontemporal_store(u2h{narrow2<kBF16>(x[0], x[1]), narrow2<kBF16>(x[2], x[3])},
-                                            reinterpret_cast<u2h*>(static_cast<uint16_t*>(t.out) + e));
-        } else {
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                if (e + q < t.numel) {
-                    if constexpr (F32) static_cast<float*>(t.out)[e + q] = x[q];
-                    else static_cast<uint16_t*>(t.out)[e + q] = static_cast<uint16_t>(narrow<kBF16>(x[q]));
-                }
-            }
-        }
+        uint8_t* to = stage + (F32 ? oo : stage_offset(oo)) + sizeof(T) * i;
+        if constexpr (F32) *reinterpret_cast<f4*>(to) = f4{x[0], x[1], x[2], x[3]};
+        else *reinterpret_cast<u2w*>(to) = u2w{narrow2<kBF16>(x[0], x[1]), narrow2<kBF16>(x[2], x[3])};
     }
+    __syncthreads();
+    const int64_t rest = t.numel - tile0;
+    const int n = static_cast<int>(rest > kReadTile ? kReadTile : rest);
+    store_lines<T>(out, stage, oo, static_cast<int>(sizeof(T)) * n, threadIdx.x, kLbBlock);
 }
 
 // ---------------------------------------------------------- the 4-bit wire
@@ -645,7 +657,8 @@ __device__ __forceinline__ void mx_quantise(const MxWork& w, const uint16_t* src
 
 template <int D, bool WHOLE, int VECS>
 __device__ __forceinline__ void mx_widen(const MxWork& w, const uint8_t* codes, const uint8_t* scales, uint16_t* out,
-                                         int t) {
+                                         uint8_t* stage, int t) {
+    const int oo = line_offset(out);
     uint32_t C[VECS], S[VECS];
 #pragma unroll
     for (int u = 0; u < VECS; ++u) {
@@ -659,8 +672,10 @@ __device__ __forceinline__ void mx_widen(const MxWork& w, const uint8_t* codes, 
 #pragma unroll
     for (int u = 0; u < VECS; ++u) {
         const int k = (u * kLbBlock + t) * 8;
-        if (WHOLE || k < w.real) store8(out + k, WHOLE ? 8 : w.real - k, mx_decode<D>(C[u], S[u]));
+        *reinterpret_cast<u4w*>(stage + stage_offset(oo) + 2 * k) = mx_decode<D>(C[u], S[u]);
     }
+    __syncthreads();
+    store_lines<uint16_t>(out, stage, oo, 2 * w.real, t, kLbBlock);
 }
 
 // Tile x of a parameter's partition, rank y: the own rank's part is quantised
@@ -681,9 +696,10 @@ __global__ __launch_bounds__(kLbBlock) void k_mx4_gather(const MxPlan plan) {
         if (w.real == kTile) mx_quantise<D, false, kOut, true, kMxGatherVecs>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
         else mx_quantise<D, false, kOut, false, kMxGatherVecs>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
     } else if constexpr (kOut) {
+        __shared__ alignas(16) uint8_t stage[stage_bytes(2 * kTile)];
         const uint8_t* chunk = chunk_of(plan, w.v);
-        if (w.real == kTile) mx_widen<D, true, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, t);
-        else mx_widen<D, false, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, t);
+        if (w.real == kTile) mx_widen<D, true, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, stage, t);
+        else mx_widen<D, false, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, stage, t);
     }
 }
 

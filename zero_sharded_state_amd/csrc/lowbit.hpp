@@ -52,8 +52,7 @@ hipError_t launch_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state
 // ------------------------------------------------------ 8-bit moments read
 
 constexpr int kReadTensors = 64;
-constexpr int kReadRuns = 4;
-constexpr int64_t kReadTile = int64_t(kLbBlock) * 4 * kReadRuns;
+constexpr int64_t kReadTile = int64_t(kLbBlock) * 16;
 
 struct ReadTensor {
     int64_t numel;

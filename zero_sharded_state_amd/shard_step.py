@@ -31,6 +31,11 @@ a few streams that fork from it and join back):
    only writer of the shard, so the shard is always the 16-bit rounding of
    the fp32 master.
 
+Fewer bits, each part by itself: ``state_bits=8`` holds Adam's moments in 8 bits
+a value, ``gather_bits=4`` sends the gathers' chunks and ``reduce_bits=4`` (with
+the non-contiguous path) the gradients' over a 4-bit wire; ``no_decay`` names
+the parameters (norms, biases) that weight decay leaves alone.
+
 No call synchronises; nothing is copied to the host.  All buffers are torch
 tensors owned by this object; all arithmetic runs in libzs3's kernels.
 """
@@ -59,8 +64,26 @@ class ShardStep:
                  sub_group_size: int, adam: AdamConfig = AdamConfig(), max_norm: float = 1.0,
                  device: str = "cuda", rs_streams: int = 1, gather_streams: int = 1,
                  fuse_norm: bool = False, reduce_path: str = "contiguous", offload: bool = False,
-                 offload_chunk: int = 0, recv_layout: str = "rank", single_launch="none"):
+                 offload_chunk: int = 0, recv_layout: str = "rank", single_launch="none",
+                 state_bits: int = 32, gather_bits: int = 16, reduce_bits: int = 16,
+                 no_decay: Sequence[int] = (), seed: int = 0):
         import torch
+
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits {state_bits!r} is not 8 or 32")
+        if gather_bits not in (4, 16) or reduce_bits not in (4, 16):
+            raise ValueError("gather_bits and reduce_bits are 4 or 16")
+        if reduce_bits == 4 and reduce_path != "coalesced":
+            raise ValueError("a 4-bit gradient wire needs the coalesced gradient path")
+        # the list step holds for 8-bit moments and for a decay by parameter
+        self.listed = state_bits == 8 or bool(no_decay)
+        if self.listed and offload:
+            raise ValueError("offloaded state has 32 bits and one weight decay")
+        unknown = set(no_decay) - set(ds_ids)
+        if unknown:
+            raise ValueError(f"no_decay names ds_ids that are not there: {sorted(unknown)}")
+        self.state_bits, self.gather_bits, self.reduce_bits = state_bits, gather_bits, reduce_bits
+        self.no_decay, self.seed = frozenset(no_decay), int(seed)
 
         if reduce_path not in ("contiguous", "coalesced"):
             raise ValueError(f"reduce_path {reduce_path!r} is not 'contiguous' or 'coalesced'")
@@ -78,6 +101,8 @@ class ShardStep:
             raise ValueError(f"single_launch {single_launch!r} is not none, gather, reduce or both")
         self.single_gather = single_launch in ("gather", "both")
         self.single_reduce = single_launch in ("reduce", "both")
+        if self.single_gather and gather_bits == 4:
+            raise ValueError("the 4-bit gather takes one launch per bucket")
         if self.single_reduce and reduce_path != "contiguous":
             raise ValueError("a single-launch gradient phase needs the contiguous gradient path")
         self.single_launch = single_launch
@@ -135,7 +160,16 @@ class ShardStep:
         dev = self.device
         self.full = torch.empty(max(1, self.full_len), dtype=i16, device=dev)  # gathered parameters
         self.pers_full = torch.empty(max(1, self.P), dtype=i16, device=dev)   # whole persistent params
-        self.wire = torch.empty(max(1, self.W), dtype=i16, device=dev)        # per-bucket all-gather output
+        if gather_bits == 4:
+            # per bucket the N chunks of codes and scales, each 16-byte aligned
+            self.chunk4, o = [], 0              # (byte offset, bytes of a chunk)
+            for b in self.gather_buckets:
+                size = zs.zs3_mx4_sizes(self.h, b)[1]
+                self.chunk4.append((o, size))
+                o += self.N * size
+            self.wire = torch.zeros(max(1, o), dtype=torch.uint8, device=dev)
+        else:
+            self.wire = torch.empty(max(1, self.W), dtype=i16, device=dev)    # per-bucket all-gather output
         self.shard = torch.zeros(max(1, self.S), dtype=i16, device=dev)
         self.grad = torch.zeros(max(1, self.S), dtype=i16, device=dev)
         # The slices the N ranks send this rank.  "rank": one copy of the
@@ -166,7 +200,17 @@ class ShardStep:
         # lives in pinned host memory ([codex] 6.1, 6.3)
         sa = (max(1, self.S) + (1 << 19) - 1) >> 19 << 19
         self.offload = bool(offload)
-        if self.offload:
+        if state_bits == 8:
+            # the moments of each parameter's real elements, at 16-byte
+            # boundaries of one allocation an array; zeros are the start
+            self.state = torch.zeros(max(1, self.S), dtype=f32, device=dev)
+            self.moment_off, o = {}, 0
+            for p in self.params:
+                self.moment_off[p["ds_id"]] = o
+                o += zs.zs3_moment8_bytes(p["own"][1] - p["own"][0])
+            self.exp_avg = torch.zeros(max(1, o), dtype=torch.uint8, device=dev)
+            self.exp_avg_sq = torch.zeros(max(1, o), dtype=torch.uint8, device=dev)
+        elif self.offload:
             # offload_chunk 0: Adam reads and writes the host state directly;
             # otherwise chunks of that many elements are staged through HBM
             self.state = torch.zeros(3 * sa, dtype=f32, pin_memory=True)
@@ -175,8 +219,9 @@ class ShardStep:
         else:
             self.state = torch.zeros(3 * sa, dtype=f32, device=dev)
         self.master = self.state[0:max(1, self.S)]
-        self.exp_avg = self.state[sa:sa + max(1, self.S)]
-        self.exp_avg_sq = self.state[2 * sa:2 * sa + max(1, self.S)]
+        if state_bits == 32:
+            self.exp_avg = self.state[sa:sa + max(1, self.S)]
+            self.exp_avg_sq = self.state[2 * sa:2 * sa + max(1, self.S)]
         self.sumsq = torch.zeros(self.N + 1, dtype=torch.float64, device=dev)
         self.n_slots, _ = zs.zs3_layout_norm_slots(self.h)
         self.partials = torch.zeros(max(1, self.n_slots), dtype=torch.float64, device=dev)
@@ -207,6 +252,9 @@ class ShardStep:
         return self.full.data_ptr() + 2 * self.full_off[ds_id]
 
     def chunk_ptr(self, bucket: int, v: int) -> int:
+        if self.gather_bits == 4:
+            o, size = self.chunk4[bucket]
+            return self.wire.data_ptr() + o + v * size
         _, _, w, c = self.bucket_meta[bucket]
         return self.wire.data_ptr() + 2 * (w + v * c)
 
@@ -249,6 +297,13 @@ class ShardStep:
         for b in self.reduce_buckets:
             ids_part = sorted(d for d in b if not self.by_id[d]["persistent"])
             ids_pers = [d for d in b if self.by_id[d]["persistent"]]
+            if self.reduce_bits == 4:       # offsets in bytes, C the bytes of a chunk
+                C = zs.zs3_mx4_sizes(self.h, ids_part)[1]
+                others = [v for v in range(self.N) if v != self.rank]
+                buckets.append((ids_part, ids_pers, C, cursor,
+                                {v: cursor + (self.N + k) * C for k, v in enumerate(others)}))
+                cursor += (self.N + len(others)) * C
+                continue
             C = sum(self.by_id[d]["partition_size"] for d in ids_part)
             if not ids_part:
                 buckets.append((ids_part, ids_pers, 0, 0, {}))
@@ -257,7 +312,8 @@ class ShardStep:
             send = place(self.N * C, (res - 2 * self.rank * C) % 16)
             chunks = {v: place(C, res) for v in range(self.N) if v != self.rank}
             buckets.append((ids_part, ids_pers, C, send, chunks))
-        self.xbuf = torch.zeros(max(1, cursor), dtype=torch.int16, device=self.device)
+        self.xbuf = torch.zeros(max(1, cursor), dtype=torch.uint8 if self.reduce_bits == 4 else torch.int16,
+                                device=self.device)
         self.coalesced = buckets
 
     def grad_ptr(self, ds_id: int) -> int:
@@ -267,12 +323,13 @@ class ShardStep:
     def recv_chunk_ptr(self, bucket: int, v: int) -> int:
         """The chunk virtual rank v sends to this rank for a gradient bucket."""
         _, _, C, send, chunks = self.coalesced[bucket]
+        unit = self.xbuf.element_size()
         if v == self.rank:
-            return self.xbuf.data_ptr() + 2 * (send + v * C)
-        return self.xbuf.data_ptr() + 2 * chunks[v]
+            return self.xbuf.data_ptr() + unit * (send + v * C)
+        return self.xbuf.data_ptr() + unit * chunks[v]
 
     def send_ptr(self, bucket: int) -> int:
-        return self.xbuf.data_ptr() + 2 * self.coalesced[bucket][3]
+        return self.xbuf.data_ptr() + self.xbuf.element_size() * self.coalesced[bucket][3]
 
     @property
     def norm_ptr(self) -> int:
@@ -313,6 +370,9 @@ class ShardStep:
             ids = (I64 * len(b))(*b)
             src = (P * (len(b) * self.N))(*[self.recv_ptr(v, d) for d in b for v in range(self.N)])
             self._r.append((len(b), ids, src))
+        if self.listed:
+            self._lists = [zs.zs3_adamw_tensor_list([self._tensor(p) for p in self.params if b <= p["shard_offset"] < e])
+                           for b, e in self.sub_groups]
         all_ids = [p["ds_id"] for p in self.params]
         self._p = (len(all_ids), (I64 * len(all_ids))(*all_ids),
                    (P * len(all_ids))(*[self.full_param_ptr(d) for d in all_ids]))
@@ -331,6 +391,28 @@ class ShardStep:
             self._rm = (len(rs_ids), (I64 * len(rs_ids))(*rs_ids),
                         (P * (len(rs_ids) * self.N))(*[self.recv_ptr(v, d) for d in rs_ids for v in range(self.N)]))
 
+    def _tensor(self, p) -> dict:
+        """A parameter's real elements as an entry of the list step."""
+        d, o = p["ds_id"], p["shard_offset"]
+        m = self.moment_off[d] if self.state_bits == 8 else 4 * o
+        return dict(numel=p["own"][1] - p["own"][0], id=d, master=self.master.data_ptr() + 4 * o,
+                    grad=self.grad.data_ptr() + 2 * o, param=self.shard.data_ptr() + 2 * o,
+                    exp_avg=self.exp_avg.data_ptr() + m, exp_avg_sq=self.exp_avg_sq.data_ptr() + m,
+                    weight_decay=0.0 if d in self.no_decay else self.adam.weight_decay)
+
+    def moments(self, ds_id: int):
+        """(exp_avg, exp_avg_sq) of a parameter's real elements in fp32: views of
+        the 32-bit state, or 8-bit moments read out."""
+        p = self.by_id[ds_id]
+        o, n = p["shard_offset"], p["own"][1] - p["own"][0]
+        if self.state_bits == 32:
+            return self.exp_avg[o:o + n], self.exp_avg_sq[o:o + n]
+        out = [self.torch.empty(n, dtype=self.torch.float32, device=self.device) for _ in range(2)]
+        m = self.moment_off[ds_id]
+        zs.zs3_moment8_read("fp32", [dict(numel=n, kind=kind, moment=buf.data_ptr() + m, out=x) for buf, kind, x in
+                                     ((self.exp_avg, zs.ZS3_EXP_AVG, out[0]), (self.exp_avg_sq, zs.ZS3_EXP_AVG_SQ, out[1]))])
+        return tuple(out)
+
     # ------------------------------------------------------------- phases
     def _stream(self) -> int:
         return int(self.torch.cuda.current_stream().cuda_stream)
@@ -339,24 +421,27 @@ class ShardStep:
         if st != 0:
             raise zs.Zs3Error(st, zs.zs3_last_error())
 
+    @property
+    def _gather_fn(self):
+        """The gather call of the wire's width (same arguments)."""
+        return zs.lib().zs3_gather_coalesced_mx4 if self.gather_bits == 4 else zs.lib().zs3_gather_coalesced
+
     def gather(self, bi: int, stream=None):
         """Pack + unpack of one bucket (one launch: the wire's own slot is the pack output)."""
         n, ids, own, chunks, fullp = self._g[bi]
-        self._ok(zs.lib().zs3_gather_coalesced(self.h, self.rank, self.dcode, zs.ZS3_PACK | zs.ZS3_UNPACK, n, ids,
-                                               self.shard.data_ptr(), own, chunks, fullp, None,
-                                               stream if stream is not None else self._stream()))
+        self._ok(self._gather_fn(self.h, self.rank, self.dcode, zs.ZS3_PACK | zs.ZS3_UNPACK, n, ids,
+                                 self.shard.data_ptr(), own, chunks, fullp, None,
+                                 stream if stream is not None else self._stream()))
 
     def pack(self, bi: int, stream=None):
         n, ids, own, chunks, fullp = self._g[bi]
-        self._ok(zs.lib().zs3_gather_coalesced(self.h, self.rank, self.dcode, zs.ZS3_PACK, n, ids,
-                                               self.shard.data_ptr(), own, None, None, None,
-                                               stream if stream is not None else self._stream()))
+        self._ok(self._gather_fn(self.h, self.rank, self.dcode, zs.ZS3_PACK, n, ids, self.shard.data_ptr(), own, None,
+                                 None, None, stream if stream is not None else self._stream()))
 
     def unpack(self, bi: int, stream=None):
         n, ids, own, chunks, fullp = self._g[bi]
-        self._ok(zs.lib().zs3_gather_coalesced(self.h, self.rank, self.dcode, zs.ZS3_UNPACK, n, ids, None, None,
-                                               chunks, fullp, None,
-                                               stream if stream is not None else self._stream()))
+        self._ok(self._gather_fn(self.h, self.rank, self.dcode, zs.ZS3_UNPACK, n, ids, None, None, chunks, fullp, None,
+                                 stream if stream is not None else self._stream()))
 
     def _fanout(self, stream, k):
         """The main stream plus k-1 auxiliary streams that wait for it."""
@@ -408,6 +493,12 @@ class ShardStep:
             return
         main, aux, handles = self._fanout(stream, self.rs_streams)
         for i, (n, ids, grads, send, recv) in enumerate(self._x):
+            if self.reduce_bits == 4:
+                self._ok(lib.zs3_reduce_scatter_coalesced_mx4(
+                    self.h, self.rank, self.dcode, zs.ZS3_PACK | zs.ZS3_REDUCE, n, ids, grads, send, recv,
+                    self.grad.data_ptr(), partials, zs.ZS3_ROUND_STOCHASTIC, self.wire_seed(i),
+                    handles[i % len(handles)]))
+                continue
             self._ok(lib.zs3_reduce_scatter_coalesced(self.h, self.rank, self.dcode, zs.ZS3_PACK | zs.ZS3_REDUCE,
                                                       n, ids, grads, send, recv, self.grad.data_ptr(), partials,
                                                       handles[i % len(handles)]))
@@ -415,6 +506,11 @@ class ShardStep:
             self._ok(lib.zs3_reduce_scatter_local(self.h, self.rank, self.dcode, n, ids, src,
                                                   self.grad.data_ptr(), partials, handles[i % len(handles)]))
         self._join(main, aux)
+
+    def wire_seed(self, bucket: int) -> int:
+        """Seed of a gradient bucket's rounding in the step under way: another
+        one for every rank, step and bucket."""
+        return (self.seed << 32) + ((self.t * self.N + self.rank) << 16) + bucket & (1 << 64) - 1
 
     def repartition(self, stream=None, dst=None):
         """The partition copy ([codex] 3.1): every full parameter's own range
@@ -440,6 +536,11 @@ class ShardStep:
         a = self.adam
         hp = zs.zs3_adam_params(a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, int(t))
         s = stream if stream is not None else self._stream()
+        if self.listed:
+            for tensors in self._lists:
+                self._ok(zs.lib().zs3_adamw_tensors(self.dcode, self.dcode, self.state_bits, tensors.count, tensors,
+                                                    self.scale_ptr, self.flag_ptr, ctypes.byref(hp), self.seed, s))
+            return
         if self.offload:
             cin, cout = (int(x.cuda_stream) for x in self.copy_streams) if self.stage is not None else (None, None)
             for b, e in self.sub_groups:
@@ -463,6 +564,8 @@ class ShardStep:
         self.t += 1
         mark = on_phase or (lambda name: None)
         if trace_pass is not None:
+            if self.gather_bits == 4:
+                raise ValueError("the coordinator's gathers run on the 16-bit wire")
             mark("gather_trace")
             trace_pass.run(stream)
         else:
@@ -496,8 +599,8 @@ class ShardStep:
             target = self.shard if v == self.rank else tmp
             self._ok(lib.zs3_partition(self.h, v, self.dcode, n, ids, ptrs, target.data_ptr(), s))
             for bi, (bn, bids, _, _, _) in enumerate(self._g):
-                self._ok(lib.zs3_gather_coalesced(self.h, v, self.dcode, zs.ZS3_PACK, bn, bids, target.data_ptr(),
-                                                  self.chunk_ptr(bi, v), None, None, None, s))
+                self._ok(self._gather_fn(self.h, v, self.dcode, zs.ZS3_PACK, bn, bids, target.data_ptr(),
+                                         self.chunk_ptr(bi, v), None, None, None, s))
         del tmp
         if self.offload:
             # built in HBM one sub-group at a time, then moved to the pinned host state
@@ -512,9 +615,12 @@ class ShardStep:
             self.exp_avg_sq.zero_()
             return
         for b, e in self.sub_groups:
+            m, v = (None, None) if self.state_bits == 8 else (self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr())
             self._ok(lib.zs3_init_master(self.h, self.rank, self.dcode, b, e, self.shard.data_ptr(),
-                                         self.master.data_ptr(), self.exp_avg.data_ptr(),
-                                         self.exp_avg_sq.data_ptr(), s))
+                                         self.master.data_ptr(), m, v, s))
+        if self.state_bits == 8:
+            self.exp_avg.zero_()
+            self.exp_avg_sq.zero_()
 
     def fill_peer_norms(self):
         """Stand-in for the N-scalar all-reduce of the norm: after one partial
@@ -536,11 +642,20 @@ class ShardStep:
             "grad_norm": 0 if self.fuse_norm else 2 * own,    # fused: no second read of grad_flat
             "adam": 28 * own,
         }
+        if self.gather_bits == 4:               # 17 bytes of wire a block, read or written once a pass
+            blocks = sum(zs.zs3_mx4_sizes(self.h, b)[0] for b in self.gather_buckets)
+            out["pack"] = 2 * (2 * part_real + 17 * blocks)
+            out["unpack"] = 2 * (17 * blocks * (N - 1) + 2 * F)
+        if self.state_bits == 8:                # fp32 master and gradient, shard, 2 codes and 2 / 32 scales each way
+            out["adam"] = 16 * own + own // 8
         if self.reduce_path == "coalesced":
             # send side: read the own full gradients, write N chunks (padding zeros included)
             full_part = sum(p["numel"] for p in self.params if not p["persistent"])
             chunks = sum(C for _, _, C, _, _ in self.coalesced)
-            out["scatter_pack"] = 2 * full_part + 2 * N * chunks
+            out["scatter_pack"] = 2 * full_part + self.xbuf.element_size() * N * chunks
+            if self.reduce_bits == 4:
+                pers = sum(p["numel"] for p in self.params if p["persistent"])
+                out["reduce_scatter"] = N * chunks + 2 * own + 2 * N * pers
         return out
 
     def budget_bytes(self) -> int:

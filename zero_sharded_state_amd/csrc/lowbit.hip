@@ -119,13 +119,17 @@ __device__ __forceinline__ uint32_t random_word(uint32_t x, uint32_t key1) {
 // scalar registers, and loads take a scalar address and a 32-bit offset.
 __device__ __forceinline__ int wave_of(int t) { return __builtin_amdgcn_readfirstlane(t >> 6); }
 
-// The list's tensor that tile b belongs to: each lane compares one prefix
-// and the wave counts them, one load where a search would make six.
+// The list's tensor that tile b belongs to: each lane compares a prefix (two,
+// where a list has more than 64) and the wave counts them, one load where a
+// search would make six.
 template <class PLAN>
 __device__ __forceinline__ int find_tensor(const PLAN& p, int32_t b, int lane) {
+    constexpr int kMost = sizeof(p.first_tile) / sizeof(p.first_tile[0]) - 1;
     if (p.n == 1) return 0;
-    const bool past = lane < p.n && p.first_tile[lane + 1] <= b;
-    return __builtin_amdgcn_readfirstlane(__builtin_popcountll(__ballot(past)));
+    int past = __builtin_popcountll(__ballot(lane < p.n && p.first_tile[lane + 1] <= b));
+    if constexpr (kMost > 64)
+        past += __builtin_popcountll(__ballot(lane + 64 < p.n && p.first_tile[umin(lane + 65, kMost)] <= b));
+    return __builtin_amdgcn_readfirstlane(past);
 }
 
 // --------------------------------------------------- results on their way out

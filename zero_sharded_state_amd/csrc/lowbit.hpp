@@ -17,7 +17,9 @@ constexpr int64_t kMxBlock = 32;           // elements that share a scale byte
 
 // ------------------------------------------------ AdamW over a tensor list
 
-constexpr int kStepTensors = 48;           // tensors of one launch
+// Tensors of one launch.  A launch more costs about 4 us of its ramps, so a
+// plan holds as many as 4 KB of kernel arguments do.
+constexpr int kStepTensors = 56;
 constexpr int kStepRuns = 2;               // runs of 256 elements of a wave
 constexpr int64_t kStepTile = int64_t(kLbBlock) * 4 * kStepRuns;   // elements of a workgroup
 
@@ -38,7 +40,7 @@ struct StepPlan {
     int32_t first_tile[kStepTensors + 1];
     StepTensor t[kStepTensors];
 };
-static_assert(sizeof(StepPlan) <= 3584, "the plan has to fit the kernel arguments");
+static_assert(sizeof(StepPlan) <= 3840, "the plan has to fit the kernel arguments");
 
 struct StepConsts {
     float b1, b2, omb1, omb2, bc1, bc2, eps;
@@ -51,7 +53,7 @@ hipError_t launch_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state
 
 // ------------------------------------------------------ 8-bit moments read
 
-constexpr int kReadTensors = 64;
+constexpr int kReadTensors = 104;
 constexpr int64_t kReadTile = int64_t(kLbBlock) * 16;
 
 struct ReadTensor {
@@ -66,6 +68,7 @@ struct ReadPlan {
     int32_t first_tile[kReadTensors + 1];
     ReadTensor t[kReadTensors];
 };
+static_assert(sizeof(ReadPlan) <= 3840, "the plan has to fit the kernel arguments");
 
 hipError_t launch_moment8_read(bool fp32_out, const ReadPlan& plan, hipStream_t stream);
 

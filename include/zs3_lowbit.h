@@ -3,7 +3,8 @@
  * tensors with states in 32 or in 8 bits, and the coalesced gather and
  * reduce-scatter over a 4-bit wire.  Layouts, status codes, error messages,
  * pointer and stream conventions and the pages' tags are those of zs3.h,
- * which this header includes.
+ * which this header includes.  Device pointers are those of the calling
+ * thread's current device, `stream` one of its streams.
  */
 #ifndef ZS3_LOWBIT_H
 #define ZS3_LOWBIT_H
@@ -18,11 +19,10 @@ enum { ZS3_FP32 = 3 };    /* a type of gradients and of read moments here */
 
 /* ------------------------------------ (1) AdamW over a list of tensors
  * [codex] 6.3 and [llmnex] section 1 as zs3_adam_step, for tensors that lie
- * anywhere:
- * a sub-group's parameters with their own decay (norms and biases without),
- * parameters that are not sharded, or state in 8 bits instead of 32.  One
- * call steps the whole list; each tensor has its own factor of the learning
- * rate and its own decoupled weight decay.
+ * anywhere: a sub-group's parameters with their own decay (norms and biases
+ * without), parameters that are not sharded, or state in 8 bits instead of
+ * 32.  One call steps the whole list; each tensor has its own factor of the
+ * learning rate and its own decoupled weight decay.
  *
  * Per element, with w = master, m = exp_avg, v = exp_avg_sq, lr = hp->lr *
  * lr_scale, wd = weight_decay (hp->weight_decay is not read):
@@ -68,10 +68,12 @@ enum { ZS3_FP32 = 3 };    /* a type of gradients and of read moments here */
  * Pointers are device pointers, aligned to their types (8-bit moments: 16
  * bytes); none that is written may overlap another buffer of the call, so a
  * tensor listed twice is refused.  grad_dtype: ZS3_FP16, ZS3_BF16 or
- * ZS3_FP32.  The call needs 0 <= beta < 1, eps >= 0, and allocates, uploads
- * and keeps nothing: it may be captured into a graph, and calls on
- * different streams with different tensors are independent.  (A captured
- * call replays the step number, learning rate and seed it was captured with.)
+ * ZS3_FP32.  Needs 0 <= beta < 1, eps >= 0 (8-bit states: eps >= 1e-12, since
+ * roots of second moments under fp32's normal range count as 0), at most
+ * 3.4e10 elements a tensor.  The call allocates, uploads and keeps nothing: it
+ * may be captured into a graph, and calls on different streams with different
+ * tensors are independent.  (A captured call replays the step number, learning
+ * rate and seed it was captured with.)
  */
 typedef struct {
     int64_t numel;

@@ -211,6 +211,34 @@ def test_zero_gradients_and_fresh_moments():
     assert np.all(np.abs(c.dw.host()[:500] - decayed[:500]) <= 1.001e-3)         # |update| <= lr at step 1
 
 
+def test_tiny_gradients():
+    """Gradients whose squares leave fp32's normal range, at the smallest eps: the
+    update is m / (sqrt(v) + eps) of the fp32 moments, where a root that counts
+    as 0 is at most 1.1e-19 of 1e-12: 2 of the 11 half-ulps more.  Codes under
+    2^-126 are not pinned; the moments read back finite."""
+    require_gpu()
+    import torch
+    note("adamw8 tiny gradients")
+    rng = np.random.default_rng(14)
+    c = Case(rng, 2048, 0, "bf16", "fp32", 8)
+    g = (rng.standard_normal(2048) * 10.0 ** rng.uniform(-24, -10, 2048)).astype(np.float32)
+    c.g = g
+    c.dg.view.copy_(torch.from_numpy(g))
+    c.dm.view.zero_()
+    c.dv.view.zero_()
+    c.m[:] = 0
+    c.v[:] = 0
+    hp = dict(HP, eps=1e-12, step=1)
+    _step([c], 8, hp=hp)
+    sync()
+    _, m, v, decayed, upd = c.expect(1.0, hp, 0)
+    exact = decayed.astype(np.float64) - upd
+    bound = 2.0 ** -24 * (13 * 1.001 * np.abs(upd) + 1.001 * np.abs(exact)) + 2.0 ** -149
+    assert np.all(np.abs(c.dw.host().astype(np.float64) - exact) <= bound)
+    for buf, second in ((c.dm, False), (c.dv, True)):
+        assert np.isfinite(lb.decode_moment(*lb.split_moment(buf.host(), c.n), second)).all()
+
+
 @pytest.mark.parametrize("bits", [8, 32])
 def test_nonfinite_flag_writes_nothing(bits):
     require_gpu()

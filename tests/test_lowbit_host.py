@@ -76,14 +76,14 @@ int main(void) {
 
 # ------------------------------------------------------------------- AdamW
 
-@pytest.mark.parametrize("n", [0, 1, 31, 32, 33, 511, 512, 513, 4095, 1 << 33])
+@pytest.mark.parametrize("n", [0, 1, 31, 32, 33, 511, 512, 513, 4095, 1 << 33, (1 << 35) - 2048])
 def test_moment_bytes(n):
     assert zs.zs3_moment8_bytes(n) == lb.moment_bytes(n)
 
 
 def test_moment_bytes_refusals():
     _refused(zs.ZS3_EINVAL, "out of range", zs.zs3_moment8_bytes, -1)
-    _refused(zs.ZS3_EINVAL, "out of range", zs.zs3_moment8_bytes, 1 << 62)
+    _refused(zs.ZS3_EINVAL, "out of range", zs.zs3_moment8_bytes, 1 << 36)
     assert zs.lib().zs3_moment8_bytes(1, None) == zs.ZS3_EINVAL
 
 
@@ -107,6 +107,8 @@ def test_adamw_refusals(bits):
         _refused(zs.ZS3_EINVAL, "NULL", _step, [t(**{k: 0})], bits=bits)
     _refused(zs.ZS3_EINVAL, "numel", _step, [t(numel=-1)], bits=bits)
     _refused(zs.ZS3_EINVAL, "numel", _step, [t(numel=1 << 60)], bits=bits)
+    # nothing of a list is launched where a later tensor is refused
+    _refused(zs.ZS3_EINVAL, "tensor 1: numel", _step, [t(), t(at=BASE + (1 << 30), numel=1 << 36)], bits=bits)
     for k, off in (("master", 2), ("grad", 1), ("param", 1)):
         _refused(zs.ZS3_EINVAL, "aligned", _step, [t(**{k: t()[k] + off})], bits=bits)
     _refused(zs.ZS3_EINVAL, "aligned", _step, [t(grad=t()["grad"] + 2)], grad="fp32", bits=bits)
@@ -118,6 +120,8 @@ def test_adamw_refusals(bits):
     for bad in ({"step": 0}, {"beta1": 1.0}, {"beta2": -0.1}, {"beta2": float("nan")}, {"eps": -1.0},
                 {"eps": float("inf")}, {"lr": float("inf")}):
         _refused(zs.ZS3_EINVAL, "", _step, [t()], hp=dict(HP, **bad), bits=bits)
+    if bits == 8:
+        _refused(zs.ZS3_EINVAL, "eps", _step, [t()], hp=dict(HP, eps=1e-13), bits=bits)
     _refused(zs.ZS3_EINVAL, "scale", _step, [t()], scale=BASE + 2, bits=bits)
     _refused(zs.ZS3_EINVAL, "scale", _step, [t()], flag=BASE + 2, bits=bits)
     f = zs.lib().zs3_adamw_tensors
@@ -243,6 +247,15 @@ def test_scatter_refusals(layout):
     _refused(zs.ZS3_EALIAS, "send overlaps", g, layout, send=BASE + (8 << 20) + 64)
     _refused(zs.ZS3_EALIAS, "grad_flat", g, layout, partials=BASE + (3 << 20))
     _refused(zs.ZS3_EALIAS, "send overlaps", g, layout, partials=BASE + 16)
+
+
+def test_partitions_too_large_for_a_launch():
+    h = zs.zs3_layout_create(2, 0, [0, 1], [64, 1 << 37])
+    try:
+        _refused(zs.ZS3_EINVAL, "too large", zs.zs3_mx4_sizes, h, [0, 1])
+        _refused(zs.ZS3_EINVAL, "too large", zs.zs3_gather_coalesced_mx4, h, 0, "bf16", zs.ZS3_PACK, [0, 1], BASE, BASE + (1 << 39), stream=0)
+    finally:
+        zs.zs3_layout_destroy(h)
 
 
 def test_more_ranks_than_pointers_need_even_spacing():

@@ -354,19 +354,20 @@ __device__ __forceinline__ float decode_v(uint32_t c, uint32_t s) {
 }
 __device__ __forceinline__ uint32_t encode_v(float v, uint32_t s, uint32_t word) {
     const uint32_t t = __float_as_uint(__builtin_ldexpf(v, 7 - static_cast<int>(s)));
-    const uint32_t c = (t + ((word & 0xffffu) << 3)) >> 19;
+    const uint32_t c = (t + (word & 0xffffu) * 8u) >> 19;
     return umax(c, umin(__float_as_uint(v), 1u));     // what is not zero never becomes zero
 }
 
 // The new moments and weights of 4 neighbouring elements, `left` of them
-// there; 8 neighbouring lanes hold a block.
+// there (all, where WHOLE); 8 neighbouring lanes hold a block.
 struct Quad8 {
     float w[4];
     uint32_t m, v;          // codes
     uint32_t ms, vs;        // scale bytes
 };
 
-__device__ __forceinline__ void adamw8_quad(Quad8& x, const float (&g)[4], int left, int64_t e, const StepTensor& t,
+template <bool WHOLE>
+__device__ __forceinline__ void adamw8_quad(Quad8& x, const float (&g)[4], int left, uint32_t x0, const StepTensor& t,
                                             const StepConsts& c) {
     const f2 m01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(x.m, scale_of(x.ms), false);
     const f2 m23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(x.m, scale_of(x.ms), true);
@@ -384,13 +385,14 @@ __device__ __forceinline__ void adamw8_quad(Quad8& x, const float (&g)[4], int l
         // added to a weight that is far larger)
         const float den = __builtin_amdgcn_sqrtf(v[q]) * c.rsqrt_bc2 + c.eps;
         x.w[q] = x.w[q] - (t.lr * m[q]) * __builtin_amdgcn_rcpf(den);
-        if (q >= left) m[q] = v[q] = 0.0f;         // padding of the last block
+        if constexpr (!WHOLE) {
+            if (q >= left) m[q] = v[q] = 0.0f;     // padding of the last block
+        }
         mtop = umax(mtop, mag(m[q]));
         vtop = umax(vtop, mag(v[q]));
     }
     x.ms = scale_byte(max8lanes(mtop), kCarryM, 8, 254);
     x.vs = scale_byte(max8lanes(vtop), kCarryV, 8, 254);
-    const uint32_t x0 = weyl(e, t.key0);
     uint32_t word[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) word[q] = random_word(x0 + static_cast<uint32_t>(q) * kWeyl, t.key1);
@@ -406,14 +408,7 @@ __device__ __forceinline__ void adamw8_quad(Quad8& x, const float (&g)[4], int l
     x.v = x.vs == 255u ? 0xffffffffu : vo;
 }
 
-// What a wave reads of its elements.
-template <int G>
-struct Load8 {
-    f4 w[kStepRuns];
-    Grad4<G> g[kStepRuns];
-    uint32_t m[kStepRuns], v[kStepRuns], ms[kStepRuns], vs[kStepRuns];
-};
-
+// A workgroup's results (see above).
 struct Stage8 {
     alignas(16) uint8_t w[stage_bytes(4 * kStepTile)];
     alignas(16) uint8_t p[stage_bytes(2 * kStepTile)];
@@ -421,81 +416,122 @@ struct Stage8 {
     alignas(16) uint8_t v[stage_bytes(kStepTile)];
 };
 
+// A tile's arrays, from its first element on: offsets in it fit 32 bits.
+template <int G>
+struct Tile8 {
+    float* w;
+    const void* g;
+    uint16_t* p;
+    uint8_t *m, *v, *ms, *vs;
+    int n;                      // its elements
+    int wo, po, mo, vo;         // their line offsets
+};
+
+template <int D, int G>
+__device__ __forceinline__ void adamw8_out(const Tile8<G>& a, Stage8& stage, const Quad8& x, uint32_t i) {
+    *reinterpret_cast<f4*>(stage.w + a.wo + 4 * i) = f4{x.w[0], x.w[1], x.w[2], x.w[3]};
+    *reinterpret_cast<u2w*>(stage.p + stage_offset(a.po) + 2 * i) = u2w{narrow2<D>(x.w[0], x.w[1]), narrow2<D>(x.w[2], x.w[3])};
+    *reinterpret_cast<uint32_t*>(stage.m + a.mo + i) = x.m;
+    *reinterpret_cast<uint32_t*>(stage.v + a.vo + i) = x.v;
+}
+
+// A wave's elements i0 .. i0 + 256 * kStepRuns of the tile, all there or not.
+template <int D, int G>
+__device__ __forceinline__ void adamw8_whole(const Tile8<G>& a, uint32_t i0, uint32_t lane, uint32_t x0, float scale,
+                                             const StepTensor& t, const StepConsts& c, Stage8& stage) {
+    f4 W[kStepRuns];
+    Grad4<G> gr[kStepRuns];
+    Quad8 x[kStepRuns];
+#pragma unroll
+    for (int k = 0; k < kStepRuns; ++k) {
+        const uint32_t i = i0 + 256 * k + 4 * lane;
+        W[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(a.w + i));
+        gr[k].load(a.g, i);
+        x[k].m = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(a.m + i));
+        x[k].v = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(a.v + i));
+        x[k].ms = a.ms[i >> 5];
+        x[k].vs = a.vs[i >> 5];
+    }
+#pragma unroll
+    for (int k = 0; k < kStepRuns; ++k) {
+        const uint32_t i = i0 + 256 * k + 4 * lane;
+        float g[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            x[k].w[q] = W[k][q];
+            g[q] = gr[k].get(q) * scale;
+        }
+        adamw8_quad<true>(x[k], g, 4, x0 + (256 * k + 4 * lane) * kWeyl, t, c);
+        adamw8_out<D>(a, stage, x[k], i);
+        if ((lane & 7) == 0) {
+            a.ms[i >> 5] = static_cast<uint8_t>(x[k].ms);
+            a.vs[i >> 5] = static_cast<uint8_t>(x[k].vs);
+        }
+    }
+}
+
+template <int D, int G>
+__device__ __forceinline__ void adamw8_ragged(const Tile8<G>& a, uint32_t i0, uint32_t lane, uint32_t x0, float scale,
+                                              const StepTensor& t, const StepConsts& c, Stage8& stage) {
+    for (int k = 0; k < kStepRuns; ++k) {
+        const uint32_t i = i0 + 256 * k + 4 * lane;
+        int left = a.n - static_cast<int>(i);
+        left = left < 0 ? 0 : left > 4 ? 4 : left;
+        Quad8 x = {};
+        float g[4] = {};
+        if (left > 0) {
+            // codes are padded to whole blocks: the four are there
+            x.m = *reinterpret_cast<const uint32_t*>(a.m + i);
+            x.v = *reinterpret_cast<const uint32_t*>(a.v + i);
+            x.ms = a.ms[i >> 5];
+            x.vs = a.vs[i >> 5];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q < left) {
+                    x.w[q] = a.w[i + q];
+                    g[q] = grad1<G>(a.g, i + q) * scale;
+                }
+            }
+        }
+        adamw8_quad<false>(x, g, left, x0 + (256 * k + 4 * lane) * kWeyl, t, c);
+        adamw8_out<D>(a, stage, x, i);
+        if (left > 0 && (lane & 7) == 0) {
+            a.ms[i >> 5] = static_cast<uint8_t>(x.ms);
+            a.vs[i >> 5] = static_cast<uint8_t>(x.vs);
+        }
+    }
+}
+
 template <int D, int G>
 __device__ __forceinline__ void adamw8_tile(const StepTensor& t, int64_t tile0, int wave, int lane, float scale,
                                             const StepConsts& c, Stage8& stage) {
-    uint8_t* m8 = static_cast<uint8_t*>(t.exp_avg);
-    uint8_t* v8 = static_cast<uint8_t*>(t.exp_avg_sq);
-    const int64_t scales = (t.numel + kMxBlock - 1) / kMxBlock * kMxBlock;
-    const int64_t e0 = tile0 + wave * (256 * kStepRuns);
-    const bool whole = e0 + 256 * kStepRuns <= t.numel;
-    Load8<G> in;
-    if (whole) {
-#pragma unroll
-        for (int k = 0; k < kStepRuns; ++k) {
-            const int64_t e = e0 + 256 * k + 4 * lane;
-            in.w[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(t.master + e));
-            in.g[k].load(t.grad, e);
-            in.m[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(m8 + e));
-            in.v[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(v8 + e));
-            in.ms[k] = m8[scales + (e >> 5)];
-            in.vs[k] = v8[scales + (e >> 5)];
-        }
-    }
-    const int wo = line_offset(t.master + tile0), po = line_offset(t.param + tile0), mo = line_offset(m8 + tile0),
-              vo = line_offset(v8 + tile0);
-    if (e0 < t.numel) {
-#pragma unroll
-        for (int k = 0; k < kStepRuns; ++k) {
-            const int64_t e = e0 + 256 * k + 4 * lane;
-            const int left = whole ? 4 : (t.numel - e >= 4 ? 4 : (t.numel > e ? static_cast<int>(t.numel - e) : 0));
-            Quad8 x = {};
-            float g[4] = {};
-            if (whole) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    x.w[q] = in.w[k][q];
-                    g[q] = in.g[k].get(q) * scale;
-                }
-                x.m = in.m[k];
-                x.v = in.v[k];
-                x.ms = in.ms[k];
-                x.vs = in.vs[k];
-            } else if (left > 0) {
-                // codes are padded to whole blocks: the four are there
-                x.m = *reinterpret_cast<const uint32_t*>(m8 + e);
-                x.v = *reinterpret_cast<const uint32_t*>(v8 + e);
-                x.ms = m8[scales + (e >> 5)];
-                x.vs = v8[scales + (e >> 5)];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q < left) {
-                        x.w[q] = t.master[e + q];
-                        g[q] = grad1<G>(t.grad, e + q) * scale;
-                    }
-                }
-            }
-            adamw8_quad(x, g, left, e, t, c);
-            const int i = static_cast<int>(e - tile0);
-            *reinterpret_cast<f4*>(stage.w + wo + 4 * i) = f4{x.w[0], x.w[1], x.w[2], x.w[3]};
-            *reinterpret_cast<u2w*>(stage.p + stage_offset(po) + 2 * i) = u2w{narrow2<D>(x.w[0], x.w[1]), narrow2<D>(x.w[2], x.w[3])};
-            *reinterpret_cast<uint32_t*>(stage.m + mo + i) = x.m;
-            *reinterpret_cast<uint32_t*>(stage.v + vo + i) = x.v;
-            if (left > 0 && (lane & 7) == 0) {
-                m8[scales + (e >> 5)] = static_cast<uint8_t>(x.ms);
-                v8[scales + (e >> 5)] = static_cast<uint8_t>(x.vs);
-            }
-        }
-    }
-    __syncthreads();
+    const int64_t scales = (t.numel + kMxBlock - 1) / kMxBlock * kMxBlock + tile0 / kMxBlock;
     const int64_t rest = t.numel - tile0;
-    const int n = static_cast<int>(rest > kStepTile ? kStepTile : rest), th = wave * 64 + lane;
-    store_lines<float>(t.master + tile0, stage.w, wo, 4 * n, th, kLbBlock);
-    if (t.param != nullptr)
-        store_lines<uint16_t>(t.param + tile0, stage.p, po, 2 * n, th, kLbBlock);
+    Tile8<G> a;
+    a.w = t.master + tile0;
+    a.g = G == 3 ? static_cast<const void*>(static_cast<const float*>(t.grad) + tile0)
+                 : static_cast<const void*>(static_cast<const uint16_t*>(t.grad) + tile0);
+    a.p = t.param + tile0;
+    a.m = static_cast<uint8_t*>(t.exp_avg) + tile0;
+    a.v = static_cast<uint8_t*>(t.exp_avg_sq) + tile0;
+    a.ms = static_cast<uint8_t*>(t.exp_avg) + scales;
+    a.vs = static_cast<uint8_t*>(t.exp_avg_sq) + scales;
+    a.n = static_cast<int>(rest > kStepTile ? kStepTile : rest);
+    a.wo = line_offset(a.w);
+    a.po = line_offset(a.p);
+    a.mo = line_offset(a.m);
+    a.vo = line_offset(a.v);
+    const int i0 = wave * (256 * kStepRuns);
+    const uint32_t x0 = weyl(tile0 + i0, t.key0);
+    if (i0 + 256 * kStepRuns <= a.n) adamw8_whole<D, G>(a, i0, lane, x0, scale, t, c, stage);
+    else if (i0 < a.n) adamw8_ragged<D, G>(a, i0, lane, x0, scale, t, c, stage);
+    __syncthreads();
+    const int th = wave * 64 + lane;
+    store_lines<float>(a.w, stage.w, a.wo, 4 * a.n, th, kLbBlock);
+    if (t.param != nullptr) store_lines<uint16_t>(a.p, stage.p, a.po, 2 * a.n, th, kLbBlock);
     // half of the threads for each moment
-    if (th < kLbBlock / 2) store_lines<uint8_t>(m8 + tile0, stage.m, mo, n, th, kLbBlock / 2);
-    else store_lines<uint8_t>(v8 + tile0, stage.v, vo, n, th - kLbBlock / 2, kLbBlock / 2);
+    if (th < kLbBlock / 2) store_lines<uint8_t>(a.m, stage.m, a.mo, a.n, th, kLbBlock / 2);
+    else store_lines<uint8_t>(a.v, stage.v, a.vo, a.n, th - kLbBlock / 2, kLbBlock / 2);
 }
 
 template <int D, int G, int BITS, bool STAGED>

@@ -40,8 +40,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int64_t div_up(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
 zs3_status launched(hipError_t e, const char* what) {
-    if (e != hipSuccess) return fail(ZS3_EHIP, "%s: %s", what, hipGetErrorString(e));
-    return ZS3_OK;
+    if (e == hipSuccess) return ZS3_OK;
+    (void)hipGetLastError();          // it is reported here, not to the next call
+    return fail(ZS3_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 // Nothing throws across the ABI: a call's host tables may not fit in memory.
@@ -112,12 +113,12 @@ uint64_t random_keys(uint64_t seed, int64_t step, int64_t id) {
 
 int64_t moment8_size(int64_t numel) { return div_up(33 * div_up(numel, kMxBlock), 16) * 16; }
 
-// The largest number of elements a tensor may have: its bytes, at 4 an
-// element and with room for rounding, have to fit 63 bits.
-constexpr int64_t kMaxNumel = int64_t(1) << 58;
-
 // Tiles of one launch: a grid of 256 threads each has to fit 32 bits.
 constexpr int64_t kMaxTiles = (int64_t(1) << 24) - 1;
+
+// The most elements of a tensor (one launch holds it): 3.4e10.
+constexpr int64_t kMaxNumel = kMaxTiles * kStepTile;
+static_assert(kReadTile >= kStepTile, "a tensor that can be stepped can be read");
 
 zs3_status check_adam_params(const zs3_adam_params* hp) {
     if (hp == nullptr) return fail(ZS3_EINVAL, "hp is NULL");
@@ -145,6 +146,10 @@ zs3_status zs3_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state_bi
         if (n > 0 && tensors == nullptr) return fail(ZS3_EINVAL, "tensors is NULL");
         zs3_status s = check_adam_params(hp);
         if (s != ZS3_OK) return s;
+        // the 8-bit form's root takes second moments under fp32's normal range,
+        // roots under 1.1e-19, as 0: eps has to be so much larger that this
+        // is within its own rounding
+        if (state_bits == 8 && hp->eps < 1e-12) return fail(ZS3_EINVAL, "eps %g < 1e-12 with 8-bit states", hp->eps);
         if ((scale != nullptr && !aligned(scale, 4)) || (nonfinite != nullptr && !aligned(nonfinite, 4)))
             return fail(ZS3_EINVAL, "scale or nonfinite is not 4-byte aligned");
         const int64_t g_bytes = grad_dtype == ZS3_FP32 ? 4 : 2;
@@ -200,7 +205,6 @@ zs3_status zs3_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state_bi
             const zs3_adamw_tensor& t = tensors[i];
             if (t.numel == 0) continue;
             const int64_t tiles = div_up(t.numel, kStepTile);
-            if (tiles > kMaxTiles) return fail(ZS3_EINVAL, "tensor %d: too large for one launch", i);
             if (plan.n == kStepTensors || plan.first_tile[plan.n] + tiles > kMaxTiles) {
                 if ((s = flush()) != ZS3_OK) return s;
             }
@@ -269,7 +273,6 @@ zs3_status zs3_moment8_read(int32_t out_dtype, int32_t n, const zs3_moment8* lis
             const zs3_moment8& m = list[i];
             if (m.numel == 0) continue;
             const int64_t tiles = div_up(m.numel, kReadTile);
-            if (tiles > kMaxTiles) return fail(ZS3_EINVAL, "moment %d: too large for one launch", i);
             if (plan.n == kReadTensors || plan.first_tile[plan.n] + tiles > kMaxTiles) {
                 if ((s = flush()) != ZS3_OK) return s;
             }
@@ -300,6 +303,8 @@ struct Bucket {
     int64_t blocks = 0, chunk_bytes = 0, chunk_numel = 0, full_numel = 0;
 };
 
+static_assert(mx_tile(1) >= kStepTile, "a partition of kMaxNumel elements fits a launch");
+
 // A request's parameters in ascending ds_id, with their places in a chunk
 // (in blocks) and in the gathered buffer (in elements).
 zs3_status resolve(zs3_layout_t L, int32_t n, const int64_t* ds_ids, Bucket* out) {
@@ -323,6 +328,7 @@ zs3_status resolve(zs3_layout_t L, int32_t n, const int64_t* ds_ids, Bucket* out
         Item& it = out->items[i];
         if (i > 0 && out->items[i - 1].ds_id == it.ds_id)
             return fail(ZS3_EDUPID, "ds_id %lld requested twice", (long long)it.ds_id);
+        if (it.ps > kMaxNumel) return fail(ZS3_EINVAL, "ds_id %lld: too large for one launch", (long long)it.ds_id);
         it.block0 = out->blocks;
         it.full0 = out->full_numel;
         out->blocks += div_up(it.ps, kMxBlock);
@@ -394,7 +400,6 @@ zs3_status by_launch(const Bucket& b, MxPlan* plan, TILES tiles_of, FILL fill, L
     plan->blocks = b.blocks;
     for (const Item& it : b.items) {
         const int64_t tiles = tiles_of(it);
-        if (tiles > kMaxTiles) return fail(ZS3_EINVAL, "ds_id %lld: too large for one launch", (long long)it.ds_id);
         if (plan->n == kMxParams || plan->first_tile[plan->n] + tiles > kMaxTiles) {
             if ((s = launch()) != ZS3_OK) return s;
             plan->n = 0;

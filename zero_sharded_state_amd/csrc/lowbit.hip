@@ -575,31 +575,38 @@ __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) 
     T* out = static_cast<T*>(t.out) + tile0;
     const int oo = line_offset(out);
     // 16 codes of a lane: half a block, one 16-byte load
-    const int i = wave * (64 * 16) + 16 * lane;
-    const int64_t e = tile0 + i;
-    u4 C = {0, 0, 0, 0};
-    uint32_t S = 0;
-    if (e < t.numel) {        // codes are padded to whole blocks: the 16 are there
-        C = __builtin_nontemporal_load(reinterpret_cast<const u4*>(t.moment + e));
-        S = t.moment[scales + (e >> 5)];
-    }
-    uint8_t* to = stage + (F32 ? oo : stage_offset(oo)) + sizeof(T) * i;
+    u4 C[kReadVecs];
+    uint32_t S[kReadVecs];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        float x[4];
-        if (t.second != 0) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = decode_v((C[k] >> (8 * q)) & 0xffu, S);
-        } else {
-            const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(C[k], scale_of(S), false);
-            const f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(C[k], scale_of(S), true);
-            x[0] = a.x;
-            x[1] = a.y;
-            x[2] = d.x;
-            x[3] = d.y;
+    for (int k = 0; k < kReadVecs; ++k) {
+        const int64_t e = tile0 + (wave * kReadVecs + k) * 1024 + 16 * lane;
+        C[k] = u4{0, 0, 0, 0};
+        S[k] = 0;
+        if (e < t.numel) {        // codes are padded to whole blocks: the 16 are there
+            C[k] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(t.moment + e));
+            S[k] = t.moment[scales + (e >> 5)];
         }
-        if constexpr (F32) reinterpret_cast<f4*>(to)[k] = f4{x[0], x[1], x[2], x[3]};
-        else reinterpret_cast<u2w*>(to)[k] = u2w{narrow2<kBF16>(x[0], x[1]), narrow2<kBF16>(x[2], x[3])};
+    }
+#pragma unroll
+    for (int k = 0; k < kReadVecs; ++k) {
+        uint8_t* to = stage + (F32 ? oo : stage_offset(oo)) + sizeof(T) * ((wave * kReadVecs + k) * 1024 + 16 * lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x[4];
+            if (t.second != 0) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = decode_v((C[k][j] >> (8 * q)) & 0xffu, S[k]);
+            } else {
+                const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(C[k][j], scale_of(S[k]), false);
+                const f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(C[k][j], scale_of(S[k]), true);
+                x[0] = a.x;
+                x[1] = a.y;
+                x[2] = d.x;
+                x[3] = d.y;
+            }
+            if constexpr (F32) reinterpret_cast<f4*>(to)[j] = f4{x[0], x[1], x[2], x[3]};
+            else reinterpret_cast<u2w*>(to)[j] = u2w{narrow2<kBF16>(x[0], x[1]), narrow2<kBF16>(x[2], x[3])};
+        }
     }
     __syncthreads();
     const int64_t rest = t.numel - tile0;

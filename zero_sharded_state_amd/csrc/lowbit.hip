@@ -121,7 +121,8 @@ __device__ __forceinline__ int wave_of(int t) { return __builtin_amdgcn_readfirs
 
 // The list's tensor that tile b belongs to: each lane compares a prefix (two,
 // where a list has more than 64) and the wave counts them, one load where a
-// search would make six.
+// search would make six.  (Counting with scalar compares on scalar loads
+// instead: 310 -> 338 us on 1500 tensors of 33,555, 137.5 -> 140.8 on 48 large ones.)
 template <class PLAN>
 __device__ __forceinline__ int find_tensor(const PLAN& p, int32_t b, int lane) {
     constexpr int kMost = sizeof(p.first_tile) / sizeof(p.first_tile[0]) - 1;
@@ -154,6 +155,10 @@ __device__ __forceinline__ int stage_offset(int off) { return off + (off & 2); }
 // Room for an array of n bytes.
 constexpr int stage_bytes(int64_t n) { return static_cast<int>(n) + kLine + 32; }
 
+// The unsigned integer of that many bytes.
+template <int N>
+using bits_of = std::conditional_t<N == 1, uint8_t, std::conditional_t<N == 2, uint16_t, uint32_t>>;
+
 // Stores an array of `len` bytes from LDS to `to`, whose address modulo 128 is
 // `off`, in 16-byte chunks, by threads t, t + step, ...; the chunks at the ends
 // by elements of T.
@@ -162,18 +167,21 @@ __device__ __forceinline__ void store_lines(void* to, const uint8_t* lds, int of
     uint8_t* base = static_cast<uint8_t*>(to) - off;
     const bool shifted = sizeof(T) == 2 && (off & 2) != 0;
     for (int c = 16 * t; c < off + len; c += 16 * step) {
+        u4 x = *reinterpret_cast<const u4*>(lds + c);
+        if (shifted) {
+            const uint32_t y = *reinterpret_cast<const uint32_t*>(lds + c + 16);
+            x = u4{__builtin_amdgcn_alignbyte(x[1], x[0], 2), __builtin_amdgcn_alignbyte(x[2], x[1], 2),
+                   __builtin_amdgcn_alignbyte(x[3], x[2], 2), __builtin_amdgcn_alignbyte(y, x[3], 2)};
+        }
         if (c >= off && c + 16 <= off + len) {
-            u4 x = *reinterpret_cast<const u4*>(lds + c);
-            if (shifted) {
-                const uint32_t y = *reinterpret_cast<const uint32_t*>(lds + c + 16);
-                x = u4{__builtin_amdgcn_alignbyte(x[1], x[0], 2), __builtin_amdgcn_alignbyte(x[2], x[1], 2),
-                       __builtin_amdgcn_alignbyte(x[3], x[2], 2), __builtin_amdgcn_alignbyte(y, x[3], 2)};
-            }
             __builtin_nontemporal_store(x, reinterpret_cast<u4*>(base + c));
         } else {
-            const uint8_t* from = lds + (shifted ? 2 : 0);
-            for (int i = c; i < c + 16; i += static_cast<int>(sizeof(T)))
-                if (i >= off && i < off + len) *reinterpret_cast<T*>(base + i) = *reinterpret_cast<const T*>(from + i);
+            constexpr int kSize = static_cast<int>(sizeof(T));
+#pragma unroll
+            for (int i = 0; i < 16; i += kSize)
+                if (c + i >= off && c + i < off + len)
+                    *reinterpret_cast<T*>(base + c + i) =
+                        __builtin_bit_cast(T, static_cast<bits_of<kSize>>(x[i / 4] >> (8 * (i % 4))));
         }
     }
 }
@@ -183,6 +191,11 @@ __device__ __forceinline__ void store_lines(void* to, const uint8_t* lds, int of
 //   g = grad * scale;  w -= (lr*wd) * w;  m = b1*m + (1-b1)*g;
 //   v = b2*v + (1-b2)*(g*g);
 //   w -= lr * ((m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps));  param = round16(w)
+// Bound by HBM: 12 + 2 bytes read and 14 written an element with 16-bit
+// gradients.  A wave takes 2 runs of 256 elements, a lane 4 neighbours of each,
+// so that every instruction covers whole lines; two workgroups a CU, as many
+// streams at once as HBM takes well.  Measured: 112 tensors of 124M elements
+// 580 us (6.0 TB/s, 97% of the rate of a large copy).
 
 template <int G>
 struct Grad4 {
@@ -343,6 +356,13 @@ __device__ __forceinline__ void adamw32_staged(const StepTensor& t, int64_t tile
 // stochastically, since a mean that moves by a thousandth of itself a step
 // would stand still when rounded to the nearest of 8 or 16 values a binade.
 // The update itself uses the new moments before they are rounded.
+//
+// 16.1 bytes an element with 16-bit gradients.  HBM bounds it, the vector unit
+// (58 instructions an element, 12 of them the random word) is busy two thirds
+// of the time beside it; all workgroups that fit are resident (five a CU
+// instead of eight: 147 -> 160 us on the unaligned set below).  Measured: 48
+// tensors of 1.05M, bf16 gradients, 137 us (5.9 TB/s, 96% of a large copy),
+// at odd elements 146 (90%: a wave's reads touch a line more an array and run).
 
 constexpr uint32_t kCarryM = 0x1fffffu;    // mantissas past 1.75 (448 = 1.75 * 2^8)
 constexpr uint32_t kCarryV = 0x07ffffu;    // mantissas past 1.9375 (496 = 1.9375 * 2^8)
@@ -473,31 +493,48 @@ __device__ __forceinline__ void adamw8_whole(const Tile8<G>& a, uint32_t i0, uin
 template <int D, int G>
 __device__ __forceinline__ void adamw8_ragged(const Tile8<G>& a, uint32_t i0, uint32_t lane, uint32_t x0, float scale,
                                               const StepTensor& t, const StepConsts& c, Stage8& stage) {
+    Quad8 x[kStepRuns] = {};
+    float g[kStepRuns][4] = {};
+    int left[kStepRuns];
+#pragma unroll
     for (int k = 0; k < kStepRuns; ++k) {
         const uint32_t i = i0 + 256 * k + 4 * lane;
-        int left = a.n - static_cast<int>(i);
-        left = left < 0 ? 0 : left > 4 ? 4 : left;
-        Quad8 x = {};
-        float g[4] = {};
-        if (left > 0) {
+        const int rest = a.n - static_cast<int>(i);
+        left[k] = rest < 0 ? 0 : rest > 4 ? 4 : rest;
+        if (left[k] > 0) {
             // codes are padded to whole blocks: the four are there
-            x.m = *reinterpret_cast<const uint32_t*>(a.m + i);
-            x.v = *reinterpret_cast<const uint32_t*>(a.v + i);
-            x.ms = a.ms[i >> 5];
-            x.vs = a.vs[i >> 5];
+            x[k].m = *reinterpret_cast<const uint32_t*>(a.m + i);
+            x[k].v = *reinterpret_cast<const uint32_t*>(a.v + i);
+            x[k].ms = a.ms[i >> 5];
+            x[k].vs = a.vs[i >> 5];
+        }
+        if (left[k] == 4) {
+            const f4 w = *reinterpret_cast<const f4*>(a.w + i);
+            Grad4<G> gr;
+            gr.load(a.g, i);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (q < left) {
-                    x.w[q] = a.w[i + q];
-                    g[q] = grad1<G>(a.g, i + q) * scale;
+                x[k].w[q] = w[q];
+                g[k][q] = gr.get(q) * scale;
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                if (q < left[k]) {
+                    x[k].w[q] = a.w[i + q];
+                    g[k][q] = grad1<G>(a.g, i + q) * scale;
                 }
             }
         }
-        adamw8_quad<false>(x, g, left, x0 + (256 * k + 4 * lane) * kWeyl, t, c);
-        adamw8_out<D>(a, stage, x, i);
-        if (left > 0 && (lane & 7) == 0) {
-            a.ms[i >> 5] = static_cast<uint8_t>(x.ms);
-            a.vs[i >> 5] = static_cast<uint8_t>(x.vs);
+    }
+#pragma unroll
+    for (int k = 0; k < kStepRuns; ++k) {
+        const uint32_t i = i0 + 256 * k + 4 * lane;
+        adamw8_quad<false>(x[k], g[k], left[k], x0 + (256 * k + 4 * lane) * kWeyl, t, c);
+        adamw8_out<D>(a, stage, x[k], i);
+        if (left[k] > 0 && (lane & 7) == 0) {
+            a.ms[i >> 5] = static_cast<uint8_t>(x[k].ms);
+            a.vs[i >> 5] = static_cast<uint8_t>(x[k].vs);
         }
     }
 }
@@ -561,6 +598,7 @@ __global__ __launch_bounds__(kLbBlock) void k_adamw(const StepPlan plan, const S
 
 // ------------------------------------------------------ 8-bit moments read
 // 1 + 1/32 bytes in, 2 or 4 out an element; both codes are exact in bf16.
+// Bound by HBM: 96 moments of 1.05M to bf16 51.2 us (6.0 TB/s), unaligned 53.4.
 
 template <bool F32>
 __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) {
@@ -796,6 +834,10 @@ __device__ __forceinline__ void mx_widen(const MxWork& w, const uint8_t* codes, 
     store_lines<uint16_t>(out, stage, oo, 2 * w.real, t, kLbBlock);
 }
 
+// Bound by HBM's writes: 2 bytes written and 17/32 read an element of the full
+// parameters.  Measured: 58.7M elements over 8 ranks 24.8 us (6.6 TB/s, some of
+// it from the last-level cache), 84M ragged ones over 64 ranks 34.3 us (6.3).
+//
 // Tile x of a parameter's partition, rank y: the own rank's part is quantised
 // from the shard into the own chunk (pack) and written, as the values that
 // the codes stand for, into the parameter's view like every other rank's
@@ -821,7 +863,11 @@ __global__ __launch_bounds__(kLbBlock) void k_mx4_gather(const MxPlan plan) {
     }
 }
 
-// Tile x of a parameter's partition for destination y.
+// Tile x of a parameter's partition for destination y.  2 bytes read and 17/32
+// written an element.  Measured: 42M elements for 8 owners 20.0 us to the
+// nearest (5.3 TB/s) and 22.6 stochastically (4.7): the random words (16
+// instructions a pair of elements, 8 issue slots of them the two multiplies)
+// bring the vector unit to 70%, and the kernel's start is 3 us of either.
 template <int D, bool SR>
 __global__ __launch_bounds__(kLbBlock) void k_mx4_send(const MxPlan plan, uint32_t key0, uint32_t key1) {
     const int t = threadIdx.x;
@@ -839,6 +885,9 @@ __global__ __launch_bounds__(kLbBlock) void k_mx4_send(const MxPlan plan, uint32
 // The owner's average of N received chunks: fp32 sums in rank order from +0,
 // one fp32 division, rounded to 16 bits; padding positions 0.  A wave has
 // VECS runs of 512 elements; a norm slot's 1024 are one wave's, or two waves'.
+// N * 17/32 bytes read and 2 written an own element.  Measured: 8 chunks, 22M
+// own elements, 23.7 us (5.8 TB/s); 64 ragged ones, 2.4M, 19.2 us (4.4): 5 us
+// of that are the launch's start and the first of the 8 rounds of loads.
 template <int VECS>
 struct MxAcc {
     float sum[VECS][8];

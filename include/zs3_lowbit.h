@@ -138,7 +138,8 @@ ZS3_API zs3_status zs3_moment8_read(int32_t out_dtype, int32_t n, const zs3_mome
  * goes to one of the two neighbouring codes with a probability that keeps
  * its expected value (small gradients then survive on average).  Either
  * way e is at least -126 and at most 13 (fp16) or 125 (bf16), where 6 * 2^e
- * is still finite; larger magnitudes are held at 6 * 2^e.
+ * is still finite; larger magnitudes are held at 6 * 2^e.  (bf16 values under
+ * 2^-126 may count as 0.)
  *
  * zs3_gather_coalesced_mx4, as zs3_gather_coalesced:
  *   mode & ZS3_PACK: own_chunk = the rank's partitions of shard_flat, rounded

@@ -243,7 +243,10 @@ def _i64s(vals: Sequence[int]):
 
 
 def _ptrs(vals: Sequence) -> ctypes.Array:
-    return (ctypes.c_void_p * max(1, len(vals)))(*[_ptr(v) for v in vals])
+    try:
+        return (ctypes.c_void_p * max(1, len(vals)))(*vals)       # plain addresses
+    except TypeError:
+        return (ctypes.c_void_p * max(1, len(vals)))(*[_ptr(v) for v in vals])
 
 
 def _dtype(d) -> int:

@@ -357,6 +357,53 @@ def test_many_parameters_in_a_bucket():
         assert np.array_equal(flat.host(), want)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_gather_past_the_last_level_cache(dtype):
+    """A bucket of more than 256 MB, which is cut into other tiles: the values,
+    and the own chunk, of calls that take its parameters one at a time."""
+    require_gpu()
+    import torch
+    note(f"mx4 gather of 2^27 + elements {dtype}")
+    world, rank = 3, 1
+    sizes = [(1 << 26) + 5, 1, 8193, 3 * 8192, 3 * 8192 - 31, (1 << 26) + 4099]
+    t = getattr(torch, {"fp16": "float16", "bf16": "bfloat16"}[dtype])
+    with Set(world, sizes, dtype, seed=51) as st:
+        ids = st.wire_ids
+        gen = torch.Generator("cuda").manual_seed(5)
+        shards = [(torch.randn(st.L.shard_numel, device="cuda", generator=gen) * 0.02).to(t) for _ in range(world)]
+
+        def chunks_of(some):
+            _, size = zs.zs3_mx4_sizes(st.h, some)
+            wire = torch.zeros(world * size, dtype=torch.uint8, device="cuda")
+            ptrs = [wire.data_ptr() + v * size for v in range(world)]
+            for v in range(world):
+                zs.zs3_gather_coalesced_mx4(st.h, v, dtype, PACK, some, shards[v], ptrs[v])
+            return wire, ptrs
+
+        one = {}
+        for p in st.L.params:
+            wire, ptrs = chunks_of([p.ds_id])
+            one[p.ds_id] = torch.empty(p.numel, dtype=t, device="cuda")
+            zs.zs3_gather_coalesced_mx4(st.h, rank, dtype, UNPACK, [p.ds_id], rank_chunks=ptrs, full_flat=one[p.ds_id])
+        wire, ptrs = chunks_of(ids)
+        packed = wire.clone()
+        for fused in (False, True):
+            out = torch.full((sum(sizes) + 64,), 7.0, dtype=t, device="cuda")
+            if fused:
+                wire.view(world, -1)[rank].zero_()
+                zs.zs3_gather_coalesced_mx4(st.h, rank, dtype, PACK | UNPACK, ids, shards[rank], ptrs[rank], ptrs, out)
+            else:
+                zs.zs3_gather_coalesced_mx4(st.h, rank, dtype, UNPACK, ids, rank_chunks=ptrs, full_flat=out)
+            sync()
+            assert torch.equal(wire, packed)
+            at = 0
+            for d in ids:
+                n = one[d].numel()
+                assert torch.equal(out[at:at + n].view(torch.int16), one[d].view(torch.int16)), (d, fused)
+                at += n
+            assert bool((out[at:] == 7.0).all())
+
+
 def test_captured_and_replayed():
     """Pack, unpack, send and reduce captured at their first call; every replay,
     with eager work between, gives the eager result of its inputs."""

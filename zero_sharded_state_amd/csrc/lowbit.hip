@@ -842,24 +842,24 @@ __device__ __forceinline__ void mx_widen(const MxWork& w, const uint8_t* codes, 
 // from the shard into the own chunk (pack) and written, as the values that
 // the codes stand for, into the parameter's view like every other rank's
 // (unpack), so that all ranks see the same parameters.
-template <int D, int MODE>
+template <int D, int MODE, int VECS>
 __global__ __launch_bounds__(kLbBlock) void k_mx4_gather(const MxPlan plan) {
     const int t = threadIdx.x;
-    constexpr int kTile = static_cast<int>(mx_tile(kMxGatherVecs));
-    const MxWork w = mx_work<kMxGatherVecs>(plan, t & 63);
+    constexpr int kTile = static_cast<int>(mx_tile(VECS));
+    const MxWork w = mx_work<VECS>(plan, t & 63);
     uint16_t* out = w.p.dst + w.v * w.p.ps + w.tile0;
     const int64_t codes = 16 * w.p.block0 + w.tile0 / 2, scales = 16 * plan.blocks + w.p.block0 + w.tile0 / 32;
     constexpr bool kOut = (MODE & kMxUnpack) != 0;
     if ((MODE & kMxPack) != 0 && w.v == plan.rank) {
         uint8_t* c = plan.own + codes;
         uint8_t* s = plan.own + scales;
-        if (w.real == kTile) mx_quantise<D, false, kOut, true, kMxGatherVecs>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
-        else mx_quantise<D, false, kOut, false, kMxGatherVecs>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
+        if (w.real == kTile) mx_quantise<D, false, kOut, true, VECS>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
+        else mx_quantise<D, false, kOut, false, VECS>(w, w.p.src + w.tile0, c, s, out, 0, 0, 0, t);
     } else if constexpr (kOut) {
         __shared__ alignas(16) uint8_t stage[stage_bytes(2 * kTile)];
         const uint8_t* chunk = chunk_of(plan, w.v);
-        if (w.real == kTile) mx_widen<D, true, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, stage, t);
-        else mx_widen<D, false, kMxGatherVecs>(w, chunk + codes, chunk + scales, out, stage, t);
+        if (w.real == kTile) mx_widen<D, true, VECS>(w, chunk + codes, chunk + scales, out, stage, t);
+        else mx_widen<D, false, VECS>(w, chunk + codes, chunk + scales, out, stage, t);
     }
 }
 
@@ -1071,16 +1071,20 @@ hipError_t launch_moment8_read(bool fp32_out, const ReadPlan& plan, hipStream_t 
 }
 
 template <int D>
-static hipError_t mx4_gather_launch(int32_t mode, dim3 g, const MxPlan& plan, hipStream_t stream) {
-    if (mode == kMxPack) return launch(k_mx4_gather<D, kMxPack>, g, 0, stream, plan);
-    if (mode == kMxUnpack) return launch(k_mx4_gather<D, kMxUnpack>, g, 0, stream, plan);
-    return launch(k_mx4_gather<D, kMxPack | kMxUnpack>, g, 0, stream, plan);
+static hipError_t mx4_gather_launch(int32_t mode, bool large, dim3 g, const MxPlan& plan, hipStream_t stream) {
+    constexpr int kBoth = kMxPack | kMxUnpack, kSmall = mx_gather_vecs(false), kLarge = mx_gather_vecs(true);
+    if (mode == kMxPack) return launch(k_mx4_gather<D, kMxPack, kSmall>, g, 0, stream, plan);
+    if (mode == kMxUnpack)
+        return launch(large ? k_mx4_gather<D, kMxUnpack, kLarge> : k_mx4_gather<D, kMxUnpack, kSmall>, g, 0, stream, plan);
+    return launch(large ? k_mx4_gather<D, kBoth, kLarge> : k_mx4_gather<D, kBoth, kSmall>, g, 0, stream, plan);
 }
 
-hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, const MxPlan& plan, int32_t n_ranks, hipStream_t stream) {
+hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, bool large, const MxPlan& plan, int32_t n_ranks,
+                             hipStream_t stream) {
     if (plan.n <= 0 || n_ranks <= 0) return hipSuccess;
     const dim3 g(static_cast<uint32_t>(plan.first_tile[plan.n]), static_cast<uint32_t>(n_ranks));
-    return dtype == kFP16 ? mx4_gather_launch<kFP16>(mode, g, plan, stream) : mx4_gather_launch<kBF16>(mode, g, plan, stream);
+    return dtype == kFP16 ? mx4_gather_launch<kFP16>(mode, large, g, plan, stream)
+                          : mx4_gather_launch<kBF16>(mode, large, g, plan, stream);
 }
 
 hipError_t launch_mx4_send(int32_t dtype, bool stochastic, uint32_t key0, uint32_t key1, const MxPlan& plan,

@@ -79,11 +79,17 @@ hipError_t launch_moment8_read(bool fp32_out, const ReadPlan& plan, hipStream_t 
 
 constexpr int kMxParams = 24;              // parameters of one launch
 constexpr int kMxRanks = 256;              // chunk pointers of one launch
-// Groups of 8 elements of a thread.  The gather is short of stores in flight
-// and has N partitions to cut into tiles: two groups ran 30.2 us where four
-// took 32.5 on 84M elements over 64 ranks (equal over 8); the send waits for
-// its loads: four took 22.9 us where two took 23.7 on 42M over 8.
-constexpr int kMxGatherVecs = 2;
+// Groups of 8 elements of a thread.  The gather takes two while its results
+// stay in the last-level cache, since it has N partitions to cut into tiles
+// (84M elements over 64 ranks 30.2 us where four groups took 32.5, 29M of 16
+// parameters 13.6 where four took 15.1; equal over 8), and four where it writes
+// more than that cache holds and the search for a workgroup's parameter no
+// longer hides behind the stores: 235M elements of 4 parameters over 8 ranks
+// 105 us against 121, over 64 ranks 100 against 115 (a single parameter, which
+// needs no search, within 3% either way).  The send waits for its loads: four
+// took 22.9 us where two took 23.7 on 42M over 8.
+constexpr int64_t kMxCached = int64_t(1) << 28;   // bytes of the last-level cache
+constexpr int mx_gather_vecs(bool large) { return large ? 4 : 2; }
 constexpr int kMxSendVecs = 4;
 constexpr int64_t mx_tile(int vecs) { return int64_t(kLbBlock) * 8 * vecs; }
 
@@ -126,7 +132,9 @@ static_assert(sizeof(MxPlan) <= 3584, "the plan has to fit the kernel arguments"
 enum MxMode : int32_t { kMxPack = 1, kMxUnpack = 2 };
 
 // ranks [v0, v0 + n_ranks): pack (the own rank's chunk) and/or unpack.
-hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, const MxPlan& plan, int32_t n_ranks, hipStream_t stream);
+// `large`: the tiles of mx_gather_vecs(true); never with kMxPack alone.
+hipError_t launch_mx4_gather(int32_t dtype, int32_t mode, bool large, const MxPlan& plan, int32_t n_ranks,
+                             hipStream_t stream);
 // destinations [v0, v0 + n_ranks): quantise every destination's partitions.
 hipError_t launch_mx4_send(int32_t dtype, bool stochastic, uint32_t key0, uint32_t key1, const MxPlan& plan,
                            int32_t n_ranks, hipStream_t stream);

@@ -480,6 +480,7 @@ zs3_status zs3_gather_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_t dtype,
         const Chunks chunks = unpack ? Chunks(rank_chunks, b.world, pack ? rank : -1) : none;
         const int32_t step = unpack ? ranks_at_once(chunks) : 1;
         const int32_t first = unpack ? 0 : rank, last = unpack ? b.world : rank + 1;
+        const bool large = unpack && 2 * b.full_numel > kMxCached;
         for (int32_t v0 = first; v0 < last; v0 += step) {
             const int32_t count = std::min(step, last - v0);
             if (unpack) {
@@ -490,14 +491,14 @@ zs3_status zs3_gather_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_t dtype,
                 plan.stride = 0;
             }
             s = by_launch(
-                b, &plan, [](const Item& it) { return div_up(it.ps, mx_tile(kMxGatherVecs)); },
+                b, &plan, [=](const Item& it) { return div_up(it.ps, mx_tile(mx_gather_vecs(large))); },
                 [&](const Item& it, MxParam* p) {
                     p->src = pack ? static_cast<const uint16_t*>(shard_flat) + it.offset : nullptr;
                     p->dst = unpack ? static_cast<uint16_t*>(full_flat) + it.full0 : nullptr;
                 },
                 [&]() {
-                    return launched(launch_mx4_gather(dtype, (pack ? kMxPack : 0) | (unpack ? kMxUnpack : 0), plan, count,
-                                                      static_cast<hipStream_t>(stream)), "4-bit gather kernel launch");
+                    return launched(launch_mx4_gather(dtype, (pack ? kMxPack : 0) | (unpack ? kMxUnpack : 0), large, plan,
+                                                      count, static_cast<hipStream_t>(stream)), "4-bit gather kernel launch");
                 });
             if (s != ZS3_OK) return s;
         }

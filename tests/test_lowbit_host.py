@@ -270,3 +270,50 @@ def test_more_ranks_than_pointers_need_even_spacing():
         assert e.value.status == zs.ZS3_EINVAL and "evenly" in e.value.message
     finally:
         zs.zs3_layout_destroy(h)
+
+
+def test_types_of_the_16_bit_calls_are_what_they_were():
+    """fp32 names a type of gradients and read moments only."""
+    assert zs.DTYPES == {"fp16": zs.ZS3_FP16, "bf16": zs.ZS3_BF16}
+    h = zs.zs3_layout_create(2, 0, [0], [64])
+    try:
+        with pytest.raises(KeyError):
+            zs.zs3_init_master(h, 0, "fp32", 0, 32, 4096, 8192, stream=0)
+    finally:
+        zs.zs3_layout_destroy(h)
+
+
+def test_lists_made_without_the_helpers():
+    """A plain array of the structures counts its own entries."""
+    for arr, call in (((zs.zs3_adamw_tensor * 3)(), lambda a: zs.zs3_adamw_tensors("bf16", "fp32", 8, a, None, None,
+                                                                                  dict(HP, step=1), stream=0)),
+                      ((zs.zs3_moment8 * 3)(), lambda a: zs.zs3_moment8_read("fp32", a, stream=0))):
+        if isinstance(arr[0], zs.zs3_moment8):
+            for x in arr:
+                x.kind = zs.ZS3_EXP_AVG
+        call(arr)                      # numel 0: skipped
+        arr[2].numel = 5
+        _refused(zs.ZS3_EINVAL, " 2: ", call, arr)
+
+
+def _host_step(**k):
+    from zero_sharded_state_amd.shard_step import ShardStep
+    return ShardStep(world_size=2, rank=0, threshold=0, ds_ids=[0, 1], numels=[64, 65], dtype="bf16", prefetch_bucket_size=1000,
+                     reduce_bucket_size=1000, sub_group_size=1000, device="cpu", **k)
+
+
+def test_shard_step_takes_no_decay_from_any_iterable():
+    for names in ([1], (1,), {1}, (d for d in [1])):
+        st = _host_step(no_decay=names)
+        assert st.no_decay == {1} and st.listed
+        st.destroy()
+    with pytest.raises(ValueError, match="not there"):
+        _host_step(no_decay=(d for d in [7]))
+
+
+def test_a_refused_step_does_not_count():
+    st = _host_step(gather_bits=4)
+    with pytest.raises(ValueError, match="16-bit wire"):
+        st.step(trace_pass=object())
+    assert st.t == 0
+    st.destroy()

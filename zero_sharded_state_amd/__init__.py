@@ -43,7 +43,8 @@ ZS3_GATHER_CURRENT, ZS3_GATHER_PREFETCH = 0, 1
 ZS3_EXP_AVG, ZS3_EXP_AVG_SQ = 1, 2
 ZS3_ROUND_NEAREST, ZS3_ROUND_STOCHASTIC = 0, 1
 
-DTYPES = {"fp16": ZS3_FP16, "bf16": ZS3_BF16, "fp32": ZS3_FP32}
+DTYPES = {"fp16": ZS3_FP16, "bf16": ZS3_BF16}
+_DTYPES_LOWBIT = dict(DTYPES, fp32=ZS3_FP32)        # gradients and read moments there
 
 # Every exported symbol of include/zs3.h.
 EXPORTS = (
@@ -251,6 +252,10 @@ def _ptrs(vals: Sequence) -> ctypes.Array:
 
 def _dtype(d) -> int:
     return DTYPES[d] if isinstance(d, str) else int(d)
+
+
+def _dtype_lowbit(d) -> int:
+    return _DTYPES_LOWBIT[d] if isinstance(d, str) else int(d)
 
 
 def _hp(hp) -> zs3_adam_params:
@@ -484,7 +489,8 @@ def zs3_adamw_tensors(dtype, grad_dtype, state_bits: int, tensors, scale, nonfin
     """``tensors``: what ``zs3_adamw_tensor_list`` gives, or the dicts."""
     arr = tensors if isinstance(tensors, ctypes.Array) else zs3_adamw_tensor_list(tensors)
     p = _hp(hp)
-    _check(lib().zs3_adamw_tensors(_dtype(dtype), _dtype(grad_dtype), int(state_bits), arr.count, arr, _ptr(scale),
+    _check(lib().zs3_adamw_tensors(_dtype_lowbit(dtype), _dtype_lowbit(grad_dtype), int(state_bits),
+                                   getattr(arr, "count", len(arr)), arr, _ptr(scale),
                                    _ptr(nonfinite), ctypes.byref(p), int(seed), _stream(stream)))
 
 
@@ -507,7 +513,7 @@ def zs3_moment8_list(moments: Sequence[dict]) -> ctypes.Array:
 def zs3_moment8_read(out_dtype, moments, stream=None) -> None:
     """``moments``: what ``zs3_moment8_list`` gives, or the dicts."""
     arr = moments if isinstance(moments, ctypes.Array) else zs3_moment8_list(moments)
-    _check(lib().zs3_moment8_read(_dtype(out_dtype), arr.count, arr, _stream(stream)))
+    _check(lib().zs3_moment8_read(_dtype_lowbit(out_dtype), getattr(arr, "count", len(arr)), arr, _stream(stream)))
 
 
 # ------------------------------------------------------------ the 4-bit wire
@@ -525,8 +531,9 @@ def zs3_gather_coalesced_mx4(layout: int, rank: int, dtype, mode: int, ds_ids: S
     n = len(ds_ids)
     offs = (ctypes.c_int64 * max(1, n))()
     chunks = _ptrs(rank_chunks) if rank_chunks is not None else None
-    _check(lib().zs3_gather_coalesced_mx4(layout, rank, _dtype(dtype), mode, n, _i64s(ds_ids), _ptr(shard_flat),
-                                          _ptr(own_chunk), chunks, _ptr(full_flat), offs, _stream(stream)))
+    _check(lib().zs3_gather_coalesced_mx4(layout, rank, _dtype_lowbit(dtype), mode, n, _i64s(ds_ids),
+                                          _ptr(shard_flat), _ptr(own_chunk), chunks, _ptr(full_flat), offs,
+                                          _stream(stream)))
     return list(offs[:n])
 
 
@@ -536,8 +543,8 @@ def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, d
                                      rounding: int = ZS3_ROUND_NEAREST, seed: int = 0, stream=None) -> None:
     g = _ptrs(grads) if grads is not None else None
     r = _ptrs(recv_chunks) if recv_chunks is not None else None
-    _check(lib().zs3_reduce_scatter_coalesced_mx4(layout, rank, _dtype(dtype), mode, len(ds_ids), _i64s(ds_ids), g,
-                                                  _ptr(send), r, _ptr(grad_flat), _ptr(partials), int(rounding),
+    _check(lib().zs3_reduce_scatter_coalesced_mx4(layout, rank, _dtype_lowbit(dtype), mode, len(ds_ids), _i64s(ds_ids),
+                                                  g, _ptr(send), r, _ptr(grad_flat), _ptr(partials), int(rounding),
                                                   int(seed), _stream(stream)))
 
 

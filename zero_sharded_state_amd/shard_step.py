@@ -76,14 +76,15 @@ class ShardStep:
         if reduce_bits == 4 and reduce_path != "coalesced":
             raise ValueError("a 4-bit gradient wire needs the coalesced gradient path")
         # the list step holds for 8-bit moments and for a decay by parameter
+        no_decay = frozenset(no_decay)
         self.listed = state_bits == 8 or bool(no_decay)
         if self.listed and offload:
             raise ValueError("offloaded state has 32 bits and one weight decay")
-        unknown = set(no_decay) - set(ds_ids)
+        unknown = no_decay - set(ds_ids)
         if unknown:
             raise ValueError(f"no_decay names ds_ids that are not there: {sorted(unknown)}")
         self.state_bits, self.gather_bits, self.reduce_bits = state_bits, gather_bits, reduce_bits
-        self.no_decay, self.seed = frozenset(no_decay), int(seed)
+        self.no_decay, self.seed = no_decay, int(seed)
 
         if reduce_path not in ("contiguous", "coalesced"):
             raise ValueError(f"reduce_path {reduce_path!r} is not 'contiguous' or 'coalesced'")
@@ -561,11 +562,11 @@ class ShardStep:
         and with None at the end (for event timing).  With ``trace_pass`` (a
         TraceGatherPass) the forward and backward gathers follow the
         fetch/release coordinator instead of the static gather buckets."""
+        if trace_pass is not None and self.gather_bits == 4:
+            raise ValueError("the coordinator's gathers run on the 16-bit wire")
         self.t += 1
         mark = on_phase or (lambda name: None)
         if trace_pass is not None:
-            if self.gather_bits == 4:
-                raise ValueError("the coordinator's gathers run on the 16-bit wire")
             mark("gather_trace")
             trace_pass.run(stream)
         else:

@@ -608,8 +608,10 @@ __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) 
     const int32_t b = static_cast<int32_t>(blockIdx.x);
     const int s = find_tensor(plan, b, lane);
     const ReadTensor t = plan.t[s];
+    const bool second = t.size < 0;
+    const int64_t numel = second ? ~t.size : t.size;
     const int64_t tile0 = int64_t(b - plan.first_tile[s]) * kReadTile;
-    const int64_t scales = (t.numel + kMxBlock - 1) / kMxBlock * kMxBlock;
+    const int64_t scales = (numel + kMxBlock - 1) / kMxBlock * kMxBlock;
     T* out = static_cast<T*>(t.out) + tile0;
     const int oo = line_offset(out);
     // 16 codes of a lane: half a block, one 16-byte load
@@ -620,7 +622,7 @@ __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) 
         const int64_t e = tile0 + (wave * kReadVecs + k) * 1024 + 16 * lane;
         C[k] = u4{0, 0, 0, 0};
         S[k] = 0;
-        if (e < t.numel) {        // codes are padded to whole blocks: the 16 are there
+        if (e < numel) {        // codes are padded to whole blocks: the 16 are there
             C[k] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(t.moment + e));
             S[k] = t.moment[scales + (e >> 5)];
         }
@@ -631,7 +633,7 @@ __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float x[4];
-            if (t.second != 0) {
+            if (second) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) x[q] = decode_v((C[k][j] >> (8 * q)) & 0xffu, S[k]);
             } else {
@@ -647,7 +649,7 @@ __global__ __launch_bounds__(kLbBlock) void k_moment8_read(const ReadPlan plan) 
         }
     }
     __syncthreads();
-    const int64_t rest = t.numel - tile0;
+    const int64_t rest = numel - tile0;
     const int n = static_cast<int>(rest > kReadTile ? kReadTile : rest);
     store_lines<T>(out, stage, oo, static_cast<int>(sizeof(T)) * n, threadIdx.x, kLbBlock);
 }

@@ -53,17 +53,16 @@ hipError_t launch_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state
 
 // ------------------------------------------------------ 8-bit moments read
 
-constexpr int kReadTensors = 104;
+constexpr int kReadTensors = 128;          // as many as the search for a tile's takes
 // Groups of 16 codes of a thread.  Two: 53.4 us where one took 59.1 and four
 // 55.2 (96 moments of 1.05M read to bf16 at odd elements; 51.2, 52.9, 52.1 aligned).
 constexpr int kReadVecs = 2;
 constexpr int64_t kReadTile = int64_t(kLbBlock) * 16 * kReadVecs;
 
 struct ReadTensor {
-    int64_t numel;
+    int64_t size;           // numel of a first moment (e4m3), ~numel of a second (unsigned, 4 + 4 bits)
     const uint8_t* moment;
     void* out;
-    int64_t second;         // 0: first moment (e4m3), 1: second (unsigned, 4 + 4 bits)
 };
 
 struct ReadPlan {

@@ -276,7 +276,7 @@ zs3_status zs3_moment8_read(int32_t out_dtype, int32_t n, const zs3_moment8* lis
             if (plan.n == kReadTensors || plan.first_tile[plan.n] + tiles > kMaxTiles) {
                 if ((s = flush()) != ZS3_OK) return s;
             }
-            plan.t[plan.n] = ReadTensor{m.numel, static_cast<const uint8_t*>(m.moment), m.out, m.kind == ZS3_EXP_AVG_SQ};
+            plan.t[plan.n] = ReadTensor{m.kind == ZS3_EXP_AVG_SQ ? ~m.numel : m.numel, static_cast<const uint8_t*>(m.moment), m.out};
             plan.first_tile[plan.n + 1] = plan.first_tile[plan.n] + static_cast<int32_t>(tiles);
             ++plan.n;
         }

@@ -162,7 +162,8 @@ ZS3_API zs3_status zs3_moment8_read(int32_t out_dtype, int32_t n, const zs3_mome
  *       within a parameter are split differently).
  *   With both bits the pack runs first and recv_chunks[rank] may point into
  *   send.
- *   More than 256 received chunks have to be evenly spaced in memory.
+ *   More than 256 received chunks have to be evenly spaced in memory, chunk v at
+ *   v spacings from chunk 0; recv_chunks[rank] alone may lie anywhere.
  *
  * Both allocate, upload and keep nothing (they may be captured into a graph).
  * No written buffer may overlap another of the call, but for what is said

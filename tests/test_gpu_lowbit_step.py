@@ -197,3 +197,60 @@ def test_low_bit_bytes_and_refusals():
                 dict(no_decay=[5]), dict(gather_bits=4, single_launch="gather")):
         with pytest.raises(ValueError):
             _make(4, 0, "bf16", IDS, SIZES, **bad)
+
+
+@pytest.mark.parametrize("dtype,world,rank", [("bf16", 300, 150), ("fp16", 300, 299), ("bf16", 257, 0)])
+def test_a_step_over_more_ranks_than_a_launch_has_pointers(dtype, world, rank):
+    """The 4-bit gradient wire past 256 ranks: a whole step's send chunks, flat
+    gradient and norm against the oracle (peers send one of three sets)."""
+    import torch
+    note(f"low-bit step N={world} rank {rank} {dtype}")
+    rng = np.random.default_rng(world + rank)
+    step = _make(world, rank, dtype, IDS, SIZES, reduce_path="coalesced", state_bits=8, gather_bits=4, reduce_bits=4, seed=9)
+    try:
+        L = oracle.make_layout(world, 100, IDS, SIZES)
+        _fill(step, rng)
+        step.init_from_full()
+        mk = lambda: {p.ds_id: oracle.from_f32((rng.standard_normal(p.numel) * 1e-3).astype(np.float32), dtype) for p in L.params}   # noqa: E731
+        mine, peers = mk(), [mk() for _ in range(3)]
+        ref = np.zeros(L.shard_numel, np.uint16)
+        sent = {}
+        step.t = 1                          # the seeds of the step under way
+        for bi, (part, _, C, send, _) in enumerate(step.coalesced):
+            if not part:
+                continue
+            i = [k for k, b in enumerate(step.coalesced) if b[0]].index(bi)
+            sent[bi] = lb.send4(L, part, mine, dtype, lb.keys(step.wire_seed(i), 0, 0))
+            theirs = [lb.send4(L, part, g, dtype, lb.keys(100 + k, 0, 0))[rank] for k, g in enumerate(peers)]
+            chunks = [sent[bi][rank] if v == rank else theirs[v % 3] for v in range(world)]
+            for v in range(world):
+                if v != rank:
+                    o = step.recv_chunk_ptr(bi, v) - step.xbuf.data_ptr()
+                    step.xbuf[o:o + C] = torch.from_numpy(chunks[v]).cuda()
+            lb.reduce4(L, rank, part, chunks, dtype, ref)
+        step.t = 0
+        for p in L.params:
+            d = p.ds_id
+            if p.persistent:
+                every = [mine if v == rank else peers[v % 3] for v in range(world)]
+                oracle.reduce_scatter(L, rank, dtype, [d], every, ref)
+                for v in range(world):
+                    k = step.recv_index(v, d)
+                    step.recv[k:k + p.numel] = torch.from_numpy(every[v][d].view(np.int16)).cuda()
+            else:
+                o = step.grad_off[d]
+                step.own_grads[o:o + p.numel] = torch.from_numpy(mine[d].view(np.int16)).cuda()
+        step.sumsq.zero_()
+        step.step()
+        sync()
+        for bi, (part, _, C, send, _) in enumerate(step.coalesced):
+            if part:
+                got = step.xbuf[send:send + world * C].cpu().numpy().reshape(world, C)
+                blocks = lb.bucket_places(L, part)[2]
+                assert np.array_equal(got[:, :17 * blocks], sent[bi][:, :17 * blocks]), "send"
+        assert np.array_equal(_h16(step.grad), ref), "flat gradient"
+        x = oracle.to_f32(ref, dtype).astype(np.float64)
+        norm = float(np.sqrt((x * x).sum()))
+        assert abs(float(step.outs[0]) - norm) <= 1e-12 * norm
+    finally:
+        step.destroy()

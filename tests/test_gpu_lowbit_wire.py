@@ -509,3 +509,37 @@ def test_a_parameter_past_32_bit_offsets():
                     assert np.array_equal(flat[k0:k0 + b - a].float().cpu().numpy(), ref)
     finally:
         zs.zs3_layout_destroy(h)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("world,rank", [(257, 0), (300, 150), (300, 299), (520, 1)])
+def test_reduce_of_many_ranks_with_the_own_chunk_apart(world, rank, norm):
+    """More chunks than a launch has pointers: evenly spaced ones, and the own one
+    in an allocation of its own (what stands in its place between the others
+    is not read)."""
+    require_gpu()
+    import torch
+    note(f"mx4 reduce N={world} rank {rank}, own chunk apart, norm {norm}")
+    with Set(world, [world * 5 + 1, 60001, 33], "bf16", seed=world + rank) as st:
+        ids = st.wire_ids[::-1]
+        _, _, _, size = lb.bucket_places(st.L, ids)
+        sends = [lb.send4(st.L, ids, st.full(1e-3), "bf16", fill=0xA5) for _ in range(3)]
+        data = [sends[v % 3][rank] for v in range(world)]
+        recv = Bytes(world, size, gap=16, data=data)
+        own = Bytes(1, size, data=[data[rank]])
+        recv.row(rank).fill_(0xFF)
+        ptrs = recv.ptrs()
+        ptrs[rank] = own.ptrs()[0]
+        flat = Buf16(st.L.shard_numel, 1)
+        ref = np.full(st.L.shard_numel, 0x5A5A, np.uint16)
+        lb.reduce4(st.L, rank, ids, data, "bf16", ref)
+        slots, _ = zs.zs3_layout_norm_slots(st.h)
+        partials = torch.full((slots,), float("nan"), dtype=torch.float64, device="cuda")
+        zs.zs3_reduce_scatter_coalesced_mx4(st.h, rank, "bf16", REDUCE, ids, recv_chunks=ptrs, grad_flat=flat.ptr(),
+                                            partials=partials if norm else None)
+        sync()
+        assert np.array_equal(flat.host(), ref)
+        flat.check_guards()
+        if norm:
+            want = float((oracle.to_f32(ref, "bf16").astype(np.float64) ** 2).sum())
+            assert abs(float(partials.sum()) - want) <= 1e-12 * want

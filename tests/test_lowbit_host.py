@@ -317,3 +317,28 @@ def test_a_refused_step_does_not_count():
         st.step(trace_pass=object())
     assert st.t == 0
     st.destroy()
+
+
+def test_a_step_of_more_ranks_than_pointers_places_its_chunks():
+    """``ShardStep``'s received chunks of the 4-bit wire past 256 ranks: evenly
+    spaced but for the own one, which lies in the send buffer, so the call gets
+    as far as its launch (made only where there is no GPU to launch on)."""
+    import torch
+    from zero_sharded_state_amd.shard_step import ShardStep
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is visible: the buffers here are the host's")
+    for world, rank in ((300, 0), (300, 150), (300, 299), (257, 1)):
+        st = ShardStep(world_size=world, rank=rank, threshold=0, ds_ids=[0, 1, 2], numels=[5000, 40000, 640], dtype="bf16",
+                       prefetch_bucket_size=100000, reduce_bucket_size=41000, sub_group_size=1000, device="cpu",
+                       reduce_path="coalesced", reduce_bits=4)
+        for bi, (part, _, C, send, _) in enumerate(st.coalesced):
+            at = [st.recv_chunk_ptr(bi, v) for v in range(world)]
+            assert at[rank] == st.send_ptr(bi) + rank * C and len(set(at)) == world
+            others = [v for v in range(world) if v != rank]
+            assert all(at[v] - at[others[0]] == (v - others[0]) * C for v in others)
+            assert max(at) + C <= st.xbuf.data_ptr() + st.xbuf.numel()
+        for n, ids, grads, send, recv in st._x:
+            code = zs.lib().zs3_reduce_scatter_coalesced_mx4(st.h, rank, st.dcode, zs.ZS3_PACK | zs.ZS3_REDUCE, n, ids, grads, send, recv,
+                                                             st.grad.data_ptr(), None, zs.ZS3_ROUND_STOCHASTIC, 1, None)
+            assert code == zs.ZS3_EHIP, zs.zs3_last_error()
+        st.destroy()

@@ -983,7 +983,7 @@ __global__ __launch_bounds__(kLbBlock) void k_mx4_reduce(const MxPlan plan, doub
             if (real == 512 * VECS) mx_sum<BATCH, VECS, true>(acc, chunk, plan.world, codes, scales, lane, real);
             else mx_sum<BATCH, VECS, false>(acc, chunk, plan.world, codes, scales, lane, real);
         };
-        if constexpr (EVEN) sum([&](int v) -> const uint8_t* { return plan.base + v * plan.stride; });
+        if constexpr (EVEN) sum([&](int v) -> const uint8_t* { return v == plan.rank ? plan.own : plan.base + v * plan.stride; });
         else sum([&](int v) -> const uint8_t* { return plan.chunk[v]; });
         const float n = static_cast<float>(plan.world);
         const bool pow2 = (plan.world & (plan.world - 1)) == 0;

@@ -112,7 +112,8 @@ struct MxParam {
     int64_t slot;           // reduce: its first norm slot
 };
 
-// Chunk v is at chunk[v], or at base + v * stride where base is set.
+// Chunk v is at chunk[v - v0], or at base + v * stride where base is set; the
+// reduce takes its own rank's from `own` then.
 struct MxPlan {
     int32_t n;
     int32_t first_tile[kMxParams + 1];
@@ -122,7 +123,7 @@ struct MxPlan {
     int64_t blocks;         // blocks of a chunk
     uint8_t* base;
     int64_t stride;
-    uint8_t* own;           // gather: the own chunk to write
+    uint8_t* own;           // gather: the own chunk to write; reduce: to read, where base is set
     MxParam p[kMxParams];
     uint8_t* chunk[kMxRanks];
 };

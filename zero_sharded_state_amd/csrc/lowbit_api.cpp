@@ -355,7 +355,7 @@ zs3_status check_chunk(const void* p, const char* what) {
 }
 
 // Chunks of a call: evenly spaced ones by their spacing, others by pointers.
-// `skip`: a rank whose entry is not read (-1: none).
+// `skip`: a rank whose place does not count (-1: none): its chunk is not read, or by a pointer of its own.
 struct Chunks {
     const void* const* list;
     int32_t world;
@@ -562,9 +562,10 @@ zs3_status zs3_reduce_scatter_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_
                 if (both.clash(&x, &y)) return fail(ZS3_EALIAS, "send overlaps grad_flat or partials");
             }
         }
-        const Chunks recv(reduce ? recv_chunks : nullptr, reduce ? b.world : 0, -1);
+        // the own chunk has its own pointer: inside `send`, it is apart from the others
+        const Chunks recv(reduce ? recv_chunks : nullptr, reduce ? b.world : 0, rank);
         if (reduce && !recv.even && b.world > kMxRanks)
-            return fail(ZS3_EINVAL, "more than %d received chunks have to be evenly spaced", kMxRanks);
+            return fail(ZS3_EINVAL, "more than %d received chunks have to be evenly spaced, but for the own one", kMxRanks);
 
         MxPlan plan;
         plan.rank = rank;
@@ -589,6 +590,7 @@ zs3_status zs3_reduce_scatter_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_
         }
         if (reduce) {
             recv.put(&plan, 0, b.world);
+            plan.own = static_cast<uint8_t*>(const_cast<void*>(recv_chunks[rank]));
             // first norm slot of each parameter: partitioned ones first, in
             // ascending ds_id, whole groups of slots for each
             std::vector<int64_t> slot(b.items.size(), 0);

@@ -299,11 +299,13 @@ class ShardStep:
             ids_part = sorted(d for d in b if not self.by_id[d]["persistent"])
             ids_pers = [d for d in b if self.by_id[d]["persistent"]]
             if self.reduce_bits == 4:       # offsets in bytes, C the bytes of a chunk
+                # the N chunks of the send buffer, then the received ones at even
+                # spacing with the own one's place left free (more than 256
+                # chunks have to lie so; the own one is in the send buffer)
                 C = zs.zs3_mx4_sizes(self.h, ids_part)[1]
-                others = [v for v in range(self.N) if v != self.rank]
                 buckets.append((ids_part, ids_pers, C, cursor,
-                                {v: cursor + (self.N + k) * C for k, v in enumerate(others)}))
-                cursor += (self.N + len(others)) * C
+                                {v: cursor + (self.N + v) * C for v in range(self.N) if v != self.rank}))
+                cursor += 2 * self.N * C
                 continue
             C = sum(self.by_id[d]["partition_size"] for d in ids_part)
             if not ids_part:

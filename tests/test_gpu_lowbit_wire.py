@@ -543,3 +543,41 @@ def test_reduce_of_many_ranks_with_the_own_chunk_apart(world, rank, norm):
         if norm:
             want = float((oracle.to_f32(ref, "bf16").astype(np.float64) ** 2).sum())
             assert abs(float(partials.sum()) - want) <= 1e-12 * want
+
+
+@pytest.mark.parametrize("rank", [0, 150, 299])
+def test_gather_of_many_ranks_with_chunks_anywhere(rank):
+    """More unevenly spaced chunks than a launch has pointers: several launches,
+    the own rank in the first or a later one, both modes."""
+    require_gpu()
+    import torch
+    note(f"mx4 gather N=300 rank {rank}, uneven chunks")
+    world = 300
+    with Set(world, [world * 7 + 3, 60001, 64], "fp16", seed=rank) as st:
+        ids = st.wire_ids
+        _, _, _, size = lb.bucket_places(st.L, ids)
+        full = st.full()
+        shards = {r: oracle.partition(st.L, r, full) for r in range(world)}
+        chunks = [lb.pack4(st.L, r, ids, shards[r], "fp16", fill=0xA5) for r in range(world)]
+        at, o = [], 0
+        for v in range(world):
+            at.append(o)
+            o += size + 16 * int(st.rng.integers(0, 5))
+        shard = Buf16(st.L.shard_numel, 1, shards[rank])
+        host = np.full(o, 0xA5, np.uint8)
+        for v in range(world):
+            host[at[v]:at[v] + size] = chunks[v]
+        ref = lb.unpack4(st.L, ids, chunks, "fp16")
+        for fused in (True, False):
+            wire = torch.from_numpy(host).cuda()
+            ptrs = [wire.data_ptr() + a for a in at]
+            out = Buf16(sum(p.numel for p in st.L.params), 3)
+            if fused:
+                wire[at[rank]:at[rank] + size] = 0xA5
+                zs.zs3_gather_coalesced_mx4(st.h, rank, "fp16", PACK | UNPACK, ids, shard.ptr(), ptrs[rank], ptrs, out.ptr())
+            else:
+                zs.zs3_gather_coalesced_mx4(st.h, rank, "fp16", UNPACK, ids, rank_chunks=ptrs, full_flat=out.ptr())
+            sync()
+            assert np.array_equal(wire.cpu().numpy(), host)
+            assert np.array_equal(out.host(), ref)
+            out.check_guards()

@@ -254,3 +254,35 @@ def test_a_step_over_more_ranks_than_a_launch_has_pointers(dtype, world, rank):
         assert abs(float(step.outs[0]) - norm) <= 1e-12 * norm
     finally:
         step.destroy()
+
+
+def test_settings_changed_between_steps():
+    """Learning rate and weight decay changed between steps, in place and by a new
+    AdamConfig: the list step (a parameter without decay makes it one) gives the
+    flat step's bits for every parameter that decays."""
+    import torch
+    note("settings changed between steps")
+    out = {}
+    for name, off in (("flat", ()), ("listed", (9,))):
+        rng = np.random.default_rng(23)
+        step = _make(4, 1, "bf16", IDS, SIZES, no_decay=off)
+        _fill(step, rng)
+        step.init_from_full()
+        step.recv.copy_(torch.from_numpy(oracle.from_f32((rng.standard_normal(step.recv.numel()) * 1e-3).astype(np.float32), "bf16").view(np.int16)))
+        step.adam = AdamConfig(lr=1e-3, beta2=0.99, weight_decay=0.1)
+        for lr, wd in ((1e-3, 0.1), (5e-4, 0.4), (2e-3, 0.0)):
+            step.adam.lr, step.adam.weight_decay = lr, wd
+            step.sumsq.zero_()
+            step.step()
+        step.adam = AdamConfig(lr=3e-3, beta2=0.9, weight_decay=0.2)
+        step.sumsq.zero_()
+        step.step()
+        sync()
+        out[name] = {p["ds_id"]: [x[p["shard_offset"]:p["shard_offset"] + p["own"][1] - p["own"][0]].cpu().numpy().copy()
+                                  for x in (step.master, step.exp_avg, step.exp_avg_sq, step.shard)] for p in step.params}
+        step.destroy()
+    for d in IDS:
+        if d == 9:
+            continue
+        for a, b in zip(out["flat"][d], out["listed"][d]):
+            assert np.array_equal(a.view(np.uint8), b.view(np.uint8)), d

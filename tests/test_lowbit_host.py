@@ -342,3 +342,33 @@ def test_a_step_of_more_ranks_than_pointers_places_its_chunks():
                                                              st.grad.data_ptr(), None, zs.ZS3_ROUND_STOCHASTIC, 1, None)
             assert code == zs.ZS3_EHIP, zs.zs3_last_error()
         st.destroy()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_changed_decay_reaches_the_next_step(bits, monkeypatch):
+    """``ShardStep.adam`` is read at every step, its weight decay with the rest:
+    changed in place or replaced, the lists carry the new one, and none for
+    parameters in no_decay."""
+    import dataclasses
+    seen = []
+
+    class Recorder:
+        @staticmethod
+        def zs3_adamw_tensors(dtype, grad, state_bits, n, tensors, scale, flag, hp, seed, stream):
+            seen.extend((hp._obj.lr, tensors[i].id, tensors[i].weight_decay) for i in range(n))
+            return zs.ZS3_OK
+
+    st = _host_step(state_bits=bits, no_decay=[1])
+    try:
+        with monkeypatch.context() as m:
+            m.setattr(zs, "lib", lambda: Recorder)
+            for lr, wd in ((1e-3, 0.1), (2e-3, 0.3), (2e-3, 0.0), (1e-3, 0.2)):
+                if wd == 0.2:
+                    st.adam = dataclasses.replace(st.adam, lr=lr, weight_decay=wd)
+                else:
+                    st.adam.lr, st.adam.weight_decay = lr, wd
+                seen.clear()
+                st.adam_step(1, stream=0)
+                assert sorted(seen) == [(lr, 0, wd), (lr, 1, 0.0)]
+    finally:
+        st.destroy()

@@ -374,6 +374,7 @@ class ShardStep:
             src = (P * (len(b) * self.N))(*[self.recv_ptr(v, d) for d in b for v in range(self.N)])
             self._r.append((len(b), ids, src))
         if self.listed:
+            self._listed_decay = self.adam.weight_decay
             self._lists = [zs.zs3_adamw_tensor_list([self._tensor(p) for p in self.params if b <= p["shard_offset"] < e])
                            for b, e in self.sub_groups]
         all_ids = [p["ds_id"] for p in self.params]
@@ -540,6 +541,11 @@ class ShardStep:
         hp = zs.zs3_adam_params(a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, int(t))
         s = stream if stream is not None else self._stream()
         if self.listed:
+            if a.weight_decay != self._listed_decay:      # like the other settings, read at every step
+                for tensors in self._lists:
+                    for x in tensors[:tensors.count]:
+                        x.weight_decay = 0.0 if x.id in self.no_decay else a.weight_decay
+                self._listed_decay = a.weight_decay
             for tensors in self._lists:
                 self._ok(zs.lib().zs3_adamw_tensors(self.dcode, self.dcode, self.state_bits, tensors.count, tensors,
                                                     self.scale_ptr, self.flag_ptr, ctypes.byref(hp), self.seed, s))

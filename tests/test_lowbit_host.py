@@ -358,7 +358,8 @@ def test_a_changed_decay_reaches_the_next_step(bits, monkeypatch):
             seen.extend((hp._obj.lr, tensors[i].id, tensors[i].weight_decay) for i in range(n))
             return zs.ZS3_OK
 
-    st = _host_step(state_bits=bits, no_decay=[1])
+    from zero_sharded_state_amd.shard_step import AdamConfig
+    st = _host_step(state_bits=bits, no_decay=[1], adam=AdamConfig())
     try:
         with monkeypatch.context() as m:
             m.setattr(zs, "lib", lambda: Recorder)

@@ -160,8 +160,8 @@ ZS3_API zs3_status zs3_moment8_read(int32_t out_dtype, int32_t n, const zs3_mome
  *       order; the padding positions of a partition are written as 0.
  *       partials: as in zs3_reduce_scatter_local (the same slots; the sums
  *       within a parameter are split differently).
- *   With both bits the pack runs first and recv_chunks[rank] may point into
- *   send.
+ *   With both bits the pack runs first, and received chunks (the own one, for
+ *   a real rank) may lie in send: what the pack wrote there is read.
  *   More than 256 received chunks have to be evenly spaced in memory, chunk v at
  *   v spacings from chunk 0; recv_chunks[rank] alone may lie anywhere.
  *

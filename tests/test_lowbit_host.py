@@ -373,3 +373,23 @@ def test_a_changed_decay_reaches_the_next_step(bits, monkeypatch):
                 assert sorted(seen) == [(lr, 0, wd), (lr, 1, 0.0)]
     finally:
         st.destroy()
+
+
+def test_pack_with_reduce_refuses_every_overlap(layout):
+    """With both bits the gradients, too, may not lie under what the reduce
+    writes; received chunks may lie in the send buffer, at any rank."""
+    import torch
+    flat, slots = BASE + (8 << 20), BASE + (9 << 20)
+    p = zs.zs3_layout_param(layout, 9)
+    first = flat + 2 * p["shard_offset"]            # of what the reduce writes for a parameter
+    for g in (first, first + 10, first + 2 * p["partition_size"] - 2):
+        for grads in ([g, BASE + (2 << 20)], [BASE + (1 << 20), g]):
+            _refused(zs.ZS3_EALIAS, "gradient overlaps", _scatter, layout, grads=grads, flat=flat)
+    _refused(zs.ZS3_EALIAS, "gradient overlaps", _scatter, layout, grads=[BASE + (1 << 20), slots + 8], partials=slots)
+    _refused(zs.ZS3_EALIAS, "gradient overlaps", _scatter, layout, grads=[slots - 2, BASE + (1 << 20)], partials=slots)
+    if not torch.cuda.is_available():       # taken: they get as far as their launch
+        _, size = zs.zs3_mx4_sizes(layout, [5, 9])
+        for recv in ([BASE + size] * 4, [BASE + v * size for v in range(4)]):
+            _refused(zs.ZS3_EHIP, "", _scatter, layout, recv=recv)
+        # two gradients may share memory: they are read only
+        _refused(zs.ZS3_EHIP, "", _scatter, layout, grads=[BASE + (1 << 20)] * 2)

@@ -553,13 +553,16 @@ zs3_status zs3_reduce_scatter_coalesced_mx4(zs3_layout_t L, int32_t rank, int32_
             // what the pack writes is what the reduce may read, and nothing it writes
             if (ranges.clash(&x, &y)) return fail(ZS3_EALIAS, "grad_flat or partials overlaps another buffer of the call");
             if (pack) {
+                constexpr int64_t kGrad = -2;
                 Ranges both;
                 both.add(send, b.chunk_bytes * b.world, true, -1);
                 for (const Item& it : b.items) {
-                    both.add(static_cast<const uint16_t*>(grad_flat) + it.offset, 2 * it.ps, true, it.ds_id);
+                    both.add(static_cast<const uint16_t*>(grad_flat) + it.offset, 2 * it.ps, true, -1);
+                    both.add(grads[it.request], 2 * it.numel, false, kGrad);
                 }
                 if (partials != nullptr) both.add(partials, 8 * n_slots, true, -1);
-                if (both.clash(&x, &y)) return fail(ZS3_EALIAS, "send overlaps grad_flat or partials");
+                if (both.clash(&x, &y))
+                    return fail(ZS3_EALIAS, "%s overlaps grad_flat or partials", x == kGrad || y == kGrad ? "a gradient" : "send");
             }
         }
         // the own chunk has its own pointer: inside `send`, it is apart from the others

@@ -393,3 +393,26 @@ def test_pack_with_reduce_refuses_every_overlap(layout):
             _refused(zs.ZS3_EHIP, "", _scatter, layout, recv=recv)
         # two gradients may share memory: they are read only
         _refused(zs.ZS3_EHIP, "", _scatter, layout, grads=[BASE + (1 << 20)] * 2)
+
+
+def test_wire_seeds_do_not_repeat():
+    """``ShardStep.wire_seed``: another one for every seed, step, rank and bucket,
+    also where steps times ranks pass 16 bits, buckets do, or the seed passes
+    32; where all fit, the fields lie side by side."""
+    seen = {}
+    for seed in (0, 1, 2, 3, (1 << 32) - 1, 1 << 32, (1 << 32) + 1, (1 << 63) + 5, -1):
+        st = _host_step(seed=seed)
+        try:
+            st.N = 64
+            for t in (1, 2, 1023, 1024, 1025, 2047, 2048, 65536, 1 << 20, 1 << 40):
+                for st.rank in (0, 1, 63):
+                    st.t = t
+                    for bucket in (0, 1, 65535, 65536, 65537, 1 << 20):
+                        s = st.wire_seed(bucket)
+                        assert 0 <= s < 1 << 64
+                        assert seen.setdefault(s, (seed, t, st.rank, bucket)) == (seed, t, st.rank, bucket)
+                        count = t * 64 + st.rank
+                        if 0 <= seed < 1 << 32 and count < 1 << 16 and bucket < 1 << 16:
+                            assert s == (seed << 32) + (count << 16) + bucket
+        finally:
+            st.destroy()

@@ -43,6 +43,7 @@ tensors owned by this object; all arithmetic runs in libzs3's kernels.
 from __future__ import annotations
 
 import ctypes
+import hashlib
 from dataclasses import dataclass
 from typing import Dict, List, Sequence, Tuple
 
@@ -513,8 +514,15 @@ class ShardStep:
 
     def wire_seed(self, bucket: int) -> int:
         """Seed of a gradient bucket's rounding in the step under way: another
-        one for every rank, step and bucket."""
-        return (self.seed << 32) + ((self.t * self.N + self.rank) << 16) + bucket & (1 << 64) - 1
+        one for every seed, rank, step and bucket.  32 + 16 + 16 bits hold the
+        seed, the count of steps and ranks and the bucket; from where one does
+        not fit (it would run into the next, and repeat another seed's words)
+        the three are hashed."""
+        seed, count = self.seed & (1 << 64) - 1, self.t * self.N + self.rank
+        if seed >> 32 == 0 and count >> 16 == 0 and bucket >> 16 == 0:
+            return seed << 32 | count << 16 | bucket
+        key = b"%d %d %d" % (seed, count, bucket)
+        return int.from_bytes(hashlib.blake2b(key, digest_size=8).digest(), "little")
 
     def repartition(self, stream=None, dst=None):
         """The partition copy ([codex] 3.1): every full parameter's own range

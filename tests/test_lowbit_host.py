@@ -416,3 +416,19 @@ def test_wire_seeds_do_not_repeat():
                             assert s == (seed << 32) + (count << 16) + bucket
         finally:
             st.destroy()
+
+
+def test_gather_timers_are_refused_with_the_4_bit_wire():
+    """The 4-bit calls record no events: a timer's pair would be left to the next
+    other launch.  Refused before anything runs, and the step does not count."""
+    st = _host_step(gather_bits=4)
+    pairs = []
+    timer = lambda: pairs.append(1) or (None, None)     # noqa: E731
+    try:
+        with pytest.raises(ValueError, match="4-bit"):
+            st.step(gather_timer=timer)
+        with pytest.raises(ValueError, match="4-bit"):
+            st.gather_pass(timer=timer)
+        assert st.t == 0 and not pairs
+    finally:
+        st.destroy()

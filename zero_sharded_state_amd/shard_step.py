@@ -469,8 +469,11 @@ class ShardStep:
         gather streams they are dealt round-robin and joined at the end
         (``streams`` overrides the step's count for this pass).
         ``timer()``, if given, returns a (start, stop) hipEvent_t pair that
-        the bucket's kernel records its own start and end into."""
+        the bucket's kernel records its own start and end into (the 16-bit
+        wire's: the 4-bit calls record none)."""
         lib = zs.lib()
+        if timer is not None and self.gather_bits == 4:
+            raise ValueError("the 4-bit gathers record no events")
         if self.single_gather:
             nb, starts, ids, owns, chunks, fulls = self._gm
             if timer is not None:
@@ -580,6 +583,8 @@ class ShardStep:
         fetch/release coordinator instead of the static gather buckets."""
         if trace_pass is not None and self.gather_bits == 4:
             raise ValueError("the coordinator's gathers run on the 16-bit wire")
+        if gather_timer is not None and self.gather_bits == 4:
+            raise ValueError("the 4-bit gathers record no events")
         self.t += 1
         mark = on_phase or (lambda name: None)
         if trace_pass is not None:

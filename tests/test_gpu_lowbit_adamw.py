@@ -444,3 +444,39 @@ def test_a_tensor_past_32_bit_offsets():
     s = spots[3]
     code, sc = m[s:s + 96].cpu().numpy(), m[32 * nb + s // 32:32 * nb + s // 32 + 3].cpu().numpy()
     assert np.array_equal(out[s:s + 96].float().cpu().numpy(), lb.decode_moment(code, sc, False))
+
+
+@pytest.mark.parametrize("beta2", [0.9, 0.99, 0.999, 0.9999])
+@pytest.mark.parametrize("step", [1, 50])
+@pytest.mark.parametrize("eps", [1e-12, 1e-8])
+def test_updates_where_the_root_counts_as_zero(beta2, step, eps):
+    """Weights of 0, so that the update itself is what is measured, and second
+    moments on both sides of fp32's normal range.  Where one lies under it the
+    root may count as 0: the denominator loses sqrt(v) / sqrt(1 - b2^t) of at
+    least eps, at most 2^-63 / (eps * sqrt(1 - b2^t)) of the update, beside
+    the 11 half-ulps that ``check`` counts and the half ulp of the result."""
+    require_gpu()
+    import torch
+    note(f"adamw8 roots that count as 0, beta2 {beta2} step {step} eps {eps}")
+    rng = np.random.default_rng(17)
+    n = 4096
+    c = Case(rng, n, 0, "bf16", "fp32", 8)
+    c.w[:] = 0
+    c.g = (rng.standard_normal(n) * 10.0 ** rng.uniform(-24, -15, n)).astype(np.float32)
+    c.m[:] = 0
+    c.v[:] = 0
+    c.dw.view.zero_()
+    c.dg.view.copy_(torch.from_numpy(c.g))
+    c.dm.view.zero_()
+    c.dv.view.zero_()
+    hp = dict(HP, beta2=beta2, eps=eps, step=step)
+    _step([c], 8, hp=hp)
+    sync()
+    _, m, v, decayed, upd = c.expect(1.0, hp, 0)
+    assert np.all(decayed == 0) and 1000 < np.count_nonzero(v < 2.0 ** -126) < n - 500
+    root = np.sqrt(v.astype(np.float64) / (1 - beta2 ** step))
+    lost = np.where(v < 2.0 ** -126, root / eps, 0.0)
+    assert lost.max() <= 2.0 ** -63 / (eps * np.sqrt(1 - beta2 ** step))
+    err = np.abs(c.dw.host().astype(np.float64) + upd)
+    bound = np.abs(upd) * (1.001 * 2.0 ** -24 * 12 * (1 + lost) + lost) + 2.0 ** -149
+    assert np.all(err <= bound), float((err / bound).max())

@@ -147,8 +147,9 @@ zs3_status zs3_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t state_bi
         zs3_status s = check_adam_params(hp);
         if (s != ZS3_OK) return s;
         // the 8-bit form's root takes second moments under fp32's normal range,
-        // roots under 1.1e-19, as 0: eps has to be so much larger that this
-        // is within its own rounding
+        // roots under 2^-63, as 0, which moves an update by up to 2^-63 / (eps *
+        // sqrt(1 - beta2^t)) of itself: at the smallest eps 3.4e-6 in the first
+        // step at beta2 = 0.999, 1.1e-7 (two half-ulps) once beta2^t is small
         if (state_bits == 8 && hp->eps < 1e-12) return fail(ZS3_EINVAL, "eps %g < 1e-12 with 8-bit states", hp->eps);
         if ((scale != nullptr && !aligned(scale, 4)) || (nonfinite != nullptr && !aligned(nonfinite, 4)))
             return fail(ZS3_EINVAL, "scale or nonfinite is not 4-byte aligned");

@@ -71,10 +71,10 @@ enum { ZS3_FP32 = 3 };    /* a type of gradients and of read moments here */
  * ZS3_FP32.  Needs 0 <= beta < 1, eps >= 0 (8-bit states: eps >= 1e-12, since
  * roots of second moments under fp32's normal range count as 0; an update so
  * grows by at most 2^-63 / (eps * sqrt(1-b2^t)) of itself: at eps = 1e-12 and
- * b2 = 0.999 3.4e-6 in the first step, at eps = 1e-8 under a hundredth of fp32's
- * rounding from there on), at most 3.4e10 elements a tensor.  The call allocates, uploads and keeps nothing: it
- * may be captured into a graph, and calls on different streams with different
- * tensors are independent.  (A captured call replays the step number, learning
+ * b2 = 0.999 3.4e-6 in the first step, at eps = 1e-8 under a hundredth of
+ * fp32's rounding from there on), at most 3.4e10 elements a tensor.  The call
+ * allocates, uploads and keeps nothing: it may be captured into a graph, and
+ * calls on different streams with different tensors are independent.  (A captured call replays the step number, learning
  * rate and seed it was captured with.)
  */
 typedef struct {
@@ -138,7 +138,12 @@ ZS3_API zs3_status zs3_moment8_read(int32_t out_dtype, int32_t n, const zs3_mome
  * nearest ends at 6; every element is off by at most half of a code's
  * spacing.  Stochastic: the smallest with |x| <= 6 * 2^e, and each element
  * goes to one of the two neighbouring codes with a probability that keeps
- * its expected value (small gradients then survive on average).  Either
+ * its expected value (small gradients then survive on average).  Elements 2i
+ * and 2i+1 of a block draw on one random word, the second on it rotated by a
+ * bit, so they are not independent: where both lie a fraction f of the way to
+ * the next code, their roundings correlate by (0.5 - f) / (1 - f), from f =
+ * 0.5 on by (f - 0.5) / f.  The error of a sum over such pairs has up to 1.5
+ * times the variance of independent ones (f near 0 or 1).  Either
  * way e is at least -126 and at most 13 (fp16) or 125 (bf16), where 6 * 2^e
  * is still finite; larger magnitudes are held at 6 * 2^e.  (bf16 values under
  * 2^-126 may count as 0.)
@@ -157,6 +162,11 @@ ZS3_API zs3_status zs3_moment8_read(int32_t out_dtype, int32_t n, const zs3_mome
  *   mode & ZS3_PACK: chunk d of send (at byte d * chunk bytes) = destination
  *       d's partitions of grads, rounded as `rounding` says; the random bits
  *       are a function of seed and an element's place in send alone.
+ *       Give every rank, step and bucket a seed of its own: ranks that share
+ *       one round the same element by the same word, and their errors add up
+ *       in the average instead of cancelling; a seed kept over steps rounds
+ *       the same way every time.  (Seed 0 draws the word 0 for the first pair
+ *       of send, which rounds toward zero.)
  *   mode & ZS3_REDUCE: grad_flat[shard_offset_j + k] = round16((0 + r_0 + ... +
  *       r_{N-1}) / N) of the received elements, fp32 operations in rank
  *       order; the padding positions of a partition are written as 0.

@@ -219,3 +219,33 @@ def test_wire_places(world, sizes):
         lb.reduce4(L, r, request, [lb.send4(L, request, full, "fp16")[r]] * world, "fp16", flat)
         ref = oracle.partition(L, r, full)
         assert np.array_equal(oracle.to_f32(flat, "fp16"), oracle.to_f32(ref, "fp16"))
+
+
+@pytest.mark.parametrize("f", [0.05, 0.1, 0.25, 0.5, 0.75, 0.95])
+def test_pairs_of_the_stochastic_wire_correlate_as_stated(f):
+    """Two neighbours a fraction f of the way to the next code: each goes up with
+    probability f, and the two correlate by (0.5 - f) / (1 - f), from f = 0.5 on
+    by (f - 0.5) / f, since the second's word is the first's rotated by a bit
+    (2u mod 1 beside u).  Within five deviations of a million pairs: sqrt(f(1-f)
+    / n) of a mean, and at most sqrt(1 / min(f, 1-f) / n) of a correlation."""
+    n = 1 << 21
+    x = np.full(n, 0.5 * f, np.float32)
+    x[31::32] = 6.0                                     # a scale of 1
+    at = np.arange(n)
+    word = lb.words(lb.keys(123, 0, 0), at // 2)
+    word = np.where(at % 2 == 0, word, (word << np.uint32(1)) | (word >> np.uint32(31)))
+    code, s = lb.encode4(x, "bf16", word)
+    assert np.all(s == 127) and np.all(code[31::32] == 7)
+    pairs = code.reshape(-1, 16, 2)[:, :15].reshape(-1, 2).astype(np.float64)       # the last pair of a block apart
+    assert set(np.unique(pairs)) <= {0, 1}
+    k = len(pairs)
+    assert np.all(np.abs(pairs.mean(0) - f) <= 5 * np.sqrt(f * (1 - f) / k) + 2.0 ** -24)
+    want = (0.5 - f) / (1 - f) if f <= 0.5 else (f - 0.5) / f
+    assert abs(np.corrcoef(pairs.T)[0, 1] - want) <= 5 * np.sqrt(1 / min(f, 1 - f) / k)
+
+
+def test_seed_zero_draws_a_zero_first():
+    """The wire's first word of seed 0 is 0, of others it is not: the first pair
+    of a send buffer then rounds toward zero."""
+    assert lb.keys(0, 0, 0) == 0 and lb.words(0, np.arange(1))[0] == 0
+    assert all(lb.words(lb.keys(s, 0, 0), np.arange(1))[0] != 0 for s in range(1, 1000))

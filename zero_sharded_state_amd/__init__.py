@@ -541,6 +541,7 @@ def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, d
                                      grads: Optional[Sequence] = None, send=None,
                                      recv_chunks: Optional[Sequence] = None, grad_flat=None, partials=None,
                                      rounding: int = ZS3_ROUND_NEAREST, seed: int = 0, stream=None) -> None:
+    """``seed`` (stochastic rounding): another one for every rank, step and bucket."""
     g = _ptrs(grads) if grads is not None else None
     r = _ptrs(recv_chunks) if recv_chunks is not None else None
     _check(lib().zs3_reduce_scatter_coalesced_mx4(layout, rank, _dtype_lowbit(dtype), mode, len(ds_ids), _i64s(ds_ids),

@@ -432,3 +432,13 @@ def test_gather_timers_are_refused_with_the_4_bit_wire():
         assert st.t == 0 and not pairs
     finally:
         st.destroy()
+
+
+def test_an_eps_that_8_bit_states_refuse_is_refused_at_once():
+    """What the list step would refuse in the first step, after its gathers."""
+    from zero_sharded_state_amd.shard_step import AdamConfig
+    for eps in (0.0, 1e-13, float("nan")):
+        with pytest.raises(ValueError, match="eps"):
+            _host_step(state_bits=8, adam=AdamConfig(eps=eps))
+    for bits, eps in ((8, 1e-12), (32, 0.0)):
+        _host_step(state_bits=bits, no_decay=[1], adam=AdamConfig(eps=eps)).destroy()

@@ -72,6 +72,8 @@ class ShardStep:
 
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits {state_bits!r} is not 8 or 32")
+        if state_bits == 8 and not adam.eps >= 1e-12:
+            raise ValueError(f"eps {adam.eps!r} < 1e-12 with 8-bit states")
         if gather_bits not in (4, 16) or reduce_bits not in (4, 16):
             raise ValueError("gather_bits and reduce_bits are 4 or 16")
         if reduce_bits == 4 and reduce_path != "coalesced":

@@ -96,7 +96,7 @@ ZS3_API zs3_status zs3_adamw_tensors(int32_t dtype, int32_t grad_dtype, int32_t 
 /* Bytes of an 8-bit moment of numel elements. */
 ZS3_API zs3_status zs3_moment8_bytes(int64_t numel, int64_t* bytes);
 
-/* Reads 8-bit moments (for a checkpoint, or to look at them): out[i] =
+/* Reads 8-bit moments (to look at them, or to go on in 32 bits): out[i] =
  * value of element i, ZS3_BF16 or ZS3_FP32, both exact (values below the
  * type's normal range apart).  list: host array of n; out must not
  * overlap a moment of the call. */

@@ -409,7 +409,9 @@ class ShardStep:
 
     def moments(self, ds_id: int):
         """(exp_avg, exp_avg_sq) of a parameter's real elements in fp32: views of
-        the 32-bit state, or 8-bit moments read out."""
+        the 32-bit state, or 8-bit moments read out.  No call writes 8-bit
+        moments back from fp32: what a checkpoint keeps to resume from is the
+        bytes of ``exp_avg`` and ``exp_avg_sq`` (for this rank and layout)."""
         p = self.by_id[ds_id]
         o, n = p["shard_offset"], p["own"][1] - p["own"][0]
         if self.state_bits == 32:

@@ -1,0 +1,258 @@
+// What the gradient-list entry points launch, checked without a GPU: the launchers
+// are replaced by recorders that succeed, and every plan is then held against the
+// request, as the kernels read it: each tensor's elements exactly once and in its
+// place, each partial result inside the workspace and in a place of its own.
+// Addresses are made up and never read.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cstdio>
+#include <map>
+#include <set>
+#include <vector>
+
+#include "grads.hpp"
+#include "zs3_grads.h"
+#include "zs3_internal.hpp"
+
+namespace zs3 {
+
+// A launch: its tensors as its kernel takes them.
+struct Launch {
+    bool written;
+    int32_t kind, n, per;
+    std::vector<int32_t> first_tile;
+    std::vector<uint32_t> meta;
+    std::vector<const void*> grad;
+    std::vector<void*> out;
+    NormParts parts;
+};
+std::vector<Launch> launches;
+struct TensorNorms {
+    int32_t kind, n, per;
+    std::vector<int32_t> first_tile;
+    const double* parts;
+    double* out;
+};
+std::vector<TensorNorms> tensor_norms;
+struct End {
+    const double* groups;
+    int64_t n;
+    NormEnd end;
+};
+std::vector<End> ends;
+
+template <class PLAN>
+Launch copy(const PLAN& p, bool written, int32_t kind, const NormParts& parts) {
+    Launch l{written, kind, p.n, p.per, {}, {}, {}, {}, parts};
+    l.first_tile.assign(p.first_tile, p.first_tile + p.n + 1);
+    l.meta.assign(p.meta, p.meta + p.n);
+    l.grad.assign(p.grad, p.grad + p.n);
+    return l;
+}
+hipError_t launch_norm(int32_t kind, const NormPlan& p, const NormParts& parts, hipStream_t) {
+    launches.push_back(copy(p, false, kind, parts));
+    return hipSuccess;
+}
+hipError_t launch_clip(const WritePlan& p, const float*, const int32_t*, hipStream_t) {
+    launches.push_back(copy(p, true, 0, NormParts{}));
+    launches.back().out.assign(p.out, p.out + p.n);
+    return hipSuccess;
+}
+hipError_t launch_accumulate(int32_t kind, const WritePlan& p, float, bool, const NormParts& parts, hipStream_t) {
+    launches.push_back(copy(p, true, kind, parts));
+    launches.back().out.assign(p.out, p.out + p.n);
+    return hipSuccess;
+}
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, const double* parts, double* out,
+                               hipStream_t) {
+    tensor_norms.push_back({kind, n, per, {first_tile, first_tile + n + 1}, parts, out});
+    return hipSuccess;
+}
+hipError_t launch_norm_end(const double* groups, int64_t n, const NormEnd& end, hipStream_t) {
+    ends.push_back({groups, n, end});
+    return hipSuccess;
+}
+hipError_t launch_norm_finalize(const NormEnd&, hipStream_t) { return hipSuccess; }
+
+}  // namespace zs3
+
+using namespace zs3;
+
+namespace {
+
+int failed = 0;
+const char* where = "";
+#define EXPECT(c) do { if (!(c) && failed++ < 40) std::printf("line %d: %s (%s)\n", __LINE__, #c, where); } while (0)
+
+struct Rng {
+    uint64_t s;
+    uint64_t next() {
+        s ^= s << 13;
+        s ^= s >> 7;
+        return s ^= s << 17;
+    }
+    int64_t below(int64_t n) { return static_cast<int64_t>(next() % static_cast<uint64_t>(n)); }
+};
+
+uintptr_t at = uintptr_t(1) << 40;
+void* take(int64_t bytes, int64_t shift) {
+    void* p = reinterpret_cast<void*>(at + static_cast<uintptr_t>(shift));
+    at += static_cast<uintptr_t>((bytes + shift) / 4096 + 2) * 4096;
+    return p;
+}
+int64_t size_of(int32_t d) { return d == ZS3_FP32 ? 4 : 2; }
+
+std::vector<zs3_grad_tensor> list(Rng& r, int32_t n, int64_t most, bool acc) {
+    std::vector<zs3_grad_tensor> v(n);
+    for (auto& t : v) {
+        t = zs3_grad_tensor{};
+        const int64_t how = r.below(10);
+        t.numel = how == 0 ? 0 : how < 7 ? 1 + r.below(std::min<int64_t>(most, 20000)) : 1 + r.below(most);
+        t.dtype = 1 + static_cast<int32_t>(r.below(3));
+        t.out_dtype = acc ? ZS3_FP32 : 1 + static_cast<int32_t>(r.below(3));
+        t.shared = static_cast<int32_t>(r.below(2));
+        t.grad = take(t.numel * 4, size_of(t.dtype) * r.below(70));
+        t.out = acc || r.below(2) ? take(t.numel * 4, size_of(t.out_dtype) * r.below(70)) : nullptr;
+    }
+    return v;
+}
+
+// The elements of every tensor, launch by launch, as the kernels cut them.
+void hold(const std::vector<zs3_grad_tensor>& want, bool written, bool sums) {
+    size_t i = 0;
+    for (const Launch& L : launches) {
+        EXPECT(L.written == written && L.per >= 1 && L.n >= 1);
+        EXPECT(L.first_tile[0] == 0);
+        const int64_t all = L.first_tile[L.n], groups = (all + L.per - 1) / L.per;
+        EXPECT(all > 0 && groups < (int64_t(1) << 24));
+        EXPECT(sums ? groups <= kNormGroups : L.per == 1);
+        for (int32_t s = 0; s < L.n; ++s, ++i) {
+            if (i >= want.size()) {
+                EXPECT(false);
+                return;
+            }
+            const zs3_grad_tensor& t = want[i];
+            void* out = t.out != nullptr ? t.out : t.grad;
+            const int32_t od = t.out != nullptr ? t.out_dtype : t.dtype;
+            EXPECT(L.grad[s] == t.grad && (!written || L.out[s] == out));
+            const uint32_t m = L.meta[s];
+            EXPECT((m >> 16 & 3) == static_cast<uint32_t>(t.dtype) && (m >> 20 & 1) == static_cast<uint32_t>(t.shared));
+            EXPECT(!written || (m >> 18 & 3) == static_cast<uint32_t>(od));
+            const int64_t size = size_of(written ? od : t.dtype), T = gr_tile(size), tiles = L.first_tile[s + 1] - L.first_tile[s];
+            const uintptr_t main = reinterpret_cast<uintptr_t>(written ? out : t.grad);
+            const int64_t head = static_cast<int64_t>(main & (kGrLine - 1)) / size;
+            int64_t next = 0;
+            for (int64_t k = 0; k < tiles; ++k) {
+                if (k == 100 && tiles > 200) {      // whole tiles in between are alike
+                    k = tiles - 100;
+                    next = k * T - head;
+                }
+                const int64_t lo = k == 0 ? head : 0, hi = k + 1 == tiles ? static_cast<int64_t>(m & 0xffff) : T;
+                EXPECT(lo < hi && hi <= T);
+                EXPECT(k * T - head + lo == next);
+                next = k * T - head + hi;
+            }
+            EXPECT(next == t.numel);
+        }
+    }
+    while (i < want.size() && want[i].numel == 0) ++i;      // a launch of empty tensors alone is not made
+    EXPECT(i == want.size());
+}
+
+void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a, bool written) {
+    hold(want, written, true);
+    const double* lo = static_cast<const double*>(a.workspace);
+    const double* hi = lo + a.workspace_bytes / 8;
+    std::set<const double*> places;
+    auto put = [&](const double* p) {
+        EXPECT(p >= lo && p < hi);
+        EXPECT(places.insert(p).second);
+    };
+    EXPECT(ends.size() == 1);
+    int64_t groups = 0;
+    for (const Launch& L : launches) {
+        const int64_t all = L.first_tile[L.n], n = (all + L.per - 1) / L.per;
+        EXPECT(L.kind == a.kind && L.parts.groups == ends[0].groups + 2 * groups);
+        for (int64_t b = 0; b < 2 * n; ++b) put(L.parts.groups + b);
+        groups += n;
+        EXPECT((L.parts.tensors != nullptr) == (a.tensor_norms != nullptr));
+        if (L.parts.tensors == nullptr) continue;
+        for (int32_t s = 0; s < L.n; ++s) {
+            const int32_t f0 = L.first_tile[s], f1 = L.first_tile[s + 1];
+            if (f1 > f0)
+                for (int32_t b = f0 / L.per; b <= (f1 - 1) / L.per; ++b) put(L.parts.tensors + b + s);
+        }
+    }
+    EXPECT(ends[0].n == groups);
+    if (a.tensor_norms == nullptr) {
+        EXPECT(tensor_norms.empty());
+        return;
+    }
+    size_t done = 0, used = 0;
+    for (const TensorNorms& t : tensor_norms) {
+        EXPECT(t.out == a.tensor_norms + done);
+        done += static_cast<size_t>(t.n);
+        if (t.first_tile[t.n] == 0) continue;
+        EXPECT(used < launches.size());
+        const Launch& L = launches[used++];
+        EXPECT(t.parts == L.parts.tensors && t.n == L.n && t.per == L.per && t.first_tile == L.first_tile);
+    }
+    EXPECT(done == want.size() && used == launches.size());
+}
+
+zs3_norm_args args(const std::vector<zs3_grad_tensor>& v, Rng& r) {
+    zs3_norm_args a{};
+    a.kind = 1 + static_cast<int32_t>(r.below(2));
+    a.world = 1 + static_cast<int32_t>(r.below(8));
+    a.rank = static_cast<int32_t>(r.below(a.world));
+    a.finalize = 1;
+    a.max_norm = a.loss_scale = 1.0;
+    a.sums = static_cast<double*>(take(80, 0));
+    a.norm = static_cast<double*>(take(8, 0));
+    a.scale = static_cast<float*>(take(4, 0));
+    a.nonfinite = static_cast<int32_t*>(take(4, 0));
+    a.tensor_norms = r.below(2) ? static_cast<double*>(take(8 * static_cast<int64_t>(v.size()) + 8, 0)) : nullptr;
+    if (zs3_norm_workspace_bytes(static_cast<int32_t>(v.size()), v.data(), &a.workspace_bytes) != ZS3_OK) EXPECT(false);
+    a.workspace = take(a.workspace_bytes, 16 * r.below(8));
+    return a;
+}
+
+void clear() {
+    launches.clear();
+    tensor_norms.clear();
+    ends.clear();
+}
+
+}  // namespace
+
+int main() {
+    Rng r{88172645463325252ull};
+    float scale;
+    for (int k = 0; k < 600; ++k) {
+        const int32_t n = static_cast<int32_t>(k % 7 == 0 ? r.below(1200) : r.below(20));
+        const int64_t most = k % 11 == 0 ? int64_t(1) << 34 : k % 5 == 0 ? 3000000000ll : 5000000;
+        const auto plain = list(r, n, most, false), acc = list(r, n, most, true);
+        clear();
+        where = "norm";
+        zs3_norm_args a = args(plain, r);
+        EXPECT(zs3_grad_norm_tensors(n, plain.data(), &a, nullptr) == ZS3_OK);
+        hold_norm(plain, a, false);
+        clear();
+        where = "clip";
+        EXPECT(zs3_clip_tensors(n, plain.data(), &scale, nullptr, nullptr) == ZS3_OK);
+        hold(plain, true, false);
+        clear();
+        where = "accumulate";
+        EXPECT(zs3_accumulate_tensors(n, acc.data(), 1.0, 0, nullptr, nullptr) == ZS3_OK);
+        hold(acc, true, false);
+        clear();
+        where = "accumulate with the norm";
+        a = args(acc, r);
+        EXPECT(zs3_accumulate_tensors(n, acc.data(), 1.0, 1, &a, nullptr) == ZS3_OK);
+        hold_norm(acc, a, true);
+    }
+    if (failed) std::printf("%d failed\n", failed);
+    else std::printf("ok\n");
+    return failed != 0;
+}

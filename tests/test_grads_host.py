@@ -1,0 +1,214 @@
+"""The gradient-list entry points without a GPU: every refusal (arguments are checked
+before any device work, so the addresses here are made up and never read)."""
+
+import ctypes
+import math
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+import zero_sharded_state_amd as zs
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BASE = 1 << 40
+STEP = 1 << 24
+
+
+def _refused(status, text, fn, *a, **k):
+    with pytest.raises(zs.Zs3Error) as e:
+        fn(*a, **k)
+    assert e.value.status == status, e.value
+    assert text in e.value.message, e.value.message
+
+
+def _t(numel=100, at=BASE, dtype="bf16", **over):
+    d = dict(numel=numel, grad=at, dtype=dtype, out=at + STEP, out_dtype="fp32")
+    d.update(over)
+    return d
+
+
+def _args(**over):
+    o = BASE << 2
+    d = dict(kind=zs.ZS3_NORM_2, rank=0, world=2, sums=o, norm=o + 64, scale=o + 128, nonfinite=o + 132, tensor_norms=o + 4096,
+             workspace=o + (1 << 20), workspace_bytes=1 << 20)
+    d.update(over)
+    return d
+
+
+def _norm(tensors, **over):
+    zs.zs3_grad_norm_tensors(tensors, _args(**over), stream=0)
+
+
+def _clip(tensors, scale=BASE << 3, nonfinite=None):
+    zs.zs3_clip_tensors(tensors, scale, nonfinite, stream=0)
+
+
+def _acc(tensors, factor=1.0, first=False, norm=None):
+    zs.zs3_accumulate_tensors(tensors, factor, first, norm=norm, stream=0)
+
+
+def _fused(tensors, **over):
+    _acc(tensors, norm=_args(**over))
+
+
+def test_library_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "zs3_grads.h")).read()
+    syms = sorted(set(re.findall(r"ZS3_API\s+[\w\s\*]*?\b(zs3_\w+)\s*\(", text)))
+    assert syms == sorted(zs.EXPORTS_GRADS) and all(hasattr(zs.lib(), s) for s in syms)
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="no gcc")
+@pytest.mark.parametrize("lang", ["c99", "c++17"])
+def test_header_is_plain_c(tmp_path, lang):
+    """It compiles with warnings as errors, and its structs are laid out as the binding has them."""
+    src = tmp_path / "t.c"
+    src.write_text('''#include <stddef.h>
+#include <stdio.h>
+#include "zs3_grads.h"
+int main(void) {
+    int64_t b = 0;
+    printf("%d %d %d %d\\n", (int)sizeof(zs3_grad_tensor), (int)offsetof(zs3_grad_tensor, shared),
+           (int)sizeof(zs3_norm_args), (int)offsetof(zs3_norm_args, workspace_bytes));
+    if (zs3_norm_workspace_bytes(0, NULL, &b) != ZS3_OK || b <= 0) return 1;
+    return zs3_clip_tensors(0, NULL, NULL, NULL, NULL) == ZS3_EINVAL ? 0 : 2;
+}
+''')
+    exe, pkg = str(tmp_path / "t"), os.path.join(ROOT, "zero_sharded_state_amd")
+    cmd = ["gcc", "-std=c99", "-pedantic"] if lang == "c99" else ["g++", "-std=c++17", "-x", "c++"]
+    cmd += ["-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-x", "none", "-L", pkg, "-lzs3",
+            f"-Wl,-rpath,{pkg}", "-o", exe]
+    b = subprocess.run(cmd, capture_output=True, text=True)
+    assert b.returncode == 0, b.stdout + b.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    t, a = zs.zs3_grad_tensor, zs.zs3_norm_args
+    assert r.returncode == 0
+    assert r.stdout.split() == [str(x) for x in (ctypes.sizeof(t), t.shared.offset, ctypes.sizeof(a), a.workspace_bytes.offset)]
+
+
+def test_workspace_grows_with_the_launches_alone():
+    one = zs.zs3_norm_workspace_bytes([_t()])
+    assert one > 0 and one % 16 == 0 and zs.zs3_norm_workspace_bytes([]) == one
+    assert zs.zs3_norm_workspace_bytes([_t(numel=1 << 34)]) == one
+    many = zs.zs3_norm_workspace_bytes([_t()] * 1000)
+    assert one < many <= 16 * one
+    assert zs.zs3_norm_workspace_bytes([_t(numel=1 << 34)] * 4) > one
+    _refused(zs.ZS3_EINVAL, "numel", zs.zs3_norm_workspace_bytes, [_t(numel=-1)])
+    assert zs.lib().zs3_norm_workspace_bytes(0, None, None) == zs.ZS3_EINVAL
+
+
+@pytest.mark.parametrize("call", [_norm, _clip, _acc, _fused])
+def test_list_refusals(call):
+    for d in (0, 4, 7):
+        _refused(zs.ZS3_EDTYPE, "dtype", call, [_t(dtype=d)])
+    _refused(zs.ZS3_EINVAL, "numel", call, [_t(numel=-1)])
+    _refused(zs.ZS3_EINVAL, "numel", call, [_t(numel=(1 << 34) + 1)])
+    # nothing of a list is launched where a later tensor is refused
+    _refused(zs.ZS3_EINVAL, "tensor 1: numel", call, [_t(), _t(at=2 * BASE, numel=1 << 36)])
+    _refused(zs.ZS3_EINVAL, "grad is NULL", call, [_t(grad=0)])
+    _refused(zs.ZS3_EINVAL, "grad is not aligned", call, [_t(grad=BASE + 1)])
+    _refused(zs.ZS3_EINVAL, "grad is not aligned", call, [_t(grad=BASE + 2, dtype="fp32")])
+    arr = zs.zs3_grad_tensor_list([_t()])
+    arr[0].reserved = 1
+    _refused(zs.ZS3_EINVAL, "reserved", call, arr)
+
+
+@pytest.mark.parametrize("call", [_norm, _fused])
+def test_norm_refusals(call):
+    t = [_t()]
+    for k in (0, 3):
+        _refused(zs.ZS3_EINVAL, "kind", call, t, kind=k)
+    _refused(zs.ZS3_EINVAL, "world", call, t, world=0)
+    for r in (-1, 2):
+        _refused(zs.ZS3_EINVAL, "rank", call, t, rank=r)
+    for v in (0.0, -1.0, math.nan):
+        _refused(zs.ZS3_EINVAL, "max_norm", call, t, max_norm=v)
+    for v in (0.0, -1.0, math.nan, math.inf):
+        _refused(zs.ZS3_EINVAL, "loss_scale", call, t, loss_scale=v)
+    o = _args()
+    for k, off in (("sums", 4), ("norm", 4), ("scale", 2), ("nonfinite", 2), ("tensor_norms", 4), ("workspace", 8)):
+        _refused(zs.ZS3_EINVAL, k, call, t, **{k: o[k] + off})
+        if k != "tensor_norms":
+            _refused(zs.ZS3_EINVAL, "NULL", call, t, **{k: 0})
+    need = zs.zs3_norm_workspace_bytes(t)
+    _refused(zs.ZS3_EINVAL, "workspace has", call, t, workspace_bytes=need - 1)
+    _refused(zs.ZS3_EINVAL, "workspace has", call, t, workspace_bytes=0)
+
+
+@pytest.mark.parametrize("call", [_norm, _fused])
+def test_norm_refuses_overlaps(call):
+    t, o = [_t()], _args()
+    outs = ("sums", "norm", "scale", "nonfinite", "tensor_norms", "workspace")
+    for k in outs:
+        _refused(zs.ZS3_EALIAS, "tensor 0", call, t, **{k: BASE + 192})         # the gradient's last 8 bytes
+    _refused(zs.ZS3_EALIAS, "overlap", call, t, norm=o["sums"] + 16)            # world + 1 sums
+    _refused(zs.ZS3_EALIAS, "overlap", call, t, scale=o["norm"] + 4)
+    _refused(zs.ZS3_EALIAS, "overlap", call, t, nonfinite=o["scale"])
+    _refused(zs.ZS3_EALIAS, "overlap", call, t, tensor_norms=o["sums"] + 8)
+    _refused(zs.ZS3_EALIAS, "overlap", call, t, sums=o["workspace"] + 1024)
+
+
+def test_norm_finalize_refusals():
+    def call(**over):
+        zs.zs3_norm_finalize(_args(**over), stream=0)
+    for k, bad in (("kind", 0), ("world", 0), ("rank", 5), ("max_norm", 0.0), ("loss_scale", 0.0), ("sums", 0), ("norm", 0),
+                   ("scale", 0), ("nonfinite", 0)):
+        _refused(zs.ZS3_EINVAL, k if bad != 0 or k in ("kind", "world", "max_norm", "loss_scale") else "NULL", call, **{k: bad})
+    _refused(zs.ZS3_EALIAS, "overlap", call, norm=_args()["sums"] + 8)
+    assert zs.lib().zs3_norm_finalize(None, None) == zs.ZS3_EINVAL
+    assert zs.lib().zs3_grad_norm_tensors(0, None, None, None) == zs.ZS3_EINVAL
+
+
+def test_clip_refusals():
+    far = BASE + (1 << 34)
+    _refused(zs.ZS3_EDTYPE, "out_dtype", _clip, [_t(out_dtype=0)])
+    _refused(zs.ZS3_EINVAL, "out is not aligned", _clip, [_t(out=BASE + STEP + 2)])
+    _refused(zs.ZS3_EINVAL, "scale", _clip, [_t()], scale=0)
+    _refused(zs.ZS3_EINVAL, "scale", _clip, [_t()], scale=BASE + 2)
+    _refused(zs.ZS3_EINVAL, "nonfinite", _clip, [_t()], nonfinite=BASE + 2)
+    _refused(zs.ZS3_EALIAS, "overlap", _clip, [_t(out=None), _t(out=None)])                    # the same tensor twice
+    _refused(zs.ZS3_EALIAS, "overlap", _clip, [_t(out=BASE)])                                  # its own place in another type
+    _refused(zs.ZS3_EALIAS, "overlap", _clip, [_t(out=BASE + 2, out_dtype="bf16")])            # its own place, shifted
+    _refused(zs.ZS3_EALIAS, "overlap", _clip, [_t(), _t(at=far, out=BASE + 100, out_dtype="bf16")])
+    _refused(zs.ZS3_EALIAS, "overlap", _clip, [_t(), _t(at=far, out=BASE + STEP + 396)])
+    _refused(zs.ZS3_EALIAS, "scale", _clip, [_t(out=None)], scale=BASE + 196)
+    _refused(zs.ZS3_EALIAS, "nonfinite", _clip, [_t(out=None)], nonfinite=BASE)
+    f = zs.lib().zs3_clip_tensors
+    assert f(1, None, BASE, None, None) == zs.ZS3_EINVAL
+    assert f(-1, None, BASE, None, None) == zs.ZS3_EINVAL
+
+
+def test_accumulate_refusals():
+    for call in (_acc, _fused):
+        for d in ("bf16", "fp16", 0):
+            _refused(zs.ZS3_EDTYPE, "out_dtype", call, [_t(out_dtype=d)])
+        _refused(zs.ZS3_EINVAL, "out is NULL", call, [_t(out=None)])
+        _refused(zs.ZS3_EINVAL, "out is NULL or not", call, [_t(out=BASE + STEP + 2)])
+        _refused(zs.ZS3_EALIAS, "overlap", call, [_t(), _t()])
+        _refused(zs.ZS3_EALIAS, "overlap", call, [_t(dtype="fp32", out=BASE)])
+        _refused(zs.ZS3_EALIAS, "overlap", call, [_t(out=BASE + 196)])
+    for f in (math.inf, math.nan, 1e39):
+        _refused(zs.ZS3_EINVAL, "factor", _acc, [_t()], factor=f)
+
+
+def test_overlaps_are_found_in_any_order():
+    """Random lists of apart ranges are taken, and refused once any two of them touch."""
+    import random
+    rng = random.Random(5)
+    for _ in range(200):
+        n = rng.randint(2, 12)
+        sizes = [rng.randint(1, 50) for _ in range(n)]
+        at, cells = BASE, []
+        for s in sizes:                       # a gradient of 2 * s bytes and an accumulator of 4 * s, apart by a word or not at all
+            cells.append([at, at + 2 * s + (2 * s) % 4])
+            at = cells[-1][1] + 4 * s + rng.choice([0, 4, 64])
+        order = list(range(n))
+        rng.shuffle(order)
+        i, j = rng.sample(range(n), 2)
+        for a_of, b_of in ((0, 1), (1, 1), (1, 0)):       # make tensor i's one array reach into j's other
+            moved = [list(c) for c in cells]
+            moved[i][a_of] = cells[j][b_of] + (4 * sizes[j] - 4 if b_of else 2 * ((sizes[j] - 1) // 2) // 4 * 4)
+            ts = [_t(numel=sizes[k], grad=moved[k][0], out=moved[k][1]) for k in order]
+            _refused(zs.ZS3_EALIAS, "overlap", _acc, ts)

@@ -1,7 +1,8 @@
 """Python binding of libzs3, the ZeRO-3 shard-step library for MI355X.
 
 Argument marshalling only: every function below has the name of a C entry
-point in ``include/zs3.h`` or ``include/zs3_lowbit.h`` and forwards to it through ctypes.  Device
+point in ``include/zs3.h``, ``include/zs3_lowbit.h`` or ``include/zs3_grads.h`` and forwards to it
+through ctypes.  Device
 buffers may be given as torch tensors (their data pointers are passed) or as
 raw integer device addresses; ``stream`` may be a ``torch.cuda.Stream``, a
 raw ``hipStream_t`` integer, or ``None`` for torch's current stream.  A
@@ -42,9 +43,10 @@ ZS3_GATHER_CURRENT, ZS3_GATHER_PREFETCH = 0, 1
 
 ZS3_EXP_AVG, ZS3_EXP_AVG_SQ = 1, 2
 ZS3_ROUND_NEAREST, ZS3_ROUND_STOCHASTIC = 0, 1
+ZS3_NORM_2, ZS3_NORM_INF = 1, 2
 
 DTYPES = {"fp16": ZS3_FP16, "bf16": ZS3_BF16}
-_DTYPES_LOWBIT = dict(DTYPES, fp32=ZS3_FP32)        # gradients and read moments there
+_DTYPES_LOWBIT = dict(DTYPES, fp32=ZS3_FP32)        # gradients and read moments there, gradient lists
 
 # Every exported symbol of include/zs3.h.
 EXPORTS = (
@@ -65,6 +67,11 @@ EXPORTS = (
 EXPORTS_LOWBIT = (
     "zs3_adamw_tensors", "zs3_moment8_bytes", "zs3_moment8_read", "zs3_mx4_sizes", "zs3_gather_coalesced_mx4",
     "zs3_reduce_scatter_coalesced_mx4",
+)
+
+# And of include/zs3_grads.h.
+EXPORTS_GRADS = (
+    "zs3_norm_workspace_bytes", "zs3_grad_norm_tensors", "zs3_norm_finalize", "zs3_clip_tensors", "zs3_accumulate_tensors",
 )
 
 
@@ -115,6 +122,36 @@ class zs3_moment8(ctypes.Structure):
         ("out", ctypes.c_void_p),
         ("kind", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class zs3_grad_tensor(ctypes.Structure):
+    _fields_ = [
+        ("numel", ctypes.c_int64),
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("shared", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class zs3_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("world", ctypes.c_int32),
+        ("finalize", ctypes.c_int32),
+        ("max_norm", ctypes.c_double),
+        ("loss_scale", ctypes.c_double),
+        ("sums", ctypes.c_void_p),
+        ("norm", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("nonfinite", ctypes.c_void_p),
+        ("tensor_norms", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
     ]
 
 
@@ -182,6 +219,12 @@ _SIGNATURES = {
     "zs3_reduce_scatter_coalesced_mx4": (_c_i32, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _p_i64, ctypes.POINTER(_c_p),
                                                   _c_p, ctypes.POINTER(_c_p), _c_p, _c_p, _c_i32, ctypes.c_uint64,
                                                   _c_p]),
+    "zs3_norm_workspace_bytes": (_c_i32, [_c_i32, ctypes.POINTER(zs3_grad_tensor), _p_i64]),
+    "zs3_grad_norm_tensors": (_c_i32, [_c_i32, ctypes.POINTER(zs3_grad_tensor), ctypes.POINTER(zs3_norm_args), _c_p]),
+    "zs3_norm_finalize": (_c_i32, [ctypes.POINTER(zs3_norm_args), _c_p]),
+    "zs3_clip_tensors": (_c_i32, [_c_i32, ctypes.POINTER(zs3_grad_tensor), _c_p, _c_p, _c_p]),
+    "zs3_accumulate_tensors": (_c_i32, [_c_i32, ctypes.POINTER(zs3_grad_tensor), ctypes.c_double, _c_i32,
+                                        ctypes.POINTER(zs3_norm_args), _c_p]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -547,6 +590,72 @@ def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, d
     _check(lib().zs3_reduce_scatter_coalesced_mx4(layout, rank, _dtype_lowbit(dtype), mode, len(ds_ids), _i64s(ds_ids),
                                                   g, _ptr(send), r, _ptr(grad_flat), _ptr(partials), int(rounding),
                                                   int(seed), _stream(stream)))
+
+
+# ------------------------------------------------ gradients over a tensor list
+
+def zs3_grad_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
+    """The list that the norm, the clip and the accumulation take: one dict a
+    tensor with numel, grad, dtype and, where they differ from these, out=None,
+    out_dtype=None (dtype, or "fp32" for an accumulator), shared=False.  It holds
+    addresses only: a caller keeps it for as long as its buffers stay where they are."""
+    out = (zs3_grad_tensor * max(1, len(tensors)))()
+    for o, t in zip(out, tensors):
+        o.numel, o.grad, o.out = int(t["numel"]), _ptr(t["grad"]), _ptr(t.get("out"))
+        o.dtype = _dtype_lowbit(t["dtype"])
+        o.out_dtype = o.dtype if t.get("out_dtype") is None else _dtype_lowbit(t["out_dtype"])
+        o.shared = int(bool(t.get("shared", False)))
+    out.count = len(tensors)
+    return out
+
+
+def _grad_list(tensors):
+    arr = tensors if isinstance(tensors, ctypes.Array) else zs3_grad_tensor_list(tensors)
+    return getattr(arr, "count", len(arr)), arr
+
+
+def zs3_norm_workspace_bytes(tensors) -> int:
+    b = ctypes.c_int64()
+    n, arr = _grad_list(tensors)
+    _check(lib().zs3_norm_workspace_bytes(n, arr, ctypes.byref(b)))
+    return b.value
+
+
+def zs3_norm_args_of(*, sums, workspace=None, workspace_bytes: Optional[int] = None, kind: int = ZS3_NORM_2, rank: int = 0,
+                     world: int = 1, finalize: bool = True, max_norm: float = 1.0, loss_scale: float = 1.0, norm=None,
+                     scale=None, nonfinite=None, tensor_norms=None) -> zs3_norm_args:
+    """What a norm is told and where it goes.  Addresses only, as
+    ``zs3_grad_tensor_list``; a tensor given as the workspace brings its bytes."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "data_ptr") else 0
+    return zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale), _ptr(sums),
+                         _ptr(norm), _ptr(scale), _ptr(nonfinite), _ptr(tensor_norms), _ptr(workspace), int(workspace_bytes))
+
+
+def _norm_args(a) -> zs3_norm_args:
+    return a if isinstance(a, zs3_norm_args) else zs3_norm_args_of(**a)
+
+
+def zs3_grad_norm_tensors(tensors, norm, stream=None) -> None:
+    """``tensors``: what ``zs3_grad_tensor_list`` gives, or the dicts; ``norm``:
+    what ``zs3_norm_args_of`` gives, or a dict of its arguments."""
+    n, arr = _grad_list(tensors)
+    _check(lib().zs3_grad_norm_tensors(n, arr, ctypes.byref(_norm_args(norm)), _stream(stream)))
+
+
+def zs3_norm_finalize(norm, stream=None) -> None:
+    _check(lib().zs3_norm_finalize(ctypes.byref(_norm_args(norm)), _stream(stream)))
+
+
+def zs3_clip_tensors(tensors, scale, nonfinite=None, stream=None) -> None:
+    n, arr = _grad_list(tensors)
+    _check(lib().zs3_clip_tensors(n, arr, _ptr(scale), _ptr(nonfinite), _stream(stream)))
+
+
+def zs3_accumulate_tensors(tensors, factor: float = 1.0, first: bool = False, norm=None, stream=None) -> None:
+    n, arr = _grad_list(tensors)
+    _check(lib().zs3_accumulate_tensors(n, arr, float(factor), int(bool(first)),
+                                        ctypes.byref(_norm_args(norm)) if norm is not None else None, _stream(stream)))
 
 
 # ------------------------------------------------------------- coordinator

@@ -1,0 +1,423 @@
+// HIP kernels of the gradient-list operators for gfx950 (MI355X): the global norm
+// of tensors that lie anywhere, their product with the clip scale, and their sum
+// over micro-batches in fp32 with the norm of the sum.
+//
+// All of it streams through HBM once: 2 or 4 bytes read an element for the norm, 2
+// to 8 moved for the clip, 6 to 12 for the accumulation.  Squares are taken and added
+// in double, where the square of any fp32 value is exact or off by 2^-53 of itself and
+// nothing overflows; at the rate of HBM that is 5 double multiply-adds a CU and
+// clock of the 64 it has.
+//
+// Floating point: compiled with -ffp-contract=off, so every expression is the
+// sequence of operations it spells; fused multiply-adds are written as such.
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "grads.hpp"
+#include "zs3_internal.hpp"
+
+namespace zs3 {
+namespace {
+
+constexpr int kFP32 = 3;
+constexpr int kSum = 1, kMax = 2;          // ZS3_NORM_2, ZS3_NORM_INF
+
+typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u2h __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u4h __attribute__((ext_vector_type(4), aligned(2)));
+
+// ------------------------------------------------------------ elements
+
+template <int D>
+using Elem = std::conditional_t<D == kFP32, float, uint16_t>;
+
+template <int D>
+__device__ __forceinline__ float widen(Elem<D> x) {
+    if constexpr (D == kFP32) return x;
+    else if constexpr (D == kFP16) return static_cast<float>(__builtin_bit_cast(_Float16, x));
+    else return __uint_as_float(static_cast<uint32_t>(x) << 16);
+}
+
+// Round to nearest, ties to even; NaN stays NaN.
+template <int D>
+__device__ __forceinline__ Elem<D> narrow(float f) {
+    if constexpr (D == kFP32) return f;
+    else if constexpr (D == kFP16) return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+    else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
+
+// V neighbouring elements (V = 4 or 8) as they come from memory, at any element.
+template <int D, int V>
+struct Raw {
+    using H = std::conditional_t<V == 4, u2h, u4h>;
+    H h;
+    __device__ void load(const uint16_t* p) { h = __builtin_nontemporal_load(reinterpret_cast<const H*>(p)); }
+    __device__ float get(int q) const {
+        return widen<D>(static_cast<uint16_t>((q & 1) ? h[q >> 1] >> 16 : h[q >> 1] & 0xffffu));
+    }
+};
+template <int V>
+struct Raw<kFP32, V> {
+    f4 f[V / 4];
+    __device__ void load(const float* p) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) f[i] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(p) + i);
+    }
+    __device__ float get(int q) const { return f[q / 4][q % 4]; }
+};
+
+template <int D, int V>
+__device__ __forceinline__ void store(Elem<D>* p, const float (&x)[V]) {
+    if constexpr (D == kFP32) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            __builtin_nontemporal_store(f4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]}, reinterpret_cast<f4*>(p) + i);
+    } else {
+        using H = std::conditional_t<V == 4, u2h, u4h>;
+        H h;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) h[i] = narrow<D>(x[2 * i]) | static_cast<uint32_t>(narrow<D>(x[2 * i + 1])) << 16;
+        __builtin_nontemporal_store(h, reinterpret_cast<H*>(p));
+    }
+}
+
+// ------------------------------------------------------------ sums
+
+// A thread's share of a sum: of squares, or the largest magnitude (as integers
+// NaN is above infinity above the rest).
+template <int KIND>
+struct Part;
+template <>
+struct Part<0> {
+    __device__ void add(float) {}
+    __device__ double value() const { return 0.0; }
+};
+template <>
+struct Part<kSum> {
+    double s = 0.0;
+    __device__ void add(float x) {
+        const double d = x;
+        s = __builtin_fma(d, d, s);
+    }
+    __device__ double value() const { return s; }
+};
+template <>
+struct Part<kMax> {
+    uint32_t top = 0;
+    __device__ void add(float x) {
+        const uint32_t m = __float_as_uint(x) & 0x7fffffffu;
+        top = m > top ? m : top;
+    }
+    __device__ double value() const { return __uint_as_float(top); }
+};
+
+template <int KIND>
+__device__ __forceinline__ double join(double a, double b) {
+    if constexpr (KIND == kMax) return b > a || b != b ? b : a;      // NaN stays
+    else return a + b;
+}
+__device__ __forceinline__ double join(int kind, double a, double b) {
+    return kind == kMax ? join<kMax>(a, b) : join<kSum>(a, b);
+}
+
+template <int KIND>
+__device__ __forceinline__ double wave_join(double x) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x = join<KIND>(x, __shfl_xor(x, o, 64));
+    return x;
+}
+
+// Over the workgroup; every thread gets it.  `sh` is free again afterwards.
+template <int KIND>
+__device__ __forceinline__ double group_join(double x, double* sh) {
+    x = wave_join<KIND>(x);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = sh[0];
+#pragma unroll
+    for (int w = 1; w < kGrBlock / 64; ++w) x = join<KIND>(x, sh[w]);
+    __syncthreads();
+    return x;
+}
+
+// The end of the norm from the sums (see the header's definition).
+__device__ void end_of_norm(const NormEnd& e, double own, double shared) {
+    double total = 0.0;
+    for (int v = 0; v < e.world; ++v) total = join(e.kind, total, v == e.rank ? own : e.sums[v]);
+    total = join(e.kind, total, shared);
+    const bool bad = !(__builtin_fabs(total) <= 1.7976931348623157e308);
+    const double norm = (e.kind == kMax ? total : __builtin_sqrt(total)) / e.loss_scale;
+    double coef = e.max_norm / (norm + 1e-6);
+    if (coef > 1.0) coef = 1.0;
+    *e.norm = norm;
+    *e.nonfinite = bad ? 1 : 0;
+    *e.scale = bad ? __builtin_nanf("") : static_cast<float>(coef / e.loss_scale);
+}
+
+// ------------------------------------------------------------ tiles
+
+enum Op { kNorm = 1, kClip = 2, kSet = 3, kAdd = 4 };
+
+// The list's tensor that tile b belongs to: each lane compares a prefix of every
+// 64 and the wave counts them.
+template <class PLAN>
+__device__ __forceinline__ int find_tensor(const PLAN& p, int32_t b, int lane) {
+    constexpr int kMost = sizeof(p.first_tile) / sizeof(p.first_tile[0]) - 1;
+    int past = 0;
+#pragma unroll
+    for (int s = 0; s < kMost; s += 64) {
+        const int i = s + lane;
+        past += __builtin_popcountll(__ballot(i < p.n && p.first_tile[i < kMost ? i + 1 : kMost] <= b));
+    }
+    return __builtin_amdgcn_readfirstlane(past);
+}
+
+// One tile: positions [0, T) from a line of the main array on, of which [lo, hi)
+// are the tensor's.  `grad` and `out` point at position 0.
+template <int OP, int KIND, int G, int O>
+__device__ __forceinline__ void tile(const Elem<G>* grad, Elem<O>* out, int lo, int hi, float f, Part<KIND>& part) {
+    constexpr int V = (OP == kNorm ? G : O) == kFP32 ? 4 : 8;      // elements of a 16-byte vector of the main array
+    Raw<G, V> x[kGrRuns];
+    Raw<kFP32, V> a[kGrRuns];
+    const int p0 = V * threadIdx.x;
+    constexpr int kStep = V * kGrBlock;
+    auto one = [&](float v, float old) {
+        float y = v;
+        if constexpr (OP == kClip || OP == kSet) y = v * f;
+        // the product is rounded to fp32, then to fp16: left to itself the compiler takes
+        // the instruction that multiplies and rounds once (another value near ties)
+        if constexpr (OP == kClip && O == kFP16) asm("" : "+v"(y));
+        if constexpr (OP == kAdd) y = __builtin_fmaf(f, v, old);
+        part.add(y);
+        return y;
+    };
+#pragma unroll
+    for (int k = 0; k < kGrRuns; ++k) {
+        const int p = p0 + k * kStep;
+        if (p >= lo && p + V <= hi) {
+            x[k].load(grad + p);
+            if constexpr (OP == kAdd) a[k].load(out + p);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kGrRuns; ++k) {
+        const int p = p0 + k * kStep;
+        if (p >= lo && p + V <= hi) {
+            float y[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                if constexpr (OP == kAdd) y[q] = one(x[k].get(q), a[k].get(q));
+                else y[q] = one(x[k].get(q), 0.0f);
+            }
+            if constexpr (OP != kNorm) store<O>(out + p, y);
+        } else if (p + V > lo && p < hi) {
+            for (int q = 0; q < V; ++q) {
+                if (p + q < lo || p + q >= hi) continue;
+                float old = 0.0f;
+                if constexpr (OP == kAdd) old = out[p + q];
+                const float y = one(widen<G>(grad[p + q]), old);
+                if constexpr (OP != kNorm) out[p + q] = narrow<O>(y);
+            }
+        }
+    }
+}
+
+template <int OP, int KIND, int G, int O>
+__device__ __forceinline__ void typed_tile(const void* grad, void* out, int32_t t, int32_t tiles, uint32_t last, float f,
+                                           Part<KIND>& part) {
+    const uintptr_t main = reinterpret_cast<uintptr_t>(OP == kNorm ? grad : out);
+    constexpr int kSize = sizeof(std::conditional_t<OP == kNorm, Elem<G>, Elem<O>>);
+    constexpr int T = static_cast<int>(gr_tile(kSize));
+    const int head = static_cast<int>(main & (kGrLine - 1)) / kSize;
+    const int64_t at = int64_t(t) * T - head;
+    tile<OP, KIND, G, O>(static_cast<const Elem<G>*>(grad) + at, static_cast<Elem<O>*>(out) + at, t == 0 ? head : 0,
+                         t + 1 == tiles ? static_cast<int>(last) : T, f, part);
+}
+
+// A workgroup's tiles, one behind the other; KIND 0: no sums.
+template <int OP, int KIND, class PLAN>
+__device__ __forceinline__ void run(const PLAN& plan, float f, const NormParts& parts) {
+    __shared__ double sh[kGrBlock / 64];
+    const int32_t b = static_cast<int32_t>(blockIdx.x), all = plan.first_tile[plan.n];
+    const int32_t t0 = b * plan.per, t1 = t0 + plan.per < all ? t0 + plan.per : all;
+    int s = find_tensor(plan, t0, threadIdx.x & 63);
+    double own = 0.0, shared = 0.0;
+    Part<KIND> part;
+    auto close = [&]() {        // the workgroup's part of tensor s is complete
+        if constexpr (KIND != 0) {
+            const double x = part.value();
+            if (plan.meta[s] >> 20 & 1) shared = join<KIND>(shared, x);
+            else own = join<KIND>(own, x);
+            if (parts.tensors != nullptr) {
+                const double y = group_join<KIND>(x, sh);
+                if (threadIdx.x == 0) parts.tensors[b + s] = y;
+            }
+            part = Part<KIND>();
+        }
+    };
+    for (int32_t t = t0; t < t1; ++t) {
+        if (t >= plan.first_tile[s + 1]) {
+            close();
+            do ++s;
+            while (t >= plan.first_tile[s + 1]);
+        }
+        const uint32_t meta = plan.meta[s], last = meta & 0xffffu;
+        const int32_t f0 = plan.first_tile[s], n = plan.first_tile[s + 1] - f0;
+        const int g = meta >> 16 & 3, o = meta >> 18 & 3;
+        const void* grad = plan.grad[s];
+        if constexpr (OP == kNorm) {
+            if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP16>(grad, nullptr, t - f0, n, last, f, part);
+            else if (g == kBF16) typed_tile<OP, KIND, kBF16, kBF16>(grad, nullptr, t - f0, n, last, f, part);
+            else typed_tile<OP, KIND, kFP32, kFP32>(grad, nullptr, t - f0, n, last, f, part);
+        } else {
+            void* out = plan.out[s];
+            if constexpr (OP == kClip) {
+                if (out == grad && f == 1.0f) continue;
+                if (o == kFP16) {
+                    if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP16>(grad, out, t - f0, n, last, f, part);
+                    else if (g == kBF16) typed_tile<OP, KIND, kBF16, kFP16>(grad, out, t - f0, n, last, f, part);
+                    else typed_tile<OP, KIND, kFP32, kFP16>(grad, out, t - f0, n, last, f, part);
+                } else if (o == kBF16) {
+                    if (g == kFP16) typed_tile<OP, KIND, kFP16, kBF16>(grad, out, t - f0, n, last, f, part);
+                    else if (g == kBF16) typed_tile<OP, KIND, kBF16, kBF16>(grad, out, t - f0, n, last, f, part);
+                    else typed_tile<OP, KIND, kFP32, kBF16>(grad, out, t - f0, n, last, f, part);
+                } else {
+                    if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP32>(grad, out, t - f0, n, last, f, part);
+                    else if (g == kBF16) typed_tile<OP, KIND, kBF16, kFP32>(grad, out, t - f0, n, last, f, part);
+                    else typed_tile<OP, KIND, kFP32, kFP32>(grad, out, t - f0, n, last, f, part);
+                }
+            } else {
+                if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP32>(grad, out, t - f0, n, last, f, part);
+                else if (g == kBF16) typed_tile<OP, KIND, kBF16, kFP32>(grad, out, t - f0, n, last, f, part);
+                else typed_tile<OP, KIND, kFP32, kFP32>(grad, out, t - f0, n, last, f, part);
+            }
+        }
+    }
+    if constexpr (KIND != 0) {
+        close();
+        own = group_join<KIND>(own, sh);
+        shared = group_join<KIND>(shared, sh);
+        if (threadIdx.x == 0) {
+            parts.groups[2 * b] = own;
+            parts.groups[2 * b + 1] = shared;
+        }
+    }
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const NormParts parts) {
+    run<kNorm, KIND>(plan, 1.0f, parts);
+}
+
+__global__ __launch_bounds__(kGrBlock) void k_clip(const WritePlan plan, const float* __restrict__ scale,
+                                                   const int32_t* __restrict__ nonfinite) {
+    if (nonfinite != nullptr && *nonfinite != 0) return;
+    run<kClip, 0>(plan, *scale, NormParts{});
+}
+
+template <int OP, int KIND>
+__global__ __launch_bounds__(kGrBlock) void k_accumulate(const WritePlan plan, float f, const NormParts parts) {
+    run<OP, KIND>(plan, f, parts);
+}
+
+// ------------------------------------------------------------ ends
+
+struct TensorTiles {
+    int32_t n, per;
+    int32_t first_tile[kNormTensors + 1];
+};
+
+// A wave a tensor.
+__global__ __launch_bounds__(kGrBlock) void k_tensor_norms(const TensorTiles p, int32_t kind, const double* __restrict__ parts,
+                                                           double* __restrict__ tensor_norms) {
+    const int s = static_cast<int>(blockIdx.x) * (kGrBlock / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (s >= p.n) return;
+    const int32_t f0 = p.first_tile[s], f1 = p.first_tile[s + 1];
+    double x = 0.0;
+    if (f1 > f0)
+        for (int32_t b = f0 / p.per + lane; b <= (f1 - 1) / p.per; b += 64) x = join(kind, x, parts[b + s]);
+    x = kind == kMax ? wave_join<kMax>(x) : wave_join<kSum>(x);
+    if (lane == 0) tensor_norms[s] = kind == kMax ? x : __builtin_sqrt(x);
+}
+
+__global__ __launch_bounds__(kGrBlock) void k_norm_end(const double* __restrict__ groups, int64_t n, const NormEnd e) {
+    __shared__ double sh[kGrBlock / 64];
+    double own = 0.0, shared = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kGrBlock) {
+        own = join(e.kind, own, groups[2 * i]);
+        shared = join(e.kind, shared, groups[2 * i + 1]);
+    }
+    if (e.kind == kMax) {
+        own = group_join<kMax>(own, sh);
+        shared = group_join<kMax>(shared, sh);
+    } else {
+        own = group_join<kSum>(own, sh);
+        shared = group_join<kSum>(shared, sh);
+    }
+    if (threadIdx.x == 0) {
+        e.sums[e.rank] = own;
+        e.sums[e.world] = shared;
+        if (e.finalize) end_of_norm(e, own, shared);
+    }
+}
+
+__global__ void k_norm_finalize_sums(const NormEnd e) { end_of_norm(e, e.sums[e.rank], e.sums[e.world]); }
+
+}  // namespace
+
+// ---------------------------------------------------------------- launchers
+
+// Launches without the copies of a plan that a call by value makes.
+template <typename... A>
+static hipError_t launch(void (*kernel)(A...), int64_t groups, int threads, hipStream_t stream,
+                         const std::remove_const_t<A>&... args) {
+    void* list[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<uint32_t>(groups)), dim3(threads), list, 0, stream);
+}
+
+template <class PLAN>
+static int64_t groups_of(const PLAN& p) {
+    return (int64_t(p.first_tile[p.n]) + p.per - 1) / p.per;
+}
+
+hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, hipStream_t stream) {
+    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups_of(plan), kGrBlock, stream, plan, parts);
+}
+
+hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream) {
+    return launch(k_clip, groups_of(plan), kGrBlock, stream, plan, scale, nonfinite);
+}
+
+template <int OP>
+static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float factor, const NormParts& parts, hipStream_t stream) {
+    auto kernel = kind == 0 ? k_accumulate<OP, 0> : kind == kMax ? k_accumulate<OP, kMax> : k_accumulate<OP, kSum>;
+    return launch(kernel, groups_of(plan), kGrBlock, stream, plan, factor, parts);
+}
+
+hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, const NormParts& parts,
+                             hipStream_t stream) {
+    return first ? accumulate_launch<kSet>(kind, plan, factor, parts, stream)
+                 : accumulate_launch<kAdd>(kind, plan, factor, parts, stream);
+}
+
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, const double* parts,
+                               double* tensor_norms, hipStream_t stream) {
+    TensorTiles p;
+    p.n = n;
+    p.per = per;
+    for (int32_t i = 0; i <= n; ++i) p.first_tile[i] = first_tile[i];
+    constexpr int kWaves = kGrBlock / 64;
+    return launch(k_tensor_norms, (n + kWaves - 1) / kWaves, kGrBlock, stream, p, kind, parts, tensor_norms);
+}
+
+hipError_t launch_norm_end(const double* groups, int64_t n_groups, const NormEnd& end, hipStream_t stream) {
+    return launch(k_norm_end, 1, kGrBlock, stream, groups, n_groups, end);
+}
+
+hipError_t launch_norm_finalize(const NormEnd& end, hipStream_t stream) {
+    return launch(k_norm_finalize_sums, 1, 1, stream, end);
+}
+
+}  // namespace zs3

@@ -1,0 +1,88 @@
+// Internal declarations of the gradient-list operators: the global norm over a
+// list of tensors, clipping it, and accumulating it in fp32.  As with the low-bit
+// operators a call's description travels in the kernel arguments (under 4 KB, longer
+// lists split over launches): nothing is allocated, uploaded or kept.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+
+namespace zs3 {
+
+constexpr int kGrBlock = 256;              // threads of a workgroup (4 waves of 64)
+constexpr int kGrRuns = 2;                 // 16-byte vectors of a thread and tile
+constexpr int64_t kGrTileBytes = int64_t(kGrBlock) * 16 * kGrRuns;
+constexpr int64_t kGrLine = 128;           // bytes of a cache line: tiles start at one
+
+// A tensor is cut into tiles of its main array, the one that is written (or, for
+// the norm, read): 8 KB of it each, starting at a line, so that a wave's accesses
+// cover whole lines whatever the tensor's address.  Element i is at position
+// head + i, head elements after the line that the array starts in.
+constexpr int64_t gr_tile(int64_t bytes_of_element) { return kGrTileBytes / bytes_of_element; }
+
+// Tensors of one launch: as many as 4 KB of kernel arguments hold.
+constexpr int kNormTensors = 224;
+constexpr int kWriteTensors = 152;
+
+// meta: positions of the last tile that are the tensor's (1 .. gr_tile), and types.
+constexpr uint32_t gr_meta(int64_t last, int32_t dtype, int32_t out_dtype, bool shared) {
+    return static_cast<uint32_t>(last) | static_cast<uint32_t>(dtype) << 16 | static_cast<uint32_t>(out_dtype) << 18 |
+           (shared ? 1u << 20 : 0u);
+}
+
+struct NormPlan {
+    int32_t n;
+    int32_t per;            // tiles of a workgroup, one behind the other
+    int32_t first_tile[kNormTensors + 1];
+    uint32_t meta[kNormTensors];
+    const void* grad[kNormTensors];
+};
+static_assert(sizeof(NormPlan) <= 3840, "the plan has to fit the kernel arguments");
+
+struct WritePlan {
+    int32_t n;
+    int32_t per;
+    int32_t first_tile[kWriteTensors + 1];
+    uint32_t meta[kWriteTensors];
+    const void* grad[kWriteTensors];
+    void* out[kWriteTensors];
+};
+static_assert(sizeof(WritePlan) <= 3840, "the plan has to fit the kernel arguments");
+
+// Workgroups of a launch that sums: each takes a run of tiles, so that there are
+// few partial results and the run's sum stays in registers.
+constexpr int kNormGroups = 2048;
+
+// What a summing launch leaves in the workspace: two values a workgroup (tensors
+// that are not shared, and shared ones), and, for the norms of single tensors, one
+// for every workgroup and tensor that meet: workgroup b's part of tensor s is at
+// b + s, since from one such pair to the next b or s grows.
+struct NormParts {
+    double* groups;         // [2 * workgroup] of this launch
+    double* tensors;        // [workgroup + tensor] of this launch, or null
+};
+
+struct NormEnd {
+    int32_t kind, rank, world, finalize;
+    double max_norm, loss_scale;
+    double* sums;
+    double* norm;
+    float* scale;
+    int32_t* nonfinite;
+};
+
+hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, hipStream_t stream);
+hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream);
+// kind 0: without sums
+hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, const NormParts& parts,
+                             hipStream_t stream);
+// tensor_norms[s] of the launch's n tensors from its parts.
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, const double* parts,
+                               double* tensor_norms, hipStream_t stream);
+// groups[0 .. 2 * n_groups) into the sums, and the end of the norm where asked.
+hipError_t launch_norm_end(const double* groups, int64_t n_groups, const NormEnd& end, hipStream_t stream);
+// The end of the norm from the sums alone.
+hipError_t launch_norm_finalize(const NormEnd& end, hipStream_t stream);
+
+}  // namespace zs3

@@ -25,52 +25,65 @@ struct Launch {
     std::vector<uint32_t> meta;
     std::vector<const void*> grad;
     std::vector<void*> out;
-    NormParts parts;
+    double* entries;        // of this launch
+    double* tensors;        // the norm's parts of single tensors
 };
 std::vector<Launch> launches;
 struct TensorNorms {
-    int32_t kind, n, per;
+    int32_t kind, n, per, skew;
     std::vector<int32_t> first_tile;
     const double* parts;
     double* out;
 };
 std::vector<TensorNorms> tensor_norms;
+struct Join {
+    const double* entries;
+    int64_t n, per;
+    double* to;
+};
+std::vector<Join> joins;
 struct End {
-    const double* groups;
+    const double* entries;
     int64_t n;
     NormEnd end;
 };
 std::vector<End> ends;
 
 template <class PLAN>
-Launch copy(const PLAN& p, bool written, int32_t kind, const NormParts& parts) {
-    Launch l{written, kind, p.n, p.per, {}, {}, {}, {}, parts};
+Launch copy(const PLAN& p, bool written, int32_t kind, int32_t per, double* entries, double* tensors) {
+    Launch l{written, kind, p.n, per, {}, {}, {}, {}, entries, tensors};
     l.first_tile.assign(p.first_tile, p.first_tile + p.n + 1);
     l.meta.assign(p.meta, p.meta + p.n);
     l.grad.assign(p.grad, p.grad + p.n);
+    for (size_t i = p.n + 1; i < sizeof p.first_tile / sizeof p.first_tile[0]; ++i)      // the search counts on it
+        if (p.first_tile[i] != INT32_MAX) l.n = -1;
     return l;
 }
 hipError_t launch_norm(int32_t kind, const NormPlan& p, const NormParts& parts, hipStream_t) {
-    launches.push_back(copy(p, false, kind, parts));
+    launches.push_back(copy(p, false, kind, p.per, parts.entries, parts.tensors));
     return hipSuccess;
 }
 hipError_t launch_clip(const WritePlan& p, const float*, const int32_t*, hipStream_t) {
-    launches.push_back(copy(p, true, 0, NormParts{}));
+    launches.push_back(copy(p, true, 0, 1, nullptr, nullptr));
     launches.back().out.assign(p.out, p.out + p.n);
     return hipSuccess;
 }
-hipError_t launch_accumulate(int32_t kind, const WritePlan& p, float, bool, const NormParts& parts, hipStream_t) {
-    launches.push_back(copy(p, true, kind, parts));
+hipError_t launch_accumulate(int32_t kind, const WritePlan& p, float, bool, double* entries, hipStream_t) {
+    launches.push_back(copy(p, true, kind, 1, entries, nullptr));
     launches.back().out.assign(p.out, p.out + p.n);
     return hipSuccess;
 }
-hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, const double* parts, double* out,
-                               hipStream_t) {
-    tensor_norms.push_back({kind, n, per, {first_tile, first_tile + n + 1}, parts, out});
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, int32_t skew, const double* parts,
+                               double* out, hipStream_t) {
+    tensor_norms.push_back({kind, n, per, skew, {first_tile, first_tile + n + 1}, parts, out});
     return hipSuccess;
 }
-hipError_t launch_norm_end(const double* groups, int64_t n, const NormEnd& end, hipStream_t) {
-    ends.push_back({groups, n, end});
+hipError_t launch_join(int32_t, const double* entries, int64_t n, int64_t per, double* to, hipStream_t) {
+    joins.push_back({entries, n, per, to});
+    return hipSuccess;
+}
+hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end, hipStream_t) {
+    ends.push_back({entries, n, end});
     return hipSuccess;
 }
 hipError_t launch_norm_finalize(const NormEnd&, hipStream_t) { return hipSuccess; }
@@ -119,14 +132,14 @@ std::vector<zs3_grad_tensor> list(Rng& r, int32_t n, int64_t most, bool acc) {
 }
 
 // The elements of every tensor, launch by launch, as the kernels cut them.
-void hold(const std::vector<zs3_grad_tensor>& want, bool written, bool sums) {
+void hold(const std::vector<zs3_grad_tensor>& want, bool written) {
     size_t i = 0;
     for (const Launch& L : launches) {
         EXPECT(L.written == written && L.per >= 1 && L.n >= 1);
         EXPECT(L.first_tile[0] == 0);
         const int64_t all = L.first_tile[L.n], groups = (all + L.per - 1) / L.per;
         EXPECT(all > 0 && groups < (int64_t(1) << 24));
-        EXPECT(sums ? groups <= kNormGroups : L.per == 1);
+        EXPECT(written ? L.per == 1 : groups <= kNormGroups);
         for (int32_t s = 0; s < L.n; ++s, ++i) {
             if (i >= want.size()) {
                 EXPECT(false);
@@ -161,44 +174,52 @@ void hold(const std::vector<zs3_grad_tensor>& want, bool written, bool sums) {
 }
 
 void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a, bool written) {
-    hold(want, written, true);
+    hold(want, written);
     const double* lo = static_cast<const double*>(a.workspace);
     const double* hi = lo + a.workspace_bytes / 8;
     std::set<const double*> places;
-    auto put = [&](const double* p) {
-        EXPECT(p >= lo && p < hi);
-        EXPECT(places.insert(p).second);
+    auto put = [&](const double* p, int64_t n) {       // the ends of n places that nothing else may take
+        EXPECT(p >= lo && p + n <= hi);
+        for (int64_t i = 0; i < n; i += n > 100000 ? 997 : 1) EXPECT(places.insert(p + i).second);
+        if (n > 1) places.insert(p + n - 1);
     };
-    EXPECT(ends.size() == 1);
-    int64_t groups = 0;
+    EXPECT(ends.size() == 1 && joins.size() <= 1);
+    int64_t used = 0;
     for (const Launch& L : launches) {
-        const int64_t all = L.first_tile[L.n], n = (all + L.per - 1) / L.per;
-        EXPECT(L.kind == a.kind && L.parts.groups == ends[0].groups + 2 * groups);
-        for (int64_t b = 0; b < 2 * n; ++b) put(L.parts.groups + b);
-        groups += n;
-        EXPECT((L.parts.tensors != nullptr) == (a.tensor_norms != nullptr));
-        if (L.parts.tensors == nullptr) continue;
+        const int64_t all = L.first_tile[L.n], groups = (all + L.per - 1) / L.per, entries = written ? all : 2 * groups;
+        EXPECT(L.kind == a.kind && L.entries == lo + used);
+        put(L.entries, entries);
+        used += entries;
+        EXPECT(written || (L.tensors != nullptr) == (a.tensor_norms != nullptr));
+        if (L.tensors == nullptr) continue;
         for (int32_t s = 0; s < L.n; ++s) {
             const int32_t f0 = L.first_tile[s], f1 = L.first_tile[s + 1];
-            if (f1 > f0)
-                for (int32_t b = f0 / L.per; b <= (f1 - 1) / L.per; ++b) put(L.parts.tensors + b + s);
+            if (f1 > f0) put(L.tensors + f0 / L.per + s, (f1 - 1) / L.per - f0 / L.per + 1);
         }
     }
-    EXPECT(ends[0].n == groups);
+    if (joins.empty()) {
+        EXPECT(used <= kEndEntries && ends[0].entries == lo && ends[0].n == used);
+    } else {
+        const Join& j = joins[0];
+        const int64_t groups = (used + j.per - 1) / j.per;
+        EXPECT(used > kEndEntries && j.entries == lo && j.n == used && groups <= kJoinGroups);
+        EXPECT(ends[0].entries == j.to && ends[0].n == 2 * groups && 2 * groups <= kEndEntries);
+        put(j.to, 2 * groups);
+    }
     if (a.tensor_norms == nullptr) {
         EXPECT(tensor_norms.empty());
         return;
     }
-    size_t done = 0, used = 0;
+    size_t done = 0, seen = 0;
     for (const TensorNorms& t : tensor_norms) {
-        EXPECT(t.out == a.tensor_norms + done);
+        EXPECT(t.out == a.tensor_norms + done && t.skew == (written ? 0 : 1));
         done += static_cast<size_t>(t.n);
         if (t.first_tile[t.n] == 0) continue;
-        EXPECT(used < launches.size());
-        const Launch& L = launches[used++];
-        EXPECT(t.parts == L.parts.tensors && t.n == L.n && t.per == L.per && t.first_tile == L.first_tile);
+        EXPECT(seen < launches.size());
+        const Launch& L = launches[seen++];
+        EXPECT(t.parts == (written ? L.entries : L.tensors) && t.n == L.n && t.per == L.per && t.first_tile == L.first_tile);
     }
-    EXPECT(done == want.size() && used == launches.size());
+    EXPECT(done == want.size() && seen == launches.size());
 }
 
 zs3_norm_args args(const std::vector<zs3_grad_tensor>& v, Rng& r) {
@@ -221,6 +242,7 @@ zs3_norm_args args(const std::vector<zs3_grad_tensor>& v, Rng& r) {
 void clear() {
     launches.clear();
     tensor_norms.clear();
+    joins.clear();
     ends.clear();
 }
 
@@ -230,6 +252,7 @@ int main() {
     Rng r{88172645463325252ull};
     float scale;
     for (int k = 0; k < 600; ++k) {
+        at = uintptr_t(1) << 40;
         const int32_t n = static_cast<int32_t>(k % 7 == 0 ? r.below(1200) : r.below(20));
         const int64_t most = k % 11 == 0 ? int64_t(1) << 34 : k % 5 == 0 ? 3000000000ll : 5000000;
         const auto plain = list(r, n, most, false), acc = list(r, n, most, true);
@@ -241,11 +264,11 @@ int main() {
         clear();
         where = "clip";
         EXPECT(zs3_clip_tensors(n, plain.data(), &scale, nullptr, nullptr) == ZS3_OK);
-        hold(plain, true, false);
+        hold(plain, true);
         clear();
         where = "accumulate";
         EXPECT(zs3_accumulate_tensors(n, acc.data(), 1.0, 0, nullptr, nullptr) == ZS3_OK);
-        hold(acc, true, false);
+        hold(acc, true);
         clear();
         where = "accumulate with the norm";
         a = args(acc, r);

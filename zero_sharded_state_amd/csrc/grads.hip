@@ -122,6 +122,12 @@ __device__ __forceinline__ double join(int kind, double a, double b) {
     return kind == kMax ? join<kMax>(a, b) : join<kSum>(a, b);
 }
 
+// A partial result in the workspace: its sign says whether its tensors are shared
+// (that of a NaN or a zero, too).
+__device__ __forceinline__ double entry(double x, bool shared) {
+    return shared ? -__builtin_fabs(x) : __builtin_fabs(x);
+}
+
 template <int KIND>
 __device__ __forceinline__ double wave_join(double x) {
 #pragma unroll
@@ -129,15 +135,15 @@ __device__ __forceinline__ double wave_join(double x) {
     return x;
 }
 
-// Over the workgroup; every thread gets it.  `sh` is free again afterwards.
-template <int KIND>
+// Over the workgroup of BLOCK threads; every thread gets it.  `sh` is free again afterwards.
+template <int KIND, int BLOCK>
 __device__ __forceinline__ double group_join(double x, double* sh) {
     x = wave_join<KIND>(x);
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
     __syncthreads();
     x = sh[0];
 #pragma unroll
-    for (int w = 1; w < kGrBlock / 64; ++w) x = join<KIND>(x, sh[w]);
+    for (int w = 1; w < BLOCK / 64; ++w) x = join<KIND>(x, sh[w]);
     __syncthreads();
     return x;
 }
@@ -160,70 +166,93 @@ __device__ void end_of_norm(const NormEnd& e, double own, double shared) {
 
 enum Op { kNorm = 1, kClip = 2, kSet = 3, kAdd = 4 };
 
-// The list's tensor that tile b belongs to: each lane compares a prefix of every
-// 64 and the wave counts them.
+// The list's tensor that tile b belongs to: each lane compares a prefix of every 64
+// (those past the list's end are larger than any tile) and the wave counts them.
 template <class PLAN>
 __device__ __forceinline__ int find_tensor(const PLAN& p, int32_t b, int lane) {
     constexpr int kMost = sizeof(p.first_tile) / sizeof(p.first_tile[0]) - 1;
     int past = 0;
 #pragma unroll
     for (int s = 0; s < kMost; s += 64) {
-        const int i = s + lane;
-        past += __builtin_popcountll(__ballot(i < p.n && p.first_tile[i < kMost ? i + 1 : kMost] <= b));
+        const int i = s + lane + 1;
+        past += __builtin_popcountll(__ballot(p.first_tile[i < kMost ? i : kMost] <= b && i <= kMost));
     }
     return __builtin_amdgcn_readfirstlane(past);
 }
 
+// An element's new value.
+template <int OP, int O>
+__device__ __forceinline__ float changed(float x, float f, float old) {
+    if constexpr (OP == kClip || OP == kSet) x = x * f;
+    // the product is rounded to fp32, then to fp16: left to itself the compiler takes
+    // the instruction that multiplies and rounds once (another value near ties)
+    if constexpr (OP == kClip && O == kFP16) asm("" : "+v"(x));
+    if constexpr (OP == kAdd) x = __builtin_fmaf(f, x, old);
+    return x;
+}
+
 // One tile: positions [0, T) from a line of the main array on, of which [lo, hi)
-// are the tensor's.  `grad` and `out` point at position 0.
-template <int OP, int KIND, int G, int O>
+// are the tensor's.  `grad` and `out` point at position 0.  All loads are issued
+// before any is used or any result stored (in place, the two arrays are one).  A
+// tensor's ends inside a vector are single elements of the first 2 V threads, in flight
+// beside the vectors (loaded by the vector's own thread, one behind the other, they took
+// several times a tile's time: 221 odd tensors of 117M elements in all 49 us against 41).
+template <int OP, int KIND, int G, int O, bool WHOLE>
 __device__ __forceinline__ void tile(const Elem<G>* grad, Elem<O>* out, int lo, int hi, float f, Part<KIND>& part) {
     constexpr int V = (OP == kNorm ? G : O) == kFP32 ? 4 : 8;      // elements of a 16-byte vector of the main array
-    Raw<G, V> x[kGrRuns];
-    Raw<kFP32, V> a[kGrRuns];
-    const int p0 = V * threadIdx.x;
     constexpr int kStep = V * kGrBlock;
-    auto one = [&](float v, float old) {
-        float y = v;
-        if constexpr (OP == kClip || OP == kSet) y = v * f;
-        // the product is rounded to fp32, then to fp16: left to itself the compiler takes
-        // the instruction that multiplies and rounds once (another value near ties)
-        if constexpr (OP == kClip && O == kFP16) asm("" : "+v"(y));
-        if constexpr (OP == kAdd) y = __builtin_fmaf(f, v, old);
-        part.add(y);
-        return y;
-    };
+    const int t = static_cast<int>(threadIdx.x);
+    int v0 = 0, v1 = 0, edge = 0;       // the whole vectors, and this thread's single element
+    bool single = false;
+    Elem<G> xe = {};
+    float ae = 0.0f;
+    if constexpr (!WHOLE) {
+        v0 = (lo + V - 1) / V * V;
+        v0 = v0 < hi ? v0 : hi;
+        v1 = hi / V * V;
+        v1 = v1 > v0 ? v1 : v0;
+        edge = t < V ? lo + t : v1 + t - V;
+        single = edge < (t < V ? v0 : hi) && t < 2 * V;
+        if (single) {
+            xe = grad[edge];
+            if constexpr (OP == kAdd) ae = out[edge];
+        }
+    }
+    Raw<G, V> x[kGrRuns] = {};
+    Raw<kFP32, V> a[kGrRuns] = {};
 #pragma unroll
     for (int k = 0; k < kGrRuns; ++k) {
-        const int p = p0 + k * kStep;
-        if (p >= lo && p + V <= hi) {
+        const int p = V * t + k * kStep;
+        if (WHOLE || (p >= v0 && p < v1)) {
             x[k].load(grad + p);
             if constexpr (OP == kAdd) a[k].load(out + p);
         }
     }
 #pragma unroll
     for (int k = 0; k < kGrRuns; ++k) {
-        const int p = p0 + k * kStep;
-        if (p >= lo && p + V <= hi) {
-            float y[V];
+        const int p = V * t + k * kStep;
+        float y[V];
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                if constexpr (OP == kAdd) y[q] = one(x[k].get(q), a[k].get(q));
-                else y[q] = one(x[k].get(q), 0.0f);
-            }
-            if constexpr (OP != kNorm) store<O>(out + p, y);
-        } else if (p + V > lo && p < hi) {
-            for (int q = 0; q < V; ++q) {
-                if (p + q < lo || p + q >= hi) continue;
-                float old = 0.0f;
-                if constexpr (OP == kAdd) old = out[p + q];
-                const float y = one(widen<G>(grad[p + q]), old);
-                if constexpr (OP != kNorm) out[p + q] = narrow<O>(y);
-            }
+        for (int q = 0; q < V; ++q) {
+            float old = 0.0f;
+            if constexpr (OP == kAdd) old = a[k].get(q);
+            y[q] = changed<OP, O>(x[k].get(q), f, old);
+            part.add(y[q]);         // of a vector that is not there, 0
+        }
+        if constexpr (OP != kNorm) {
+            if (WHOLE || (p >= v0 && p < v1)) store<O>(out + p, y);
+        }
+    }
+    if constexpr (!WHOLE) {
+        const float y = changed<OP, O>(widen<G>(xe), f, ae);
+        if (single) {
+            part.add(y);
+            if constexpr (OP != kNorm) out[edge] = narrow<O>(y);
         }
     }
 }
 
+// Tile t of a tensor's `tiles`.
 template <int OP, int KIND, int G, int O>
 __device__ __forceinline__ void typed_tile(const void* grad, void* out, int32_t t, int32_t tiles, uint32_t last, float f,
                                            Part<KIND>& part) {
@@ -231,14 +260,20 @@ __device__ __forceinline__ void typed_tile(const void* grad, void* out, int32_t 
     constexpr int kSize = sizeof(std::conditional_t<OP == kNorm, Elem<G>, Elem<O>>);
     constexpr int T = static_cast<int>(gr_tile(kSize));
     const int head = static_cast<int>(main & (kGrLine - 1)) / kSize;
+    const int lo = t == 0 ? head : 0, hi = t + 1 == tiles ? static_cast<int>(last) : T;
     const int64_t at = int64_t(t) * T - head;
-    tile<OP, KIND, G, O>(static_cast<const Elem<G>*>(grad) + at, static_cast<Elem<O>*>(out) + at, t == 0 ? head : 0,
-                         t + 1 == tiles ? static_cast<int>(last) : T, f, part);
+    const Elem<G>* g = static_cast<const Elem<G>*>(grad) + at;
+    Elem<O>* o = OP == kNorm ? nullptr : static_cast<Elem<O>*>(out) + at;
+    if (lo == 0 && hi == T) tile<OP, KIND, G, O, true>(g, o, lo, hi, f, part);
+    else tile<OP, KIND, G, O, false>(g, o, lo, hi, f, part);
 }
 
-// A workgroup's tiles, one behind the other; KIND 0: no sums.
-template <int OP, int KIND, class PLAN>
-__device__ __forceinline__ void run(const PLAN& plan, float f, const NormParts& parts) {
+// ------------------------------------------------------------ the norm
+// Bound by HBM.  A workgroup takes a run of tiles one behind the other and keeps its sum in
+// registers; 2048 workgroups, all that fit on the chip at once.
+
+template <int KIND>
+__global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const NormParts parts) {
     __shared__ double sh[kGrBlock / 64];
     const int32_t b = static_cast<int32_t>(blockIdx.x), all = plan.first_tile[plan.n];
     const int32_t t0 = b * plan.per, t1 = t0 + plan.per < all ? t0 + plan.per : all;
@@ -246,16 +281,14 @@ __device__ __forceinline__ void run(const PLAN& plan, float f, const NormParts& 
     double own = 0.0, shared = 0.0;
     Part<KIND> part;
     auto close = [&]() {        // the workgroup's part of tensor s is complete
-        if constexpr (KIND != 0) {
-            const double x = part.value();
-            if (plan.meta[s] >> 20 & 1) shared = join<KIND>(shared, x);
-            else own = join<KIND>(own, x);
-            if (parts.tensors != nullptr) {
-                const double y = group_join<KIND>(x, sh);
-                if (threadIdx.x == 0) parts.tensors[b + s] = y;
-            }
-            part = Part<KIND>();
+        const double x = part.value();
+        if (plan.meta[s] >> 20 & 1) shared = join<KIND>(shared, x);
+        else own = join<KIND>(own, x);
+        if (parts.tensors != nullptr) {
+            const double y = group_join<KIND, kGrBlock>(x, sh);
+            if (threadIdx.x == 0) parts.tensors[b + s] = y;
         }
+        part = Part<KIND>();
     };
     for (int32_t t = t0; t < t1; ++t) {
         if (t >= plan.first_tile[s + 1]) {
@@ -265,97 +298,133 @@ __device__ __forceinline__ void run(const PLAN& plan, float f, const NormParts& 
         }
         const uint32_t meta = plan.meta[s], last = meta & 0xffffu;
         const int32_t f0 = plan.first_tile[s], n = plan.first_tile[s + 1] - f0;
-        const int g = meta >> 16 & 3, o = meta >> 18 & 3;
+        const int g = meta >> 16 & 3;
         const void* grad = plan.grad[s];
-        if constexpr (OP == kNorm) {
-            if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP16>(grad, nullptr, t - f0, n, last, f, part);
-            else if (g == kBF16) typed_tile<OP, KIND, kBF16, kBF16>(grad, nullptr, t - f0, n, last, f, part);
-            else typed_tile<OP, KIND, kFP32, kFP32>(grad, nullptr, t - f0, n, last, f, part);
-        } else {
-            void* out = plan.out[s];
-            if constexpr (OP == kClip) {
-                if (out == grad && f == 1.0f) continue;
-                if (o == kFP16) {
-                    if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP16>(grad, out, t - f0, n, last, f, part);
-                    else if (g == kBF16) typed_tile<OP, KIND, kBF16, kFP16>(grad, out, t - f0, n, last, f, part);
-                    else typed_tile<OP, KIND, kFP32, kFP16>(grad, out, t - f0, n, last, f, part);
-                } else if (o == kBF16) {
-                    if (g == kFP16) typed_tile<OP, KIND, kFP16, kBF16>(grad, out, t - f0, n, last, f, part);
-                    else if (g == kBF16) typed_tile<OP, KIND, kBF16, kBF16>(grad, out, t - f0, n, last, f, part);
-                    else typed_tile<OP, KIND, kFP32, kBF16>(grad, out, t - f0, n, last, f, part);
-                } else {
-                    if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP32>(grad, out, t - f0, n, last, f, part);
-                    else if (g == kBF16) typed_tile<OP, KIND, kBF16, kFP32>(grad, out, t - f0, n, last, f, part);
-                    else typed_tile<OP, KIND, kFP32, kFP32>(grad, out, t - f0, n, last, f, part);
-                }
-            } else {
-                if (g == kFP16) typed_tile<OP, KIND, kFP16, kFP32>(grad, out, t - f0, n, last, f, part);
-                else if (g == kBF16) typed_tile<OP, KIND, kBF16, kFP32>(grad, out, t - f0, n, last, f, part);
-                else typed_tile<OP, KIND, kFP32, kFP32>(grad, out, t - f0, n, last, f, part);
-            }
-        }
+        if (g == kFP16) typed_tile<kNorm, KIND, kFP16, kFP16>(grad, nullptr, t - f0, n, last, 1.0f, part);
+        else if (g == kBF16) typed_tile<kNorm, KIND, kBF16, kBF16>(grad, nullptr, t - f0, n, last, 1.0f, part);
+        else typed_tile<kNorm, KIND, kFP32, kFP32>(grad, nullptr, t - f0, n, last, 1.0f, part);
     }
-    if constexpr (KIND != 0) {
-        close();
-        own = group_join<KIND>(own, sh);
-        shared = group_join<KIND>(shared, sh);
-        if (threadIdx.x == 0) {
-            parts.groups[2 * b] = own;
-            parts.groups[2 * b + 1] = shared;
-        }
+    close();
+    own = group_join<KIND, kGrBlock>(own, sh);
+    shared = group_join<KIND, kGrBlock>(shared, sh);
+    if (threadIdx.x == 0) {
+        parts.entries[2 * b] = entry(own, false);
+        parts.entries[2 * b + 1] = entry(shared, true);
     }
 }
 
-template <int KIND>
-__global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const NormParts parts) {
-    run<kNorm, KIND>(plan, 1.0f, parts);
+// ------------------------------------------------------------ writing
+// Bound by HBM.  A workgroup a tile (8 KB written): with reads and writes in flight short
+// workgroups that follow the arrays' order stream fastest.
+
+template <int OP, int KIND, int O>
+__device__ __forceinline__ void write_tile(const WritePlan& plan, int s, int32_t t, float f, Part<KIND>& part) {
+    const uint32_t meta = plan.meta[s], last = meta & 0xffffu;
+    const int32_t f0 = plan.first_tile[s], n = plan.first_tile[s + 1] - f0;
+    const int g = meta >> 16 & 3;
+    const void* grad = plan.grad[s];
+    void* out = plan.out[s];
+    if (g == kFP16) typed_tile<OP, KIND, kFP16, O>(grad, out, t - f0, n, last, f, part);
+    else if (g == kBF16) typed_tile<OP, KIND, kBF16, O>(grad, out, t - f0, n, last, f, part);
+    else typed_tile<OP, KIND, kFP32, O>(grad, out, t - f0, n, last, f, part);
 }
 
 __global__ __launch_bounds__(kGrBlock) void k_clip(const WritePlan plan, const float* __restrict__ scale,
                                                    const int32_t* __restrict__ nonfinite) {
-    if (nonfinite != nullptr && *nonfinite != 0) return;
-    run<kClip, 0>(plan, *scale, NormParts{});
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int32_t flag = nonfinite != nullptr ? *nonfinite : 0;
+    const float f = *scale;
+    const int s = find_tensor(plan, b, threadIdx.x & 63);
+    if (flag != 0 || (plan.out[s] == plan.grad[s] && f == 1.0f)) return;
+    Part<0> none;
+    const int o = plan.meta[s] >> 18 & 3;
+    if (o == kFP16) write_tile<kClip, 0, kFP16>(plan, s, b, f, none);
+    else if (o == kBF16) write_tile<kClip, 0, kBF16>(plan, s, b, f, none);
+    else write_tile<kClip, 0, kFP32>(plan, s, b, f, none);
 }
 
+// KIND 0: without sums; otherwise a tile's goes to its entry, negative where the
+// tensor is shared.
 template <int OP, int KIND>
-__global__ __launch_bounds__(kGrBlock) void k_accumulate(const WritePlan plan, float f, const NormParts parts) {
-    run<OP, KIND>(plan, f, parts);
+__global__ __launch_bounds__(kGrBlock) void k_accumulate(const WritePlan plan, float f, double* __restrict__ entries) {
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int s = find_tensor(plan, b, threadIdx.x & 63);
+    Part<KIND> part;
+    write_tile<OP, KIND, kFP32>(plan, s, b, f, part);
+    if constexpr (KIND != 0) {
+        __shared__ double sh[kGrBlock / 64];
+        const double x = group_join<KIND, kGrBlock>(part.value(), sh);
+        if (threadIdx.x == 0) entries[b] = entry(x, (plan.meta[s] >> 20 & 1) != 0);
+    }
 }
 
 // ------------------------------------------------------------ ends
 
 struct TensorTiles {
-    int32_t n, per;
+    int32_t n, per, skew;
     int32_t first_tile[kNormTensors + 1];
 };
 
-// A wave a tensor.
+// A workgroup a tensor: its entries are [f0 / per, (f1 - 1) / per], moved by skew * s.
 __global__ __launch_bounds__(kGrBlock) void k_tensor_norms(const TensorTiles p, int32_t kind, const double* __restrict__ parts,
                                                            double* __restrict__ tensor_norms) {
-    const int s = static_cast<int>(blockIdx.x) * (kGrBlock / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (s >= p.n) return;
+    __shared__ double sh[kGrBlock / 64];
+    const int s = static_cast<int>(blockIdx.x);
     const int32_t f0 = p.first_tile[s], f1 = p.first_tile[s + 1];
     double x = 0.0;
-    if (f1 > f0)
-        for (int32_t b = f0 / p.per + lane; b <= (f1 - 1) / p.per; b += 64) x = join(kind, x, parts[b + s]);
-    x = kind == kMax ? wave_join<kMax>(x) : wave_join<kSum>(x);
-    if (lane == 0) tensor_norms[s] = kind == kMax ? x : __builtin_sqrt(x);
+    if (f1 > f0) {
+        const double* at = parts + int64_t(p.skew) * s;
+        const int32_t end = (f1 - 1) / p.per + 1;
+#pragma unroll 4
+        for (int32_t i = f0 / p.per + static_cast<int32_t>(threadIdx.x); i < end; i += kGrBlock)
+            x = join(kind, x, __builtin_fabs(at[i]));
+    }
+    x = kind == kMax ? group_join<kMax, kGrBlock>(x, sh) : group_join<kSum, kGrBlock>(x, sh);
+    if (threadIdx.x == 0) tensor_norms[s] = kind == kMax ? x : __builtin_sqrt(x);
 }
 
-__global__ __launch_bounds__(kGrBlock) void k_norm_end(const double* __restrict__ groups, int64_t n, const NormEnd e) {
+// Joins entries [i0, i1), those that are not negative into `own`, the others into `shared`.
+template <int KIND, int BLOCK>
+__device__ __forceinline__ void join_entries(const double* __restrict__ entries, int64_t i0, int64_t i1, double* sh, double& own,
+                                             double& shared) {
+    own = shared = 0.0;
+    constexpr int kBatch = 8;       // loads in flight of a thread
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kBatch * BLOCK) {
+        double x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) x[k] = i + k * BLOCK < i1 ? entries[i + k * BLOCK] : 0.0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const bool second = __builtin_signbit(x[k]);
+            own = join<KIND>(own, second ? 0.0 : x[k]);
+            shared = join<KIND>(shared, second ? -x[k] : 0.0);
+        }
+    }
+    own = group_join<KIND, BLOCK>(own, sh);
+    shared = group_join<KIND, BLOCK>(shared, sh);
+}
+
+// Workgroup b joins `per` entries into two.
+template <int KIND>
+__global__ __launch_bounds__(kGrBlock) void k_join(const double* __restrict__ entries, int64_t n, int64_t per,
+                                                   double* __restrict__ to) {
     __shared__ double sh[kGrBlock / 64];
-    double own = 0.0, shared = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kGrBlock) {
-        own = join(e.kind, own, groups[2 * i]);
-        shared = join(e.kind, shared, groups[2 * i + 1]);
+    const int64_t i0 = blockIdx.x * per, i1 = i0 + per < n ? i0 + per : n;
+    double own, shared;
+    join_entries<KIND, kGrBlock>(entries, i0, i1, sh, own, shared);
+    if (threadIdx.x == 0) {
+        to[2 * blockIdx.x] = entry(own, false);
+        to[2 * blockIdx.x + 1] = entry(shared, true);
     }
-    if (e.kind == kMax) {
-        own = group_join<kMax>(own, sh);
-        shared = group_join<kMax>(shared, sh);
-    } else {
-        own = group_join<kSum>(own, sh);
-        shared = group_join<kSum>(shared, sh);
-    }
+}
+
+constexpr int kEndBlock = 1024;
+
+template <int KIND>
+__global__ __launch_bounds__(kEndBlock) void k_norm_end(const double* __restrict__ entries, int64_t n, const NormEnd e) {
+    __shared__ double sh[kEndBlock / 64];
+    double own, shared;
+    join_entries<KIND, kEndBlock>(entries, 0, n, sh, own, shared);
     if (threadIdx.x == 0) {
         e.sums[e.rank] = own;
         e.sums[e.world] = shared;
@@ -377,43 +446,42 @@ static hipError_t launch(void (*kernel)(A...), int64_t groups, int threads, hipS
     return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<uint32_t>(groups)), dim3(threads), list, 0, stream);
 }
 
-template <class PLAN>
-static int64_t groups_of(const PLAN& p) {
-    return (int64_t(p.first_tile[p.n]) + p.per - 1) / p.per;
-}
-
 hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, hipStream_t stream) {
-    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups_of(plan), kGrBlock, stream, plan, parts);
+    const int64_t groups = (int64_t(plan.first_tile[plan.n]) + plan.per - 1) / plan.per;
+    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, stream, plan, parts);
 }
 
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream) {
-    return launch(k_clip, groups_of(plan), kGrBlock, stream, plan, scale, nonfinite);
+    return launch(k_clip, plan.first_tile[plan.n], kGrBlock, stream, plan, scale, nonfinite);
 }
 
 template <int OP>
-static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float factor, const NormParts& parts, hipStream_t stream) {
+static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float factor, double* entries, hipStream_t stream) {
     auto kernel = kind == 0 ? k_accumulate<OP, 0> : kind == kMax ? k_accumulate<OP, kMax> : k_accumulate<OP, kSum>;
-    return launch(kernel, groups_of(plan), kGrBlock, stream, plan, factor, parts);
+    return launch(kernel, plan.first_tile[plan.n], kGrBlock, stream, plan, factor, entries);
 }
 
-hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, const NormParts& parts,
-                             hipStream_t stream) {
-    return first ? accumulate_launch<kSet>(kind, plan, factor, parts, stream)
-                 : accumulate_launch<kAdd>(kind, plan, factor, parts, stream);
+hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, double* entries, hipStream_t stream) {
+    return first ? accumulate_launch<kSet>(kind, plan, factor, entries, stream)
+                 : accumulate_launch<kAdd>(kind, plan, factor, entries, stream);
 }
 
-hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, const double* parts,
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, int32_t skew, const double* parts,
                                double* tensor_norms, hipStream_t stream) {
     TensorTiles p;
     p.n = n;
     p.per = per;
+    p.skew = skew;
     for (int32_t i = 0; i <= n; ++i) p.first_tile[i] = first_tile[i];
-    constexpr int kWaves = kGrBlock / 64;
-    return launch(k_tensor_norms, (n + kWaves - 1) / kWaves, kGrBlock, stream, p, kind, parts, tensor_norms);
+    return launch(k_tensor_norms, n, kGrBlock, stream, p, kind, parts, tensor_norms);
 }
 
-hipError_t launch_norm_end(const double* groups, int64_t n_groups, const NormEnd& end, hipStream_t stream) {
-    return launch(k_norm_end, 1, kGrBlock, stream, groups, n_groups, end);
+hipError_t launch_join(int32_t kind, const double* entries, int64_t n, int64_t per, double* to, hipStream_t stream) {
+    return launch(kind == kMax ? k_join<kMax> : k_join<kSum>, (n + per - 1) / per, kGrBlock, stream, entries, n, per, to);
+}
+
+hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end, hipStream_t stream) {
+    return launch(end.kind == kMax ? k_norm_end<kMax> : k_norm_end<kSum>, 1, kEndBlock, stream, entries, n, end);
 }
 
 hipError_t launch_norm_finalize(const NormEnd& end, hipStream_t stream) {

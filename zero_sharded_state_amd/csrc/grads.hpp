@@ -42,7 +42,6 @@ static_assert(sizeof(NormPlan) <= 3840, "the plan has to fit the kernel argument
 
 struct WritePlan {
     int32_t n;
-    int32_t per;
     int32_t first_tile[kWriteTensors + 1];
     uint32_t meta[kWriteTensors];
     const void* grad[kWriteTensors];
@@ -50,18 +49,24 @@ struct WritePlan {
 };
 static_assert(sizeof(WritePlan) <= 3840, "the plan has to fit the kernel arguments");
 
-// Workgroups of a launch that sums: each takes a run of tiles, so that there are
+// Workgroups of a launch of the norm: each takes a run of tiles, so that there are
 // few partial results and the run's sum stays in registers.
 constexpr int kNormGroups = 2048;
 
-// What a summing launch leaves in the workspace: two values a workgroup (tensors
-// that are not shared, and shared ones), and, for the norms of single tensors, one
-// for every workgroup and tensor that meet: workgroup b's part of tensor s is at
-// b + s, since from one such pair to the next b or s grows.
+// Partial results in the workspace.  An entry is a sum of squares or a largest magnitude,
+// with a minus sign where its tensors are shared.  A launch of the norm leaves two a
+// workgroup (one of each sort), and, for the norms of single tensors, one for every workgroup
+// and tensor that meet: workgroup b's part of tensor s is at b + s, since from one such
+// pair to the next b or s grows.  The accumulation leaves one a tile.
 struct NormParts {
-    double* groups;         // [2 * workgroup] of this launch
+    double* entries;        // [2 * workgroup] of this launch
     double* tensors;        // [workgroup + tensor] of this launch, or null
 };
+
+// Entries that one workgroup ends the norm from; more are joined by kJoinGroups at
+// most first.
+constexpr int64_t kEndEntries = 16384;
+constexpr int64_t kJoinGroups = 512;
 
 struct NormEnd {
     int32_t kind, rank, world, finalize;
@@ -74,14 +79,17 @@ struct NormEnd {
 
 hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, hipStream_t stream);
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream);
-// kind 0: without sums
-hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, const NormParts& parts,
+// kind 0: without sums (entries may be null)
+hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, double* entries,
                              hipStream_t stream);
-// tensor_norms[s] of the launch's n tensors from its parts.
-hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, const double* parts,
+// tensor_norms[s] of the launch's n tensors; tensor s's parts are [first_tile[s] / per,
+// (first_tile[s + 1] - 1) / per], moved by skew * s.
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, int32_t skew, const double* parts,
                                double* tensor_norms, hipStream_t stream);
-// groups[0 .. 2 * n_groups) into the sums, and the end of the norm where asked.
-hipError_t launch_norm_end(const double* groups, int64_t n_groups, const NormEnd& end, hipStream_t stream);
+// to[2 * b], to[2 * b + 1]: entries [b * per, (b + 1) * per) joined.
+hipError_t launch_join(int32_t kind, const double* entries, int64_t n, int64_t per, double* to, hipStream_t stream);
+// n entries into the sums, and the end of the norm where asked.
+hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end, hipStream_t stream);
 // The end of the norm from the sums alone.
 hipError_t launch_norm_finalize(const NormEnd& end, hipStream_t stream);
 

@@ -160,27 +160,41 @@ zs3_status check_grad(int32_t i, const zs3_grad_tensor& t) {
 
 // ------------------------------------------------------------- the norm
 
-// The workspace: for every launch the values of its workgroups, then those of its tensors' parts.
-constexpr int64_t kGroupDoubles = 2 * int64_t(kNormGroups);
-constexpr int64_t kTensorDoubles = kNormGroups + kNormTensors;
-
-// Launches that a list takes at most, whichever call makes them: an address adds up to one tile.
-int64_t launches_of(int32_t n, const zs3_grad_tensor* tensors) {
+// What a list takes at most, whichever call takes it: launches, and tiles of all of them (an
+// address adds up to one a tensor).
+struct Extent {
     int64_t launches = 1, tiles = 0;
+};
+
+Extent extent_of(int32_t n, const zs3_grad_tensor* tensors) {
+    Extent e;
+    int64_t here = 0;
     int32_t held = 0;
     for (int32_t i = 0; i < n; ++i) {
-        const int64_t here = tensors[i].numel == 0 ? 0 : tensors[i].numel / gr_tile(4) + 2;
-        if (held == std::min(kNormTensors, kWriteTensors) || tiles + here > kMaxTiles) {
-            ++launches;
-            tiles = held = 0;
+        const int64_t t = tensors[i].numel == 0 ? 0 : tensors[i].numel / gr_tile(4) + 2;
+        if (held == std::min(kNormTensors, kWriteTensors) || here + t > kMaxTiles) {
+            ++e.launches;
+            here = held = 0;
         }
         ++held;
-        tiles += here;
+        here += t;
+        e.tiles += t;
     }
-    return launches;
+    return e;
 }
 
-int64_t workspace_size(int64_t launches) { return launches * 8 * (kGroupDoubles + kTensorDoubles); }
+// The workspace, in doubles: the entries (two a workgroup of the norm, or one a tile of
+// the accumulation), what they are joined into, and the parts of single tensors.
+struct Workspace {
+    int64_t joined, tensors, end;
+    explicit Workspace(const Extent& e) {
+        joined = std::max(e.launches * 2 * kNormGroups, e.tiles);
+        tensors = joined + 2 * kJoinGroups;
+        end = tensors + e.launches * (kNormGroups + kNormTensors);
+        end += end & 1;
+    }
+    int64_t bytes() const { return 8 * end; }
+};
 
 zs3_status check_finalize(const zs3_norm_args& a) {
     if (a.kind != ZS3_NORM_2 && a.kind != ZS3_NORM_INF) return fail(ZS3_EINVAL, "kind %d is not ZS3_NORM_2 or ZS3_NORM_INF", a.kind);
@@ -214,7 +228,7 @@ zs3_status check_norm(int32_t n, const zs3_grad_tensor* tensors, const zs3_norm_
     zs3_status s = check_finalize(a);
     if (s != ZS3_OK || (s = check_end(a, a.finalize != 0)) != ZS3_OK) return s;
     if (!aligned(a.tensor_norms, 8)) return fail(ZS3_EINVAL, "tensor_norms is not 8-byte aligned");
-    const int64_t need = workspace_size(launches_of(n, tensors));
+    const int64_t need = Workspace(extent_of(n, tensors)).bytes();
     if (a.workspace == nullptr || !aligned(a.workspace, 16)) return fail(ZS3_EINVAL, "workspace is NULL or not 16-byte aligned");
     if (a.workspace_bytes < need)
         return fail(ZS3_EINVAL, "workspace has %lld bytes, the list needs %lld", (long long)a.workspace_bytes, (long long)need);
@@ -234,10 +248,10 @@ void set_out(NormPlan&, int32_t, void*) {}
 void set_out(WritePlan& p, int32_t i, void* out) { p.out[i] = out; }
 
 // Cuts a list into launches.  `written`: tiles are those of out (grad where NULL),
-// otherwise grad's; `sums`: a launch has at most kNormGroups workgroups, otherwise
-// one a tile; `emit(plan, first tensor)` launches one plan.
+// otherwise grad's.  `emit(plan, first tensor)` launches one plan; a plan may hold
+// empty tensors alone.
 template <class PLAN, class EMIT>
-zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, bool sums, EMIT emit) {
+zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, EMIT emit) {
     constexpr int32_t kMost = sizeof(PLAN::meta) / sizeof(uint32_t);
     PLAN plan;
     plan.n = 0;
@@ -245,9 +259,7 @@ zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, 
     int32_t first = 0;
     auto flush = [&](int32_t next) -> zs3_status {
         if (plan.n == 0) return ZS3_OK;
-        const int64_t tiles = plan.first_tile[plan.n];
-        plan.per = sums ? static_cast<int32_t>((tiles + kNormGroups - 1) / kNormGroups) : 1;
-        if (plan.per < 1) plan.per = 1;
+        for (int32_t i = plan.n + 1; i <= kMost; ++i) plan.first_tile[i] = INT32_MAX;
         const zs3_status s = emit(plan, first);
         plan.n = 0;
         first = next;
@@ -277,29 +289,18 @@ zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, 
     return flush(n);
 }
 
-// The launches of a call with a norm, their parts in the workspace, and its end.
-template <class PLAN, class LAUNCH>
-zs3_status with_norm(int32_t n, const zs3_grad_tensor* tensors, bool written, const zs3_norm_args& a, void* stream,
-                     const char* what, LAUNCH go) {
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    double* groups = static_cast<double*>(a.workspace);
-    double* parts = groups + launches_of(n, tensors) * kGroupDoubles;
-    int64_t used = 0;
-    zs3_status s = each_launch<PLAN>(n, tensors, written, true, [&](const PLAN& plan, int32_t first) -> zs3_status {
-        const int64_t tiles = plan.first_tile[plan.n];
-        if (tiles > 0) {
-            const zs3_status e = launched(go(plan, NormParts{groups + 2 * used, a.tensor_norms != nullptr ? parts : nullptr}, st), what);
-            if (e != ZS3_OK) return e;
-            used += (tiles + plan.per - 1) / plan.per;
-        }
-        if (a.tensor_norms == nullptr) return ZS3_OK;
-        const zs3_status e = launched(launch_tensor_norms(a.kind, plan.first_tile, plan.n, plan.per, parts, a.tensor_norms + first, st),
-                                      "tensor norm kernel launch");
-        parts += kTensorDoubles;
-        return e;
-    });
-    if (s != ZS3_OK) return s;
-    s = launched(launch_norm_end(groups, used, end_of(a), st), "norm kernel launch");
+// The end of a norm from `used` entries at the workspace's start.
+zs3_status end_norm(int64_t used, const Workspace& w, const zs3_norm_args& a, hipStream_t stream) {
+    const double* entries = static_cast<const double*>(a.workspace);
+    zs3_status s;
+    if (used > kEndEntries) {
+        double* to = static_cast<double*>(a.workspace) + w.joined;
+        const int64_t per = (used + kJoinGroups - 1) / kJoinGroups;
+        if ((s = launched(launch_join(a.kind, entries, used, per, to, stream), "norm kernel launch")) != ZS3_OK) return s;
+        entries = to;
+        used = 2 * ((used + per - 1) / per);
+    }
+    s = launched(launch_norm_end(entries, used, end_of(a), stream), "norm kernel launch");
     return s != ZS3_OK ? s : ok();
 }
 
@@ -311,7 +312,7 @@ zs3_status zs3_norm_workspace_bytes(int32_t n, const zs3_grad_tensor* tensors, i
     if (bytes == nullptr) return fail(ZS3_EINVAL, "bytes is NULL");
     const zs3_status s = check_list(n, tensors);
     if (s != ZS3_OK) return s;
-    *bytes = workspace_size(launches_of(n, tensors));
+    *bytes = Workspace(extent_of(n, tensors)).bytes();
     return ok();
 }
 
@@ -328,10 +329,28 @@ zs3_status zs3_grad_norm_tensors(int32_t n, const zs3_grad_tensor* tensors, cons
             ranges.read(t.grad, size_of(t.dtype) * t.numel, i);
         }
         if ((s = check_overlaps(ranges)) != ZS3_OK) return s;
-        return with_norm<NormPlan>(n, tensors, false, *norm, stream, "norm kernel launch",
-                                   [&](const NormPlan& plan, const NormParts& parts, hipStream_t st) {
-                                       return launch_norm(norm->kind, plan, parts, st);
-                                   });
+        const hipStream_t st = static_cast<hipStream_t>(stream);
+        const zs3_norm_args& a = *norm;
+        const Workspace w(extent_of(n, tensors));
+        double* entries = static_cast<double*>(a.workspace);
+        double* parts = entries + w.tensors;
+        int64_t used = 0;
+        s = each_launch<NormPlan>(n, tensors, false, [&](NormPlan& plan, int32_t first) -> zs3_status {
+            const int64_t tiles = plan.first_tile[plan.n];
+            plan.per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + kNormGroups - 1) / kNormGroups));
+            if (tiles > 0) {
+                const NormParts to{entries + used, a.tensor_norms != nullptr ? parts : nullptr};
+                const zs3_status e = launched(launch_norm(a.kind, plan, to, st), "norm kernel launch");
+                if (e != ZS3_OK) return e;
+                used += 2 * ((tiles + plan.per - 1) / plan.per);
+            }
+            if (a.tensor_norms == nullptr) return ZS3_OK;
+            const zs3_status e = launched(launch_tensor_norms(a.kind, plan.first_tile, plan.n, plan.per, 1, parts,
+                                                              a.tensor_norms + first, st), "norm kernel launch");
+            parts += kNormGroups + kNormTensors;
+            return e;
+        });
+        return s != ZS3_OK ? s : end_norm(used, w, a, st);
     });
 }
 
@@ -373,7 +392,7 @@ zs3_status zs3_clip_tensors(int32_t n, const zs3_grad_tensor* tensors, const flo
             ranges.written(t.out, size_of(t.out_dtype) * t.numel, i);
         }
         if ((s = check_overlaps(ranges)) != ZS3_OK) return s;
-        s = each_launch<WritePlan>(n, tensors, true, false, [&](const WritePlan& plan, int32_t) -> zs3_status {
+        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t) -> zs3_status {
             if (plan.first_tile[plan.n] == 0) return ZS3_OK;
             return launched(launch_clip(plan, scale, nonfinite, static_cast<hipStream_t>(stream)), "clip kernel launch");
         });
@@ -400,17 +419,24 @@ zs3_status zs3_accumulate_tensors(int32_t n, const zs3_grad_tensor* tensors, dou
         }
         if (norm != nullptr && (s = check_norm(n, tensors, norm, &ranges)) != ZS3_OK) return s;
         if ((s = check_overlaps(ranges)) != ZS3_OK) return s;
-        constexpr const char* kWhat = "accumulate kernel launch";
-        if (norm != nullptr)
-            return with_norm<WritePlan>(n, tensors, true, *norm, stream, kWhat,
-                                        [&](const WritePlan& plan, const NormParts& parts, hipStream_t st) {
-                                            return launch_accumulate(norm->kind, plan, f, first != 0, parts, st);
-                                        });
-        s = each_launch<WritePlan>(n, tensors, true, false, [&](const WritePlan& plan, int32_t) -> zs3_status {
-            if (plan.first_tile[plan.n] == 0) return ZS3_OK;
-            return launched(launch_accumulate(0, plan, f, first != 0, NormParts{}, static_cast<hipStream_t>(stream)), kWhat);
+        const hipStream_t st = static_cast<hipStream_t>(stream);
+        double* entries = norm != nullptr ? static_cast<double*>(norm->workspace) : nullptr;
+        int64_t used = 0;
+        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t at) -> zs3_status {
+            const int64_t tiles = plan.first_tile[plan.n];
+            double* to = entries != nullptr ? entries + used : nullptr;
+            used += tiles;
+            if (tiles > 0) {
+                const zs3_status e = launched(launch_accumulate(norm != nullptr ? norm->kind : 0, plan, f, first != 0, to, st),
+                                              "accumulate kernel launch");
+                if (e != ZS3_OK) return e;
+            }
+            if (norm == nullptr || norm->tensor_norms == nullptr) return ZS3_OK;
+            return launched(launch_tensor_norms(norm->kind, plan.first_tile, plan.n, 1, 0, to, norm->tensor_norms + at, st),
+                            "norm kernel launch");
         });
-        return s != ZS3_OK ? s : ok();
+        if (s != ZS3_OK || norm == nullptr) return s != ZS3_OK ? s : ok();
+        return end_norm(used, Workspace(extent_of(n, tensors)), *norm, st);
     });
 }
 

@@ -70,18 +70,21 @@ typedef struct {
     float* scale;            /* dev */
     int32_t* nonfinite;      /* dev */
     double* tensor_norms;    /* dev, one for each entry of the list, or NULL */
-    void* workspace;         /* dev, 16-byte aligned, zs3_norm_workspace_bytes of the list */
+    void* workspace;         /* dev, 16-byte aligned, zs3_norm_workspace_bytes of the list; see there */
     int64_t workspace_bytes;
 } zs3_norm_args;
 
 /* Bytes of workspace that a list of these sizes and types needs (the
- * addresses in it are not looked at). */
+ * addresses in it are not looked at).  Fill a workspace with zeros once, before
+ * its first use: it starts with counters that every call leaves at 0.  One
+ * workspace serves any lists it is large enough for, calls one after
+ * the other; calls that may run at once (on two streams, in two graphs that are
+ * replayed side by side) need one each, and outputs of their own. */
 ZS3_API zs3_status zs3_norm_workspace_bytes(int32_t n, const zs3_grad_tensor* tensors, int64_t* bytes);
 
 /* `out` and `out_dtype` are not looked at.  Written buffers (sums, norm, scale,
  * nonfinite, tensor_norms, workspace) must not overlap each other or a tensor.
- * The call allocates, uploads and keeps nothing (it may be captured into a
- * graph); calls that may run at once need workspaces and outputs of their own. */
+ * The call allocates and uploads nothing (it may be captured into a graph). */
 ZS3_API zs3_status zs3_grad_norm_tensors(int32_t n, const zs3_grad_tensor* tensors, const zs3_norm_args* norm,
                                  void* stream);
 

@@ -27,6 +27,8 @@ struct Launch {
     std::vector<void*> out;
     double* entries;        // of this launch
     double* tensors;        // the norm's parts of single tensors
+    uint32_t* counters;
+    double* tensor_norms;
 };
 std::vector<Launch> launches;
 struct TensorNorms {
@@ -51,7 +53,7 @@ std::vector<End> ends;
 
 template <class PLAN>
 Launch copy(const PLAN& p, bool written, int32_t kind, int32_t per, double* entries, double* tensors) {
-    Launch l{written, kind, p.n, per, {}, {}, {}, {}, entries, tensors};
+    Launch l{written, kind, p.n, per, {}, {}, {}, {}, entries, tensors, nullptr, nullptr};
     l.first_tile.assign(p.first_tile, p.first_tile + p.n + 1);
     l.meta.assign(p.meta, p.meta + p.n);
     l.grad.assign(p.grad, p.grad + p.n);
@@ -59,8 +61,12 @@ Launch copy(const PLAN& p, bool written, int32_t kind, int32_t per, double* entr
         if (p.first_tile[i] != INT32_MAX) l.n = -1;
     return l;
 }
-hipError_t launch_norm(int32_t kind, const NormPlan& p, const NormParts& parts, hipStream_t) {
+hipError_t launch_norm(int32_t kind, const NormPlan& p, const NormParts& parts, const NormEnd& end, hipStream_t) {
     launches.push_back(copy(p, false, kind, p.per, parts.entries, parts.tensors));
+    launches.back().counters = parts.counters;
+    launches.back().tensor_norms = parts.tensor_norms;
+    if (parts.counters != nullptr)      // its last workgroup ends the norm
+        ends.push_back({parts.all, parts.entries - parts.all + 2 * ((int64_t(p.first_tile[p.n]) + p.per - 1) / p.per), end});
     return hipSuccess;
 }
 hipError_t launch_clip(const WritePlan& p, const float*, const int32_t*, hipStream_t) {
@@ -184,8 +190,12 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
         if (n > 1) places.insert(p + n - 1);
     };
     EXPECT(ends.size() == 1 && joins.size() <= 1);
+    put(lo, kCounterBytes / 8);
+    lo += kCounterBytes / 8;
     int64_t used = 0;
     for (const Launch& L : launches) {
+        EXPECT(L.counters == nullptr || (L.counters == a.workspace && &L == &launches.back()));
+        EXPECT(L.tensor_norms == nullptr || L.counters != nullptr);
         const int64_t all = L.first_tile[L.n], groups = (all + L.per - 1) / L.per, entries = written ? all : 2 * groups;
         EXPECT(L.kind == a.kind && L.entries == lo + used);
         put(L.entries, entries);
@@ -198,7 +208,7 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
         }
     }
     if (joins.empty()) {
-        EXPECT(used <= kEndEntries && ends[0].entries == lo && ends[0].n == used);
+        EXPECT((!written || used <= kEndEntries) && ends[0].entries == lo && ends[0].n == used);
     } else {
         const Join& j = joins[0];
         const int64_t groups = (used + j.per - 1) / j.per;
@@ -211,6 +221,14 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
         return;
     }
     size_t done = 0, seen = 0;
+    for (const Launch& L : launches) {      // those that a launch's last workgroup does
+        if (L.tensor_norms == nullptr) continue;
+        EXPECT(L.tensor_norms + L.n == a.tensor_norms + want.size());
+        tensor_norms.push_back({L.kind, L.n, L.per, 1, L.first_tile, L.tensors, L.tensor_norms});
+        for (int32_t s = 0; s < L.n; ++s)
+            EXPECT(L.first_tile[s + 1] == L.first_tile[s] ||
+                   (L.first_tile[s + 1] - 1) / L.per - L.first_tile[s] / L.per < kFewParts);
+    }
     for (const TensorNorms& t : tensor_norms) {
         EXPECT(t.out == a.tensor_norms + done && t.skew == (written ? 0 : 1));
         done += static_cast<size_t>(t.n);

@@ -462,22 +462,30 @@ def test_micro_batches_to_adamw():
     assert torch.isfinite(norms.norm).all()
 
 
-def test_same_bits_again_and_in_any_workspace():
+def test_same_bits_again_and_in_a_workspace_of_other_lists():
+    """One workspace serves lists of other sizes, kinds and calls in turn."""
     import torch
     require_gpu()
     note("determinism")
     rng = np.random.default_rng(31)
-    ts = [Tensor(rng, n, "bf16", i, out="acc") for i, n in enumerate((2_000_001, 300, 40_000))]
-    entries = [t.entry() for t in ts]
-    seen = set()
-    for k in range(5):
-        n = Norm(entries)
-        n.ws[64:].fill_(255 if k % 2 else 0)     # what earlier calls left beyond its head does not count
-        for _ in range(2):
-            zs.zs3_grad_norm_tensors(entries, n.args)
-        torch.cuda.synchronize()
-        seen.add((n.got()["norm"], n.got()["scale"], n.got()["each"].tobytes(), n.got()["sums"].tobytes()))
-    assert len(seen) == 1
+    lists = [[Tensor(rng, n, "bf16", i, out="acc", shared=i == 1) for i, n in enumerate(sizes)]
+             for sizes in ((2_000_001, 300, 40_000), (5,), (7_000_000, 1, 900), [700] * 260, (33_000_000,))]
+    entries = [[t.entry() for t in ts] for ts in lists]
+    ws = torch.zeros(max(zs.zs3_norm_workspace_bytes(e) for e in entries), dtype=torch.uint8, device="cuda")
+    seen = [set() for _ in lists]
+    for k in range(3):
+        for i, (ts, e) in enumerate(zip(lists, entries)):
+            for kind in ("2", "inf"):
+                n = Norm(e, kind=kind)
+                n.args.workspace, n.args.workspace_bytes = ws.data_ptr(), ws.numel()
+                zs.zs3_grad_norm_tensors(e, n.args)
+                sync()
+                if k == 0:
+                    n.check([(t.x, t.shared) for t in ts])
+                seen[i].add((kind, n.got()["norm"], n.got()["scale"], n.got()["each"].tobytes(), n.got()["sums"].tobytes()))
+            zs.zs3_accumulate_tensors(e, 1.0, True, norm=Norm(e).args if k else n.args)
+    sync()
+    assert all(len(s) == 2 for s in seen)
 
 
 def test_captured_and_replayed():

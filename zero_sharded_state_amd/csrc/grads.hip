@@ -148,15 +148,26 @@ __device__ __forceinline__ double group_join(double x, double* sh) {
     return x;
 }
 
-// The end of the norm from the sums (see the header's definition).
-__device__ void end_of_norm(const NormEnd& e, double own, double shared) {
-    double total = 0.0;
-    for (int v = 0; v < e.world; ++v) total = join(e.kind, total, v == e.rank ? own : e.sums[v]);
-    total = join(e.kind, total, shared);
+// The peers' sums, read by the lanes of a wave.
+template <int KIND>
+__device__ __forceinline__ double peers_of(const NormEnd& e) {
+    double x = 0.0;
+    if (e.finalize)
+        for (int v = static_cast<int>(threadIdx.x & 63); v < e.world; v += 64)
+            if (v != e.rank) x = join<KIND>(x, e.sums[v]);
+    return x;
+}
+
+// The end of the norm (see the header's definition), by a wave whose lanes hold the
+// peers' sums.
+template <int KIND>
+__device__ __forceinline__ void end_of_norm(const NormEnd& e, double peers, double own, double shared) {
+    const double total = join<KIND>(join<KIND>(wave_join<KIND>(peers), own), shared);
     const bool bad = !(__builtin_fabs(total) <= 1.7976931348623157e308);
-    const double norm = (e.kind == kMax ? total : __builtin_sqrt(total)) / e.loss_scale;
+    const double norm = (KIND == kMax ? total : __builtin_sqrt(total)) / e.loss_scale;
     double coef = e.max_norm / (norm + 1e-6);
     if (coef > 1.0) coef = 1.0;
+    if ((threadIdx.x & 63) != 0) return;
     *e.norm = norm;
     *e.nonfinite = bad ? 1 : 0;
     *e.scale = bad ? __builtin_nanf("") : static_cast<float>(coef / e.loss_scale);
@@ -272,9 +283,88 @@ __device__ __forceinline__ void typed_tile(const void* grad, void* out, int32_t 
 // Bound by HBM.  A workgroup takes a run of tiles one behind the other and keeps its sum in
 // registers; 2048 workgroups, all that fit on the chip at once.
 
+// ------------------------------------------------------------ the last workgroup
+// Partial results that the workgroup that ends last joins.  They are stored and
+// loaded as device-scope atomics, which go past the L2 of the XCD (each has its own), and a
+// workgroup counts itself once its stores are done.  That is the order that is needed; a
+// release and an acquire by each workgroup give it too, but write back and empty
+// the L2 for all that passes through it (the norm of 27M elements 16 -> 59 us).
+
+template <bool FRESH>
+__device__ __forceinline__ void put(double* p, double x) {
+    if constexpr (FRESH) __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else *p = x;
+}
+template <bool FRESH>
+__device__ __forceinline__ double get(const double* p) {
+    if constexpr (FRESH) return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else return *p;
+}
+
+// Whether workgroup b of n is the last, asked by one thread of each after its stores.
+// Workgroups count in kCounters groups, and the last of each group at the head (atomics on one
+// word take 10 ns each: 27M elements 30 us with a single counter, 15 with these).  The
+// counters are left at 0.
+__device__ __forceinline__ bool ends_last(uint32_t* counters, int32_t b, int32_t n) {
+    constexpr int kWords = static_cast<int>(kGrLine / 4);
+    const int32_t group = b % kCounters, groups = n < kCounters ? n : kCounters, size = (n - group + kCounters - 1) / kCounters;
+    uint32_t* mine = counters + (1 + group) * kWords;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // the stores above have reached memory
+    const bool last_of_group = __hip_atomic_fetch_add(mine, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == static_cast<uint32_t>(size);
+    if (!last_of_group) return false;
+    __hip_atomic_store(mine, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = __hip_atomic_fetch_add(counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == static_cast<uint32_t>(groups);
+    if (last) __hip_atomic_store(counters, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::: "memory");                          // what is loaded next was stored before
+    return last;
+}
+
+// Joins two values over the workgroup of BLOCK threads; every thread gets them.
+template <int KIND, int BLOCK>
+__device__ __forceinline__ void group_join2(double& x, double& y, double (&sh)[2 * (BLOCK / 64)]) {
+    x = wave_join<KIND>(x);
+    y = wave_join<KIND>(y);
+    const int w = static_cast<int>(threadIdx.x >> 6);
+    if ((threadIdx.x & 63) == 0) sh[2 * w] = x, sh[2 * w + 1] = y;
+    __syncthreads();
+    x = sh[0];
+    y = sh[1];
+#pragma unroll
+    for (int i = 1; i < BLOCK / 64; ++i) {
+        x = join<KIND>(x, sh[2 * i]);
+        y = join<KIND>(y, sh[2 * i + 1]);
+    }
+    __syncthreads();
+}
+
+// Joins entries [i0, i1), those that are not negative into `own`, the others into `shared`.
+// FRESH: entries that this launch's other workgroups have just written.
+template <int KIND, int BLOCK, bool FRESH>
+__device__ __forceinline__ void join_entries(const double* entries, int64_t i0, int64_t i1, double (&sh)[2 * (BLOCK / 64)],
+                                             double& own, double& shared) {
+    own = shared = 0.0;
+    constexpr int kBatch = 8;       // loads in flight of a thread
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kBatch * BLOCK) {
+        double x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const double* at = entries + i + k * BLOCK;
+            x[k] = i + k * BLOCK < i1 ? get<FRESH>(at) : 0.0;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const bool second = __builtin_signbit(x[k]);
+            own = join<KIND>(own, second ? 0.0 : x[k]);
+            shared = join<KIND>(shared, second ? -x[k] : 0.0);
+        }
+    }
+    group_join2<KIND, BLOCK>(own, shared, sh);
+}
+
 template <int KIND>
-__global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const NormParts parts) {
-    __shared__ double sh[kGrBlock / 64];
+__global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const NormParts parts, const NormEnd e) {
+    __shared__ double sh[2 * (kGrBlock / 64)];
+    __shared__ uint32_t last;
     const int32_t b = static_cast<int32_t>(blockIdx.x), all = plan.first_tile[plan.n];
     const int32_t t0 = b * plan.per, t1 = t0 + plan.per < all ? t0 + plan.per : all;
     int s = find_tensor(plan, t0, threadIdx.x & 63);
@@ -286,7 +376,7 @@ __global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const No
         else own = join<KIND>(own, x);
         if (parts.tensors != nullptr) {
             const double y = group_join<KIND, kGrBlock>(x, sh);
-            if (threadIdx.x == 0) parts.tensors[b + s] = y;
+            if (threadIdx.x == 0) put<true>(parts.tensors + b + s, y);
         }
         part = Part<KIND>();
     };
@@ -305,11 +395,39 @@ __global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const No
         else typed_tile<kNorm, KIND, kFP32, kFP32>(grad, nullptr, t - f0, n, last, 1.0f, part);
     }
     close();
-    own = group_join<KIND, kGrBlock>(own, sh);
-    shared = group_join<KIND, kGrBlock>(shared, sh);
+    group_join2<KIND, kGrBlock>(own, shared, sh);
+    double* mine = parts.entries + 2 * int64_t(b);
     if (threadIdx.x == 0) {
-        parts.entries[2 * b] = entry(own, false);
-        parts.entries[2 * b + 1] = entry(shared, true);
+        put<true>(mine, entry(own, false));
+        put<true>(mine + 1, entry(shared, true));
+        last = parts.counters != nullptr && ends_last(parts.counters, b, static_cast<int32_t>(gridDim.x)) ? 1u : 0u;
+    }
+    __syncthreads();
+    if (last == 0) return;
+    const double peers = peers_of<KIND>(e);
+    join_entries<KIND, kGrBlock, true>(parts.all, 0, mine - parts.all + 2 * int64_t(static_cast<int32_t>(gridDim.x) - b), sh, own, shared);
+    if (threadIdx.x == 0) {
+        e.sums[e.rank] = own;
+        e.sums[e.world] = shared;
+    }
+    if (e.finalize && threadIdx.x < 64) end_of_norm<KIND>(e, peers, own, shared);
+    if (parts.tensor_norms != nullptr) {
+        for (int i = static_cast<int>(threadIdx.x); i < plan.n; i += kGrBlock) {
+            const int32_t f0 = plan.first_tile[i], f1 = plan.first_tile[i + 1];
+            double x = 0.0;
+            if (f1 > f0) {
+                const int32_t end = (f1 - 1) / plan.per;
+                constexpr int kBatch = 8;
+                for (int32_t k = f0 / plan.per; k <= end; k += kBatch) {
+                    double y[kBatch];
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) y[j] = k + j <= end ? get<true>(parts.tensors + k + j + i) : 0.0;
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) x = join<KIND>(x, y[j]);
+                }
+            }
+            parts.tensor_norms[i] = KIND == kMax ? x : __builtin_sqrt(x);
+        }
     }
 }
 
@@ -383,35 +501,14 @@ __global__ __launch_bounds__(kGrBlock) void k_tensor_norms(const TensorTiles p, 
     if (threadIdx.x == 0) tensor_norms[s] = kind == kMax ? x : __builtin_sqrt(x);
 }
 
-// Joins entries [i0, i1), those that are not negative into `own`, the others into `shared`.
-template <int KIND, int BLOCK>
-__device__ __forceinline__ void join_entries(const double* __restrict__ entries, int64_t i0, int64_t i1, double* sh, double& own,
-                                             double& shared) {
-    own = shared = 0.0;
-    constexpr int kBatch = 8;       // loads in flight of a thread
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kBatch * BLOCK) {
-        double x[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) x[k] = i + k * BLOCK < i1 ? entries[i + k * BLOCK] : 0.0;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const bool second = __builtin_signbit(x[k]);
-            own = join<KIND>(own, second ? 0.0 : x[k]);
-            shared = join<KIND>(shared, second ? -x[k] : 0.0);
-        }
-    }
-    own = group_join<KIND, BLOCK>(own, sh);
-    shared = group_join<KIND, BLOCK>(shared, sh);
-}
-
 // Workgroup b joins `per` entries into two.
 template <int KIND>
 __global__ __launch_bounds__(kGrBlock) void k_join(const double* __restrict__ entries, int64_t n, int64_t per,
                                                    double* __restrict__ to) {
-    __shared__ double sh[kGrBlock / 64];
+    __shared__ double sh[2 * (kGrBlock / 64)];
     const int64_t i0 = blockIdx.x * per, i1 = i0 + per < n ? i0 + per : n;
     double own, shared;
-    join_entries<KIND, kGrBlock>(entries, i0, i1, sh, own, shared);
+    join_entries<KIND, kGrBlock, false>(entries, i0, i1, sh, own, shared);
     if (threadIdx.x == 0) {
         to[2 * blockIdx.x] = entry(own, false);
         to[2 * blockIdx.x + 1] = entry(shared, true);
@@ -422,17 +519,21 @@ constexpr int kEndBlock = 1024;
 
 template <int KIND>
 __global__ __launch_bounds__(kEndBlock) void k_norm_end(const double* __restrict__ entries, int64_t n, const NormEnd e) {
-    __shared__ double sh[kEndBlock / 64];
+    __shared__ double sh[2 * (kEndBlock / 64)];
     double own, shared;
-    join_entries<KIND, kEndBlock>(entries, 0, n, sh, own, shared);
+    const double peers = peers_of<KIND>(e);
+    join_entries<KIND, kEndBlock, false>(entries, 0, n, sh, own, shared);
     if (threadIdx.x == 0) {
         e.sums[e.rank] = own;
         e.sums[e.world] = shared;
-        if (e.finalize) end_of_norm(e, own, shared);
     }
+    if (e.finalize && threadIdx.x < 64) end_of_norm<KIND>(e, peers, own, shared);
 }
 
-__global__ void k_norm_finalize_sums(const NormEnd e) { end_of_norm(e, e.sums[e.rank], e.sums[e.world]); }
+template <int KIND>
+__global__ __launch_bounds__(64) void k_norm_finalize(const NormEnd e) {
+    end_of_norm<KIND>(e, peers_of<KIND>(e), e.sums[e.rank], e.sums[e.world]);
+}
 
 }  // namespace
 
@@ -446,9 +547,9 @@ static hipError_t launch(void (*kernel)(A...), int64_t groups, int threads, hipS
     return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<uint32_t>(groups)), dim3(threads), list, 0, stream);
 }
 
-hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, hipStream_t stream) {
+hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
     const int64_t groups = (int64_t(plan.first_tile[plan.n]) + plan.per - 1) / plan.per;
-    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, stream, plan, parts);
+    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, stream, plan, parts, end);
 }
 
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream) {
@@ -485,7 +586,7 @@ hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end,
 }
 
 hipError_t launch_norm_finalize(const NormEnd& end, hipStream_t stream) {
-    return launch(k_norm_finalize_sums, 1, 1, stream, end);
+    return launch(end.kind == kMax ? k_norm_finalize<kMax> : k_norm_finalize<kSum>, 1, 64, stream, end);
 }
 
 }  // namespace zs3

@@ -59,9 +59,27 @@ constexpr int kNormGroups = 2048;
 // and tensor that meet: workgroup b's part of tensor s is at b + s, since from one such
 // pair to the next b or s grows.  The accumulation leaves one a tile.
 struct NormParts {
+    double* all;            // the first launch's entries: one launch's follow another's
     double* entries;        // [2 * workgroup] of this launch
     double* tensors;        // [workgroup + tensor] of this launch, or null
+    uint32_t* counters;     // the last launch's, whose last workgroup ends the norm; otherwise null
+    double* tensor_norms;   // of this launch's tensors, by that workgroup, or null
 };
+
+// The workspace starts with counters of the workgroups that are done, a line each: kCounters
+// groups of them, and, first, the groups.
+constexpr int kCounters = 32;
+constexpr int64_t kCounterBytes = (1 + kCounters) * kGrLine;
+
+// Parts of one tensor up to which the norm's last workgroup joins them, a thread a tensor;
+// otherwise a launch of its own does, a workgroup a tensor (221 tensors of at most 28 parts 55 ->
+// 47 us, one of 2048 would take 200).
+constexpr int kFewParts = 32;
+
+// Entries up to which the norm's last workgroup joins them: those of two launches
+// (7 launches' 25,000 by that one workgroup: 52.5 us for 1500 tensors of 33,555, by launches of their
+// own 49).
+constexpr int64_t kLastEntries = 4 * kNormGroups;
 
 // Entries that one workgroup ends the norm from; more are joined by kJoinGroups at
 // most first.
@@ -77,7 +95,7 @@ struct NormEnd {
     int32_t* nonfinite;
 };
 
-hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, hipStream_t stream);
+hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream);
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream);
 // kind 0: without sums (entries may be null)
 hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, double* entries,

@@ -183,12 +183,13 @@ Extent extent_of(int32_t n, const zs3_grad_tensor* tensors) {
     return e;
 }
 
-// The workspace, in doubles: the entries (two a workgroup of the norm, or one a tile of
+// The workspace, in doubles: the counters, the entries (two a workgroup of the norm, or one a tile of
 // the accumulation), what they are joined into, and the parts of single tensors.
 struct Workspace {
+    static constexpr int64_t entries = kCounterBytes / 8;
     int64_t joined, tensors, end;
     explicit Workspace(const Extent& e) {
-        joined = std::max(e.launches * 2 * kNormGroups, e.tiles);
+        joined = entries + std::max(e.launches * 2 * kNormGroups, e.tiles);
         tensors = joined + 2 * kJoinGroups;
         end = tensors + e.launches * (kNormGroups + kNormTensors);
         end += end & 1;
@@ -238,8 +239,8 @@ zs3_status check_norm(int32_t n, const zs3_grad_tensor* tensors, const zs3_norm_
     return ZS3_OK;
 }
 
-NormEnd end_of(const zs3_norm_args& a) {
-    return NormEnd{a.kind, a.rank, a.world, a.finalize, a.max_norm, a.loss_scale, a.sums, a.norm, a.scale, a.nonfinite};
+NormEnd end_of(const zs3_norm_args& a, bool finalize) {
+    return NormEnd{a.kind, a.rank, a.world, finalize ? 1 : 0, a.max_norm, a.loss_scale, a.sums, a.norm, a.scale, a.nonfinite};
 }
 
 // ------------------------------------------------------------- launches
@@ -248,8 +249,8 @@ void set_out(NormPlan&, int32_t, void*) {}
 void set_out(WritePlan& p, int32_t i, void* out) { p.out[i] = out; }
 
 // Cuts a list into launches.  `written`: tiles are those of out (grad where NULL),
-// otherwise grad's.  `emit(plan, first tensor)` launches one plan; a plan may hold
-// empty tensors alone.
+// otherwise grad's.  `emit(plan, first tensor, whether it is the last)` launches one plan; a
+// plan may hold empty tensors alone.
 template <class PLAN, class EMIT>
 zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, EMIT emit) {
     constexpr int32_t kMost = sizeof(PLAN::meta) / sizeof(uint32_t);
@@ -260,7 +261,7 @@ zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, 
     auto flush = [&](int32_t next) -> zs3_status {
         if (plan.n == 0) return ZS3_OK;
         for (int32_t i = plan.n + 1; i <= kMost; ++i) plan.first_tile[i] = INT32_MAX;
-        const zs3_status s = emit(plan, first);
+        const zs3_status s = emit(plan, first, next == n);
         plan.n = 0;
         first = next;
         return s;
@@ -289,9 +290,9 @@ zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, 
     return flush(n);
 }
 
-// The end of a norm from `used` entries at the workspace's start.
+// The end of a norm from the first `used` entries.
 zs3_status end_norm(int64_t used, const Workspace& w, const zs3_norm_args& a, hipStream_t stream) {
-    const double* entries = static_cast<const double*>(a.workspace);
+    const double* entries = static_cast<const double*>(a.workspace) + w.entries;
     zs3_status s;
     if (used > kEndEntries) {
         double* to = static_cast<double*>(a.workspace) + w.joined;
@@ -300,7 +301,7 @@ zs3_status end_norm(int64_t used, const Workspace& w, const zs3_norm_args& a, hi
         entries = to;
         used = 2 * ((used + per - 1) / per);
     }
-    s = launched(launch_norm_end(entries, used, end_of(a), stream), "norm kernel launch");
+    s = launched(launch_norm_end(entries, used, end_of(a, a.finalize != 0), stream), "norm kernel launch");
     return s != ZS3_OK ? s : ok();
 }
 
@@ -332,25 +333,35 @@ zs3_status zs3_grad_norm_tensors(int32_t n, const zs3_grad_tensor* tensors, cons
         const hipStream_t st = static_cast<hipStream_t>(stream);
         const zs3_norm_args& a = *norm;
         const Workspace w(extent_of(n, tensors));
-        double* entries = static_cast<double*>(a.workspace);
-        double* parts = entries + w.tensors;
+        double* entries = static_cast<double*>(a.workspace) + w.entries;
+        double* parts = static_cast<double*>(a.workspace) + w.tensors;
+        uint32_t* counters = static_cast<uint32_t*>(a.workspace);
         int64_t used = 0;
-        s = each_launch<NormPlan>(n, tensors, false, [&](NormPlan& plan, int32_t first) -> zs3_status {
+        bool ended = false;
+        s = each_launch<NormPlan>(n, tensors, false, [&](NormPlan& plan, int32_t first, bool last) -> zs3_status {
             const int64_t tiles = plan.first_tile[plan.n];
             plan.per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + kNormGroups - 1) / kNormGroups));
+            const int64_t here = 2 * ((tiles + plan.per - 1) / plan.per);
+            const bool ends = last && tiles > 0 && used + here <= kLastEntries;
+            bool few = ends;                    // its last workgroup joins the tensors' parts, too
+            for (int32_t i = 0; i < plan.n && few; ++i)
+                few = plan.first_tile[i + 1] - plan.first_tile[i] <= int64_t(kFewParts - 1) * plan.per;
+            double* each = a.tensor_norms != nullptr ? a.tensor_norms + first : nullptr;
             if (tiles > 0) {
-                const NormParts to{entries + used, a.tensor_norms != nullptr ? parts : nullptr};
-                const zs3_status e = launched(launch_norm(a.kind, plan, to, st), "norm kernel launch");
+                const NormParts to{entries, entries + used, each != nullptr ? parts : nullptr, ends ? counters : nullptr, few ? each : nullptr};
+                const zs3_status e = launched(launch_norm(a.kind, plan, to, end_of(a, a.finalize != 0), st), "norm kernel launch");
                 if (e != ZS3_OK) return e;
-                used += 2 * ((tiles + plan.per - 1) / plan.per);
+                used += here;
+                ended = ends;
             }
-            if (a.tensor_norms == nullptr) return ZS3_OK;
-            const zs3_status e = launched(launch_tensor_norms(a.kind, plan.first_tile, plan.n, plan.per, 1, parts,
-                                                              a.tensor_norms + first, st), "norm kernel launch");
+            if (each == nullptr || few) return ZS3_OK;
+            const zs3_status e = launched(launch_tensor_norms(a.kind, plan.first_tile, plan.n, plan.per, 1, parts, each, st),
+                                          "norm kernel launch");
             parts += kNormGroups + kNormTensors;
             return e;
         });
-        return s != ZS3_OK ? s : end_norm(used, w, a, st);
+        if (s != ZS3_OK) return s;
+        return ended ? ok() : end_norm(used, w, a, st);
     });
 }
 
@@ -362,7 +373,7 @@ zs3_status zs3_norm_finalize(const zs3_norm_args* norm, void* stream) {
         Ranges ranges(0);
         end_ranges(*norm, true, &ranges);
         if ((s = check_overlaps(ranges)) != ZS3_OK) return s;
-        s = launched(launch_norm_finalize(end_of(*norm), static_cast<hipStream_t>(stream)), "norm kernel launch");
+        s = launched(launch_norm_finalize(end_of(*norm, true), static_cast<hipStream_t>(stream)), "norm kernel launch");
         return s != ZS3_OK ? s : ok();
     });
 }
@@ -392,7 +403,7 @@ zs3_status zs3_clip_tensors(int32_t n, const zs3_grad_tensor* tensors, const flo
             ranges.written(t.out, size_of(t.out_dtype) * t.numel, i);
         }
         if ((s = check_overlaps(ranges)) != ZS3_OK) return s;
-        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t) -> zs3_status {
+        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t, bool) -> zs3_status {
             if (plan.first_tile[plan.n] == 0) return ZS3_OK;
             return launched(launch_clip(plan, scale, nonfinite, static_cast<hipStream_t>(stream)), "clip kernel launch");
         });
@@ -420,9 +431,9 @@ zs3_status zs3_accumulate_tensors(int32_t n, const zs3_grad_tensor* tensors, dou
         if (norm != nullptr && (s = check_norm(n, tensors, norm, &ranges)) != ZS3_OK) return s;
         if ((s = check_overlaps(ranges)) != ZS3_OK) return s;
         const hipStream_t st = static_cast<hipStream_t>(stream);
-        double* entries = norm != nullptr ? static_cast<double*>(norm->workspace) : nullptr;
+        double* entries = norm != nullptr ? static_cast<double*>(norm->workspace) + Workspace::entries : nullptr;
         int64_t used = 0;
-        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t at) -> zs3_status {
+        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t at, bool) -> zs3_status {
             const int64_t tiles = plan.first_tile[plan.n];
             double* to = entries != nullptr ? entries + used : nullptr;
             used += tiles;

@@ -129,10 +129,33 @@ __device__ __forceinline__ double entry(double x, bool shared) {
 }
 
 template <int KIND>
+__device__ __forceinline__ double root(double x) {
+    return KIND == kMax ? x : __builtin_sqrt(x);
+}
+
+// Over a wave, every lane gets it: within rows of 16 lanes by lane permutations, then over the
+// four rows through scalar registers (six steps through LDS instead: twice the time of a
+// small call's ends).
+template <int CTRL>
+__device__ __forceinline__ double permuted(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double of_lane(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <int KIND>
 __device__ __forceinline__ double wave_join(double x) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x = join<KIND>(x, __shfl_xor(x, o, 64));
-    return x;
+    x = join<KIND>(x, permuted<0xB1>(x));       // lane i and i ^ 1
+    x = join<KIND>(x, permuted<0x4E>(x));       // i ^ 2
+    x = join<KIND>(x, permuted<0x141>(x));      // the quads of 8 lanes, mirrored
+    x = join<KIND>(x, permuted<0x140>(x));      // the halves of 16
+    return join<KIND>(join<KIND>(of_lane(x, 0), of_lane(x, 16)), join<KIND>(of_lane(x, 32), of_lane(x, 48)));
 }
 
 // Over the workgroup of BLOCK threads; every thread gets it.  `sh` is free again afterwards.
@@ -164,7 +187,7 @@ template <int KIND>
 __device__ __forceinline__ void end_of_norm(const NormEnd& e, double peers, double own, double shared) {
     const double total = join<KIND>(join<KIND>(wave_join<KIND>(peers), own), shared);
     const bool bad = !(__builtin_fabs(total) <= 1.7976931348623157e308);
-    const double norm = (KIND == kMax ? total : __builtin_sqrt(total)) / e.loss_scale;
+    const double norm = root<KIND>(total) / e.loss_scale;
     double coef = e.max_norm / (norm + 1e-6);
     if (coef > 1.0) coef = 1.0;
     if ((threadIdx.x & 63) != 0) return;
@@ -343,7 +366,9 @@ template <int KIND, int BLOCK, bool FRESH>
 __device__ __forceinline__ void join_entries(const double* entries, int64_t i0, int64_t i1, double (&sh)[2 * (BLOCK / 64)],
                                              double& own, double& shared) {
     own = shared = 0.0;
-    constexpr int kBatch = 8;       // loads in flight of a thread
+    // loads in flight of a thread (in the norm's kernel 16 take it past 96 scalar registers, where
+    // seven of its waves fit a SIMD instead of eight: the ragged share 43 -> 50 us)
+    constexpr int kBatch = FRESH ? 8 : 16;
     for (int64_t i = i0 + threadIdx.x; i < i1; i += kBatch * BLOCK) {
         double x[kBatch];
 #pragma unroll
@@ -362,12 +387,14 @@ __device__ __forceinline__ void join_entries(const double* entries, int64_t i0, 
 }
 
 template <int KIND>
-__global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const NormParts parts, const NormEnd e) {
+__global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) void k_norm(const NormPlan plan, const NormParts parts, const NormEnd e) {
     __shared__ double sh[2 * (kGrBlock / 64)];
     __shared__ uint32_t last;
     const int32_t b = static_cast<int32_t>(blockIdx.x), all = plan.first_tile[plan.n];
     const int32_t t0 = b * plan.per, t1 = t0 + plan.per < all ? t0 + plan.per : all;
     int s = find_tensor(plan, t0, threadIdx.x & 63);
+    // the list's only workgroup: what it joins is in its registers
+    const bool alone = gridDim.x == 1 && parts.counters != nullptr && parts.entries == parts.all;
     double own = 0.0, shared = 0.0;
     Part<KIND> part;
     auto close = [&]() {        // the workgroup's part of tensor s is complete
@@ -376,7 +403,10 @@ __global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const No
         else own = join<KIND>(own, x);
         if (parts.tensors != nullptr) {
             const double y = group_join<KIND, kGrBlock>(x, sh);
-            if (threadIdx.x == 0) put<true>(parts.tensors + b + s, y);
+            if (threadIdx.x == 0) {
+                if (alone) parts.tensor_norms[s] = root<KIND>(y);
+                else put<true>(parts.tensors + b + s, y);
+            }
         }
         part = Part<KIND>();
     };
@@ -396,22 +426,27 @@ __global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const No
     }
     close();
     group_join2<KIND, kGrBlock>(own, shared, sh);
-    double* mine = parts.entries + 2 * int64_t(b);
-    if (threadIdx.x == 0) {
-        put<true>(mine, entry(own, false));
-        put<true>(mine + 1, entry(shared, true));
-        last = parts.counters != nullptr && ends_last(parts.counters, b, static_cast<int32_t>(gridDim.x)) ? 1u : 0u;
+    double peers = 0.0;
+    if (!alone) {
+        double* mine = parts.entries + 2 * int64_t(b);
+        if (threadIdx.x == 0) {
+            put<true>(mine, entry(own, false));
+            put<true>(mine + 1, entry(shared, true));
+            last = parts.counters != nullptr && ends_last(parts.counters, b, static_cast<int32_t>(gridDim.x)) ? 1u : 0u;
+        }
+        __syncthreads();
+        if (last == 0) return;
+        peers = peers_of<KIND>(e);
+        join_entries<KIND, kGrBlock, true>(parts.all, 0, mine - parts.all + 2 * int64_t(static_cast<int32_t>(gridDim.x) - b), sh, own, shared);
+    } else {
+        peers = peers_of<KIND>(e);
     }
-    __syncthreads();
-    if (last == 0) return;
-    const double peers = peers_of<KIND>(e);
-    join_entries<KIND, kGrBlock, true>(parts.all, 0, mine - parts.all + 2 * int64_t(static_cast<int32_t>(gridDim.x) - b), sh, own, shared);
     if (threadIdx.x == 0) {
         e.sums[e.rank] = own;
         e.sums[e.world] = shared;
     }
     if (e.finalize && threadIdx.x < 64) end_of_norm<KIND>(e, peers, own, shared);
-    if (parts.tensor_norms != nullptr) {
+    if (parts.tensor_norms != nullptr && !alone) {
         for (int i = static_cast<int>(threadIdx.x); i < plan.n; i += kGrBlock) {
             const int32_t f0 = plan.first_tile[i], f1 = plan.first_tile[i + 1];
             double x = 0.0;
@@ -426,7 +461,7 @@ __global__ __launch_bounds__(kGrBlock) void k_norm(const NormPlan plan, const No
                     for (int j = 0; j < kBatch; ++j) x = join<KIND>(x, y[j]);
                 }
             }
-            parts.tensor_norms[i] = KIND == kMax ? x : __builtin_sqrt(x);
+            parts.tensor_norms[i] = root<KIND>(x);
         }
     }
 }
@@ -498,7 +533,7 @@ __global__ __launch_bounds__(kGrBlock) void k_tensor_norms(const TensorTiles p, 
             x = join(kind, x, __builtin_fabs(at[i]));
     }
     x = kind == kMax ? group_join<kMax, kGrBlock>(x, sh) : group_join<kSum, kGrBlock>(x, sh);
-    if (threadIdx.x == 0) tensor_norms[s] = kind == kMax ? x : __builtin_sqrt(x);
+    if (threadIdx.x == 0) tensor_norms[s] = kind == kMax ? x : root<kSum>(x);
 }
 
 // Workgroup b joins `per` entries into two.
@@ -541,25 +576,34 @@ __global__ __launch_bounds__(64) void k_norm_finalize(const NormEnd e) {
 
 // Launches without the copies of a plan that a call by value makes.
 template <typename... A>
-static hipError_t launch(void (*kernel)(A...), int64_t groups, int threads, hipStream_t stream,
+static hipError_t launch(void (*kernel)(A...), int64_t groups, int threads, unsigned lds, hipStream_t stream,
                          const std::remove_const_t<A>&... args) {
     void* list[] = {const_cast<void*>(static_cast<const void*>(&args))...};
-    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<uint32_t>(groups)), dim3(threads), list, 0, stream);
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<uint32_t>(groups)), dim3(threads), list, lds, stream);
 }
 
 hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
     const int64_t groups = (int64_t(plan.first_tile[plan.n]) + plan.per - 1) / plan.per;
-    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, stream, plan, parts, end);
+    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, 0, stream, plan, parts, end);
 }
 
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream) {
-    return launch(k_clip, plan.first_tile[plan.n], kGrBlock, stream, plan, scale, nonfinite);
+    return launch(k_clip, plan.first_tile[plan.n], kGrBlock, 0, stream, plan, scale, nonfinite);
 }
+
+constexpr int64_t kManyTiles = 100000;      // 205M elements
 
 template <int OP>
 static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float factor, double* entries, hipStream_t stream) {
     auto kernel = kind == 0 ? k_accumulate<OP, 0> : kind == kMax ? k_accumulate<OP, kMax> : k_accumulate<OP, kSum>;
-    return launch(kernel, plan.first_tile[plan.n], kGrBlock, stream, plan, factor, entries);
+    // LDS that is reserved and never used: five workgroups a CU instead of eight (six with the
+    // sums, which keep a workgroup longer), as many streams as HBM takes best where a launch
+    // reads and writes gigabytes (the 1.0B elements of a share of 291 tensors 1655 -> 1560 us,
+    // 1630 -> 1564 with the sums; equal on 400 of 1M; smaller launches lose: 27M elements 50 ->
+    // 54 us)
+    const int64_t tiles = plan.first_tile[plan.n];
+    const unsigned lds = OP == kAdd && tiles >= kManyTiles ? (kind == 0 ? 32 : 26) * 1024u : 0;
+    return launch(kernel, tiles, kGrBlock, lds, stream, plan, factor, entries);
 }
 
 hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, double* entries, hipStream_t stream) {
@@ -574,19 +618,19 @@ hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t 
     p.per = per;
     p.skew = skew;
     for (int32_t i = 0; i <= n; ++i) p.first_tile[i] = first_tile[i];
-    return launch(k_tensor_norms, n, kGrBlock, stream, p, kind, parts, tensor_norms);
+    return launch(k_tensor_norms, n, kGrBlock, 0, stream, p, kind, parts, tensor_norms);
 }
 
 hipError_t launch_join(int32_t kind, const double* entries, int64_t n, int64_t per, double* to, hipStream_t stream) {
-    return launch(kind == kMax ? k_join<kMax> : k_join<kSum>, (n + per - 1) / per, kGrBlock, stream, entries, n, per, to);
+    return launch(kind == kMax ? k_join<kMax> : k_join<kSum>, (n + per - 1) / per, kGrBlock, 0, stream, entries, n, per, to);
 }
 
 hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end, hipStream_t stream) {
-    return launch(end.kind == kMax ? k_norm_end<kMax> : k_norm_end<kSum>, 1, kEndBlock, stream, entries, n, end);
+    return launch(end.kind == kMax ? k_norm_end<kMax> : k_norm_end<kSum>, 1, kEndBlock, 0, stream, entries, n, end);
 }
 
 hipError_t launch_norm_finalize(const NormEnd& end, hipStream_t stream) {
-    return launch(end.kind == kMax ? k_norm_finalize<kMax> : k_norm_finalize<kSum>, 1, 64, stream, end);
+    return launch(end.kind == kMax ? k_norm_finalize<kMax> : k_norm_finalize<kSum>, 1, 64, 0, stream, end);
 }
 
 }  // namespace zs3

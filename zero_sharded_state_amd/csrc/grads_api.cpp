@@ -340,7 +340,7 @@ zs3_status zs3_grad_norm_tensors(int32_t n, const zs3_grad_tensor* tensors, cons
         bool ended = false;
         s = each_launch<NormPlan>(n, tensors, false, [&](NormPlan& plan, int32_t first, bool last) -> zs3_status {
             const int64_t tiles = plan.first_tile[plan.n];
-            plan.per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + kNormGroups - 1) / kNormGroups));
+            plan.per = static_cast<int32_t>(std::max<int64_t>(1, tiles <= kAloneTiles ? tiles : (tiles + kNormGroups - 1) / kNormGroups));
             const int64_t here = 2 * ((tiles + plan.per - 1) / plan.per);
             const bool ends = last && tiles > 0 && used + here <= kLastEntries;
             bool few = ends;                    // its last workgroup joins the tensors' parts, too

@@ -212,3 +212,75 @@ def test_overlaps_are_found_in_any_order():
             moved[i][a_of] = cells[j][b_of] + (4 * sizes[j] - 4 if b_of else 2 * ((sizes[j] - 1) // 2) // 4 * 4)
             ts = [_t(numel=sizes[k], grad=moved[k][0], out=moved[k][1]) for k in order]
             _refused(zs.ZS3_EALIAS, "overlap", _acc, ts)
+
+
+# --------------------------------------------------------------- ShardStep
+
+def _host_step(**k):
+    from zero_sharded_state_amd.shard_step import ShardStep
+    return ShardStep(world_size=2, rank=1, threshold=0, ds_ids=[0, 1], numels=[64, 65], dtype="bf16", prefetch_bucket_size=1000,
+                     reduce_bucket_size=1000, sub_group_size=1000, device="cpu", **k)
+
+
+def test_shard_step_takes_micro_batches_in_order():
+    st = _host_step(accumulate=3, gather_bits=4)
+    assert st.listed and st.acc.numel() == st.S
+    with pytest.raises(ValueError, match="0 of 2 micro-batches"):
+        st.step()
+    with pytest.raises(ValueError, match="16-bit wire"):
+        st.micro_step(trace_pass=object())
+    assert (st.t, st.micro) == (0, 0)
+    st.micro = 2
+    with pytest.raises(ValueError, match="micro-batch 3 of 3"):
+        st.micro_step()
+    with pytest.raises(ValueError, match="no events"):
+        st.step(gather_timer=object())
+    assert (st.t, st.micro) == (0, 2)
+    st.destroy()
+    one = _host_step()
+    assert one.acc is None and not one.listed
+    with pytest.raises(ValueError, match="micro-batch 1 of 1"):
+        one.micro_step()
+    with pytest.raises(ValueError, match="no accumulators"):
+        one.accumulate_grads()
+    one.destroy()
+
+
+def test_shard_step_refuses_accumulation_it_cannot_do():
+    for k in (0, -1):
+        with pytest.raises(ValueError, match="accumulate"):
+            _host_step(accumulate=k)
+    with pytest.raises(TypeError):
+        _host_step(accumulate=1.5)
+    with pytest.raises(ValueError, match="16-bit gradients"):
+        _host_step(accumulate=2, offload=True)
+
+
+def test_shard_step_seeds_do_not_repeat_over_micro_batches():
+    """One micro-batch a step has the seeds it had; several have one each."""
+    seen = set()
+    for rank in (0, 1):
+        from zero_sharded_state_amd.shard_step import ShardStep
+        st = ShardStep(world_size=2, rank=rank, threshold=0, ds_ids=[0], numels=[64], dtype="bf16", prefetch_bucket_size=1000,
+                       reduce_bucket_size=1000, sub_group_size=1000, device="cpu", reduce_path="coalesced", reduce_bits=4, seed=7,
+                       accumulate=3)
+        for st.t in range(1, 6):
+            for st.micro in range(3):
+                for bucket in range(4):
+                    seen.add(st.wire_seed(bucket))
+        st.destroy()
+    assert len(seen) == 2 * 5 * 3 * 4
+    st = _host_step(seed=7)
+    st.t = 9
+    assert st.wire_seed(3) == 7 << 32 | (9 * 2 + 1) << 16 | 3
+    st.destroy()
+
+
+def test_shard_step_counts_the_bytes_of_every_micro_batch():
+    one, four = _host_step(), _host_step(accumulate=4)
+    a, b = one.algorithmic_bytes(), four.algorithmic_bytes()
+    own = one.own_real
+    assert b["unpack"] == 4 * a["unpack"] and b["reduce_scatter"] == 4 * a["reduce_scatter"]
+    assert b["accumulate"] == 4 * (2 + 4) * own + 3 * 4 * own
+    assert b["grad_norm"] == 4 * own and b["adam"] == a["adam"] + 2 * own
+    one.destroy(), four.destroy()

@@ -36,6 +36,13 @@ a value, ``gather_bits=4`` sends the gathers' chunks and ``reduce_bits=4`` (with
 the non-contiguous path) the gradients' over a 4-bit wire; ``no_decay`` names
 the parameters (norms, biases) that weight decay leaves alone.
 
+Several micro-batches a step (``accumulate=K``): ``micro_step`` runs 1 to 3 for
+each of the first K-1 and adds their averaged gradients, over K, to fp32
+accumulators; ``step`` does the same with the last one, takes the norm of the
+sum (with ``fuse_norm`` in the same pass) and steps on the sum.
+``grad_norms`` looks at each parameter's gradient, ``clip_grads`` scales them
+for an optimizer of the caller's own.
+
 No call synchronises; nothing is copied to the host.  All buffers are torch
 tensors owned by this object; all arithmetic runs in libzs3's kernels.
 """
@@ -44,6 +51,7 @@ from __future__ import annotations
 
 import ctypes
 import hashlib
+import operator
 from dataclasses import dataclass
 from typing import Dict, List, Sequence, Tuple
 
@@ -67,7 +75,7 @@ class ShardStep:
                  fuse_norm: bool = False, reduce_path: str = "contiguous", offload: bool = False,
                  offload_chunk: int = 0, recv_layout: str = "rank", single_launch="none",
                  state_bits: int = 32, gather_bits: int = 16, reduce_bits: int = 16,
-                 no_decay: Sequence[int] = (), seed: int = 0):
+                 no_decay: Sequence[int] = (), seed: int = 0, accumulate: int = 1):
         import torch
 
         if state_bits not in (8, 32):
@@ -78,11 +86,15 @@ class ShardStep:
             raise ValueError("gather_bits and reduce_bits are 4 or 16")
         if reduce_bits == 4 and reduce_path != "coalesced":
             raise ValueError("a 4-bit gradient wire needs the coalesced gradient path")
-        # the list step holds for 8-bit moments and for a decay by parameter
+        accumulate = operator.index(accumulate)
+        if accumulate < 1:
+            raise ValueError(f"accumulate {accumulate!r} < 1")
+        # the list step holds for 8-bit moments, for a decay by parameter and for fp32 gradients
         no_decay = frozenset(no_decay)
-        self.listed = state_bits == 8 or bool(no_decay)
+        self.listed = state_bits == 8 or bool(no_decay) or accumulate > 1
         if self.listed and offload:
-            raise ValueError("offloaded state has 32 bits and one weight decay")
+            raise ValueError("offloaded state has 32 bits and one weight decay, and steps on 16-bit gradients")
+        self.accumulate, self.micro = accumulate, 0     # micro: accumulated in the step under way
         unknown = no_decay - set(ds_ids)
         if unknown:
             raise ValueError(f"no_decay names ds_ids that are not there: {sorted(unknown)}")
@@ -226,6 +238,7 @@ class ShardStep:
         if state_bits == 32:
             self.exp_avg = self.state[sa:sa + max(1, self.S)]
             self.exp_avg_sq = self.state[2 * sa:2 * sa + max(1, self.S)]
+        self.acc = torch.zeros(max(1, self.S), dtype=f32, device=dev) if accumulate > 1 else None
         self.sumsq = torch.zeros(self.N + 1, dtype=torch.float64, device=dev)
         self.n_slots, _ = zs.zs3_layout_norm_slots(self.h)
         self.partials = torch.zeros(max(1, self.n_slots), dtype=torch.float64, device=dev)
@@ -380,6 +393,12 @@ class ShardStep:
             self._listed_decay = self.adam.weight_decay
             self._lists = [zs.zs3_adamw_tensor_list([self._tensor(p) for p in self.params if b <= p["shard_offset"] < e])
                            for b, e in self.sub_groups]
+        self._grad_list = None
+        if self.accumulate > 1:
+            self._acc_list = zs.zs3_grad_tensor_list([
+                dict(self._gradient(p, self.grad, self.dtype), out=self.acc.data_ptr() + 4 * p["shard_offset"], out_dtype="fp32")
+                for p in self.params])
+            self._held()
         all_ids = [p["ds_id"] for p in self.params]
         self._p = (len(all_ids), (I64 * len(all_ids))(*all_ids),
                    (P * len(all_ids))(*[self.full_param_ptr(d) for d in all_ids]))
@@ -398,12 +417,18 @@ class ShardStep:
             self._rm = (len(rs_ids), (I64 * len(rs_ids))(*rs_ids),
                         (P * (len(rs_ids) * self.N))(*[self.recv_ptr(v, d) for d in rs_ids for v in range(self.N)]))
 
+    def _gradient(self, p, buf, dtype: str) -> dict:
+        """A parameter's real elements of a flat gradient as an entry of a gradient list."""
+        return dict(numel=p["own"][1] - p["own"][0], grad=buf.data_ptr() + buf.element_size() * p["shard_offset"], dtype=dtype,
+                    shared=p["persistent"])
+
     def _tensor(self, p) -> dict:
         """A parameter's real elements as an entry of the list step."""
         d, o = p["ds_id"], p["shard_offset"]
+        g = self.grad if self.acc is None else self.acc
         m = self.moment_off[d] if self.state_bits == 8 else 4 * o
         return dict(numel=p["own"][1] - p["own"][0], id=d, master=self.master.data_ptr() + 4 * o,
-                    grad=self.grad.data_ptr() + 2 * o, param=self.shard.data_ptr() + 2 * o,
+                    grad=g.data_ptr() + g.element_size() * o, param=self.shard.data_ptr() + 2 * o,
                     exp_avg=self.exp_avg.data_ptr() + m, exp_avg_sq=self.exp_avg_sq.data_ptr() + m,
                     weight_decay=0.0 if d in self.no_decay else self.adam.weight_decay)
 
@@ -497,7 +522,8 @@ class ShardStep:
         """Every gradient bucket, fanned out over the main and auxiliary
         streams and joined back into the main stream."""
         lib = zs.lib()
-        partials = self.partials.data_ptr() if self.fuse_norm else None
+        # with accumulators it is their sum that has a norm
+        partials = self.partials.data_ptr() if self.fuse_norm and self.acc is None else None
         if self.single_reduce:
             n, ids, src = self._rm
             self._ok(lib.zs3_reduce_scatter_local(self.h, self.rank, self.dcode, n, ids, src, self.grad.data_ptr(),
@@ -521,11 +547,11 @@ class ShardStep:
 
     def wire_seed(self, bucket: int) -> int:
         """Seed of a gradient bucket's rounding in the step under way: another
-        one for every seed, rank, step and bucket.  32 + 16 + 16 bits hold the
-        seed, the count of steps and ranks and the bucket; from where one does
+        one for every seed, rank, micro-batch, step and bucket.  32 + 16 + 16 bits hold the
+        seed, the count of micro-batches and ranks and the bucket; from where one does
         not fit (it would run into the next, and repeat another seed's words)
         the three are hashed."""
-        seed, count = self.seed & (1 << 64) - 1, self.t * self.N + self.rank
+        seed, count = self.seed & (1 << 64) - 1, (self.t * self.accumulate + self.micro) * self.N + self.rank
         if seed >> 32 == 0 and count >> 16 == 0 and bucket >> 16 == 0:
             return seed << 32 | count << 16 | bucket
         key = b"%d %d %d" % (seed, count, bucket)
@@ -540,7 +566,53 @@ class ShardStep:
         self._ok(zs.lib().zs3_partition(self.h, self.rank, self.dcode, n, ids, ptrs, out.data_ptr(),
                                         stream if stream is not None else self._stream()))
 
+    def _held(self):
+        """The gradient that the norm and the clip see, as a list: the sum, or the flat gradient."""
+        if self._grad_list is None:
+            held, kind = (self.grad, self.dtype) if self.acc is None else (self.acc, "fp32")
+            self._grad_list = zs.zs3_grad_tensor_list([self._gradient(p, held, kind) for p in self.params])
+            self.norm_workspace = self.torch.zeros(zs.zs3_norm_workspace_bytes(self._grad_list), dtype=self.torch.uint8,
+                                                   device=self.device)
+        return self._grad_list
+
+    def _norm_args(self, finalize: bool, **over):
+        return zs.zs3_norm_args_of(**dict(
+            dict(rank=self.rank, world=self.N, finalize=finalize, max_norm=self.max_norm, sums=self.sumsq, norm=self.norm_ptr,
+                 scale=self.scale_ptr, nonfinite=self.flag_ptr, workspace=self.norm_workspace), **over))
+
+    def accumulate_grads(self, stream=None, norm: bool = False):
+        """Adds the flat gradient, over the number of micro-batches, to the
+        accumulators (the first of a step overwrites them), with the norm of the sum where asked."""
+        if self.acc is None:
+            raise ValueError("accumulate is 1: there are no accumulators")
+        args = self._norm_args(True) if norm else None
+        zs.zs3_accumulate_tensors(self._acc_list, 1.0 / self.accumulate, first=self.micro == 0, norm=args,
+                                  stream=stream if stream is not None else self._stream())
+
+    def grad_norms(self, inf: bool = False, stream=None):
+        """The norm of each parameter's real elements of the gradient that the step
+        holds (the sum of the micro-batches so far, if it accumulates), as doubles in the
+        order of ``params``; with ``inf`` the largest magnitude.  The clip norm and its
+        sums are left alone.  On the step's own stream, whose workspace it uses."""
+        torch = self.torch
+        held = self._held()
+        each = torch.empty(len(self.params), dtype=torch.float64, device=self.device)
+        sums = torch.empty(2, dtype=torch.float64, device=self.device)
+        args = self._norm_args(False, rank=0, world=1, sums=sums, tensor_norms=each, kind=zs.ZS3_NORM_INF if inf else zs.ZS3_NORM_2)
+        zs.zs3_grad_norm_tensors(held, args, stream=stream if stream is not None else self._stream())
+        return each
+
+    def clip_grads(self, stream=None):
+        """Multiplies the gradient that the step holds by the clip scale of the last norm, in place
+        (nothing, where the norm was not finite): for an optimizer of the caller's own in
+        place of ``adam_step``, which takes the scale itself."""
+        zs.zs3_clip_tensors(self._held(), self.scale_ptr, self.flag_ptr, stream=stream if stream is not None else self._stream())
+
     def grad_norm(self, finalize: bool = True, stream=None):
+        if self.acc is not None:
+            zs.zs3_grad_norm_tensors(self._held(), self._norm_args(finalize),
+                                     stream=stream if stream is not None else self._stream())
+            return
         if self.fuse_norm:
             self._ok(zs.lib().zs3_grad_norm_partials(self.h, self.rank, self.partials.data_ptr(),
                                                      self.sumsq.data_ptr(), int(finalize), self.max_norm, 1.0,
@@ -562,7 +634,8 @@ class ShardStep:
                         x.weight_decay = 0.0 if x.id in self.no_decay else a.weight_decay
                 self._listed_decay = a.weight_decay
             for tensors in self._lists:
-                self._ok(zs.lib().zs3_adamw_tensors(self.dcode, self.dcode, self.state_bits, tensors.count, tensors,
+                self._ok(zs.lib().zs3_adamw_tensors(self.dcode, self.dcode if self.acc is None else zs.ZS3_FP32,
+                                                    self.state_bits, tensors.count, tensors,
                                                     self.scale_ptr, self.flag_ptr, ctypes.byref(hp), self.seed, s))
             return
         if self.offload:
@@ -580,17 +653,8 @@ class ShardStep:
                                             self.grad.data_ptr(), self.shard.data_ptr(), self.scale_ptr,
                                             self.flag_ptr, ctypes.byref(hp), s))
 
-    def step(self, stream=None, on_phase=None, gather_timer=None, trace_pass=None):
-        """One whole shard step; ``on_phase(name)`` is called before each phase
-        and with None at the end (for event timing).  With ``trace_pass`` (a
-        TraceGatherPass) the forward and backward gathers follow the
-        fetch/release coordinator instead of the static gather buckets."""
-        if trace_pass is not None and self.gather_bits == 4:
-            raise ValueError("the coordinator's gathers run on the 16-bit wire")
-        if gather_timer is not None and self.gather_bits == 4:
-            raise ValueError("the 4-bit gathers record no events")
-        self.t += 1
-        mark = on_phase or (lambda name: None)
+    def _gather_and_reduce(self, stream, mark, gather_timer, trace_pass):
+        """A micro-batch's gathers and reduce-scatter."""
         if trace_pass is not None:
             mark("gather_trace")
             trace_pass.run(stream)
@@ -601,10 +665,50 @@ class ShardStep:
             self.gather_pass(stream, gather_timer)
         mark("reduce_scatter")
         self.reduce_scatter(stream)
+
+    def _check_wire(self, gather_timer, trace_pass):
+        if trace_pass is not None and self.gather_bits == 4:
+            raise ValueError("the coordinator's gathers run on the 16-bit wire")
+        if gather_timer is not None and self.gather_bits == 4:
+            raise ValueError("the 4-bit gathers record no events")
+
+    def micro_step(self, stream=None, on_phase=None, gather_timer=None, trace_pass=None):
+        """One of a step's micro-batches but the last: gathers, reduce-scatter,
+        accumulation.  Arguments as for ``step``, which takes the last one."""
+        if self.micro >= self.accumulate - 1:
+            raise ValueError(f"micro-batch {self.micro + 1} of {self.accumulate} is step()'s")
+        self._check_wire(gather_timer, trace_pass)
+        if self.micro == 0:
+            self.t += 1
+        mark = on_phase or (lambda name: None)
+        self._gather_and_reduce(stream, mark, gather_timer, trace_pass)
+        mark("accumulate")
+        self.accumulate_grads(stream)
+        self.micro += 1
+        mark(None)
+
+    def step(self, stream=None, on_phase=None, gather_timer=None, trace_pass=None):
+        """One whole shard step (with ``accumulate`` = K its last micro-batch, after
+        K-1 calls of ``micro_step``); ``on_phase(name)`` is called before each phase
+        and with None at the end (for event timing).  With ``trace_pass`` (a
+        TraceGatherPass) the forward and backward gathers follow the
+        fetch/release coordinator instead of the static gather buckets."""
+        self._check_wire(gather_timer, trace_pass)
+        if self.micro != self.accumulate - 1:
+            raise ValueError(f"{self.micro} of {self.accumulate - 1} micro-batches before step()")
+        if self.micro == 0:
+            self.t += 1
+        mark = on_phase or (lambda name: None)
+        self._gather_and_reduce(stream, mark, gather_timer, trace_pass)
+        if self.acc is not None:
+            mark("accumulate")
+            self.accumulate_grads(stream, norm=self.fuse_norm)
+            self.micro = 0
         # the pre-step pass ([codex] 6.3): the gathered views are dropped;
         # the shard already is the partitioned form, so nothing moves
-        mark("grad_norm")
-        self.grad_norm(True, stream)
+        if self.acc is None or not self.fuse_norm:
+            mark("grad_norm")
+            self.grad_norm(True, stream)
         mark("adam")
         self.adam_step(self.t, stream)
         mark(None)
@@ -656,7 +760,8 @@ class ShardStep:
 
     # --------------------------------------------------------- accounting
     def algorithmic_bytes(self) -> Dict[str, int]:
-        """Bytes each part of the step must move (real elements only)."""
+        """Bytes each part of the step must move (real elements only); with several
+        micro-batches, of all of them."""
         N = self.N
         part_real = sum(p["own"][1] - p["own"][0] for p in self.params if not p["persistent"])
         own = self.own_real
@@ -682,6 +787,12 @@ class ShardStep:
             if self.reduce_bits == 4:
                 pers = sum(p["numel"] for p in self.params if p["persistent"])
                 out["reduce_scatter"] = N * chunks + 2 * own + 2 * N * pers
+        if self.acc is not None:                # fp32 sums: written by each micro-batch, read by all but the first
+            K = self.accumulate
+            out = {k: v * (1 if k in ("grad_norm", "adam") else K) for k, v in out.items()}
+            out["accumulate"] = K * 6 * own + (K - 1) * 4 * own
+            out["grad_norm"] *= 2
+            out["adam"] += 2 * own
         return out
 
     def budget_bytes(self) -> int:

@@ -13,6 +13,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "grads.hpp"
@@ -235,7 +236,7 @@ template <int OP, int KIND, int G, int O, bool WHOLE>
 __device__ __forceinline__ void tile(const Elem<G>* grad, Elem<O>* out, int lo, int hi, float f, Part<KIND>& part) {
     constexpr int V = (OP == kNorm ? G : O) == kFP32 ? 4 : 8;      // elements of a 16-byte vector of the main array
     constexpr int kStep = V * kGrBlock;
-    const int t = static_cast<int>(threadIdx.x);
+    const int t = static_cast<int>(threadIdx.x) & (kGrBlock - 1);
     int v0 = 0, v1 = 0, edge = 0;       // the whole vectors, and this thread's single element
     bool single = false;
     Elem<G> xe = {};
@@ -386,6 +387,17 @@ __device__ __forceinline__ void join_entries(const double* entries, int64_t i0, 
     group_join2<KIND, BLOCK>(own, shared, sh);
 }
 
+template <int KIND, class PLAN>
+__device__ __forceinline__ void norm_tile(const PLAN& plan, int s, int32_t t, Part<KIND>& part) {
+    const uint32_t meta = plan.meta[s], last = meta & 0xffffu;
+    const int32_t f0 = plan.first_tile[s], n = plan.first_tile[s + 1] - f0;
+    const int g = meta >> 16 & 3;
+    const void* grad = plan.grad[s];
+    if (g == kFP16) typed_tile<kNorm, KIND, kFP16, kFP16>(grad, nullptr, t - f0, n, last, 1.0f, part);
+    else if (g == kBF16) typed_tile<kNorm, KIND, kBF16, kBF16>(grad, nullptr, t - f0, n, last, 1.0f, part);
+    else typed_tile<kNorm, KIND, kFP32, kFP32>(grad, nullptr, t - f0, n, last, 1.0f, part);
+}
+
 template <int KIND>
 __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) void k_norm(const NormPlan plan, const NormParts parts, const NormEnd e) {
     __shared__ double sh[2 * (kGrBlock / 64)];
@@ -393,8 +405,6 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
     const int32_t b = static_cast<int32_t>(blockIdx.x), all = plan.first_tile[plan.n];
     const int32_t t0 = b * plan.per, t1 = t0 + plan.per < all ? t0 + plan.per : all;
     int s = find_tensor(plan, t0, threadIdx.x & 63);
-    // the list's only workgroup: what it joins is in its registers
-    const bool alone = gridDim.x == 1 && parts.counters != nullptr && parts.entries == parts.all;
     double own = 0.0, shared = 0.0;
     Part<KIND> part;
     auto close = [&]() {        // the workgroup's part of tensor s is complete
@@ -403,10 +413,7 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
         else own = join<KIND>(own, x);
         if (parts.tensors != nullptr) {
             const double y = group_join<KIND, kGrBlock>(x, sh);
-            if (threadIdx.x == 0) {
-                if (alone) parts.tensor_norms[s] = root<KIND>(y);
-                else put<true>(parts.tensors + b + s, y);
-            }
+            if (threadIdx.x == 0) put<true>(parts.tensors + b + s, y);
         }
         part = Part<KIND>();
     };
@@ -416,37 +423,26 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
             do ++s;
             while (t >= plan.first_tile[s + 1]);
         }
-        const uint32_t meta = plan.meta[s], last = meta & 0xffffu;
-        const int32_t f0 = plan.first_tile[s], n = plan.first_tile[s + 1] - f0;
-        const int g = meta >> 16 & 3;
-        const void* grad = plan.grad[s];
-        if (g == kFP16) typed_tile<kNorm, KIND, kFP16, kFP16>(grad, nullptr, t - f0, n, last, 1.0f, part);
-        else if (g == kBF16) typed_tile<kNorm, KIND, kBF16, kBF16>(grad, nullptr, t - f0, n, last, 1.0f, part);
-        else typed_tile<kNorm, KIND, kFP32, kFP32>(grad, nullptr, t - f0, n, last, 1.0f, part);
+        norm_tile<KIND>(plan, s, t, part);
     }
     close();
     group_join2<KIND, kGrBlock>(own, shared, sh);
-    double peers = 0.0;
-    if (!alone) {
-        double* mine = parts.entries + 2 * int64_t(b);
-        if (threadIdx.x == 0) {
-            put<true>(mine, entry(own, false));
-            put<true>(mine + 1, entry(shared, true));
-            last = parts.counters != nullptr && ends_last(parts.counters, b, static_cast<int32_t>(gridDim.x)) ? 1u : 0u;
-        }
-        __syncthreads();
-        if (last == 0) return;
-        peers = peers_of<KIND>(e);
-        join_entries<KIND, kGrBlock, true>(parts.all, 0, mine - parts.all + 2 * int64_t(static_cast<int32_t>(gridDim.x) - b), sh, own, shared);
-    } else {
-        peers = peers_of<KIND>(e);
+    double* mine = parts.entries + 2 * int64_t(b);
+    if (threadIdx.x == 0) {
+        put<true>(mine, entry(own, false));
+        put<true>(mine + 1, entry(shared, true));
+        last = parts.counters != nullptr && ends_last(parts.counters, b, static_cast<int32_t>(gridDim.x)) ? 1u : 0u;
     }
+    __syncthreads();
+    if (last == 0) return;
+    const double peers = peers_of<KIND>(e);
+    join_entries<KIND, kGrBlock, true>(parts.all, 0, mine - parts.all + 2 * int64_t(static_cast<int32_t>(gridDim.x) - b), sh, own, shared);
     if (threadIdx.x == 0) {
         e.sums[e.rank] = own;
         e.sums[e.world] = shared;
     }
     if (e.finalize && threadIdx.x < 64) end_of_norm<KIND>(e, peers, own, shared);
-    if (parts.tensor_norms != nullptr && !alone) {
+    if (parts.tensor_norms != nullptr) {
         for (int i = static_cast<int>(threadIdx.x); i < plan.n; i += kGrBlock) {
             const int32_t f0 = plan.first_tile[i], f1 = plan.first_tile[i + 1];
             double x = 0.0;
@@ -466,12 +462,42 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
     }
 }
 
+// A list of few tiles, each of 256 threads; what they have joined meets in LDS.
+template <int KIND>
+__global__ __launch_bounds__(kGrBlock* kFewTiles) void k_norm_few(const NormPlanOf<kFewTensors> plan, const NormEnd e,
+                                                                   double* __restrict__ tensor_norms) {
+    constexpr int kWaves = kGrBlock / 64;
+    __shared__ double sh[kFewTiles * kWaves];
+    const int lane = static_cast<int>(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int32_t t = wave / kWaves;
+    const double peers = peers_of<KIND>(e);
+    Part<KIND> part;
+    if (t < plan.first_tile[plan.n]) norm_tile<KIND>(plan, find_tensor(plan, t, lane), t, part);
+    const double x = wave_join<KIND>(part.value());
+    if (lane == 0) sh[wave] = x;
+    __syncthreads();
+    if (wave != 0) return;
+    // a lane a tensor
+    double mine = 0.0;
+    const int s = lane < plan.n ? lane : 0;
+    const int32_t f1 = lane < plan.n ? plan.first_tile[s + 1] : 0;
+    for (int32_t i = plan.first_tile[s] * kWaves; i < f1 * kWaves; ++i) mine = join<KIND>(mine, sh[i]);
+    if (tensor_norms != nullptr && lane < plan.n) tensor_norms[lane] = root<KIND>(mine);
+    const bool second = lane < plan.n && (plan.meta[s] >> 20 & 1) != 0;
+    const double own = wave_join<KIND>(second ? 0.0 : mine), shared = wave_join<KIND>(second ? mine : 0.0);
+    if (lane == 0) {
+        e.sums[e.rank] = own;
+        e.sums[e.world] = shared;
+    }
+    if (e.finalize) end_of_norm<KIND>(e, peers, own, shared);
+}
+
 // ------------------------------------------------------------ writing
 // Bound by HBM.  A workgroup a tile (8 KB written): with reads and writes in flight short
 // workgroups that follow the arrays' order stream fastest.
 
-template <int OP, int KIND, int O>
-__device__ __forceinline__ void write_tile(const WritePlan& plan, int s, int32_t t, float f, Part<KIND>& part) {
+template <int OP, int KIND, int O, class PLAN>
+__device__ __forceinline__ void write_tile(const PLAN& plan, int s, int32_t t, float f, Part<KIND>& part) {
     const uint32_t meta = plan.meta[s], last = meta & 0xffffu;
     const int32_t f0 = plan.first_tile[s], n = plan.first_tile[s + 1] - f0;
     const int g = meta >> 16 & 3;
@@ -482,7 +508,8 @@ __device__ __forceinline__ void write_tile(const WritePlan& plan, int s, int32_t
     else typed_tile<OP, KIND, kFP32, O>(grad, out, t - f0, n, last, f, part);
 }
 
-__global__ __launch_bounds__(kGrBlock) void k_clip(const WritePlan plan, const float* __restrict__ scale,
+template <int N>
+__global__ __launch_bounds__(kGrBlock) void k_clip(const WritePlanOf<N> plan, const float* __restrict__ scale,
                                                    const int32_t* __restrict__ nonfinite) {
     const int32_t b = static_cast<int32_t>(blockIdx.x);
     const int32_t flag = nonfinite != nullptr ? *nonfinite : 0;
@@ -498,8 +525,8 @@ __global__ __launch_bounds__(kGrBlock) void k_clip(const WritePlan plan, const f
 
 // KIND 0: without sums; otherwise a tile's goes to its entry, negative where the
 // tensor is shared.
-template <int OP, int KIND>
-__global__ __launch_bounds__(kGrBlock) void k_accumulate(const WritePlan plan, float f, double* __restrict__ entries) {
+template <int OP, int KIND, int N>
+__global__ __launch_bounds__(kGrBlock) void k_accumulate(const WritePlanOf<N> plan, float f, double* __restrict__ entries) {
     const int32_t b = static_cast<int32_t>(blockIdx.x);
     const int s = find_tensor(plan, b, threadIdx.x & 63);
     Part<KIND> part;
@@ -587,15 +614,42 @@ hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& part
     return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, 0, stream, plan, parts, end);
 }
 
+// A plan of at most kFewTensors in a smaller one (the places past its end are copied, too: the
+// search counts on them).
+static NormPlanOf<kFewTensors> few(const NormPlan& plan) {
+    NormPlanOf<kFewTensors> p;
+    p.n = plan.n;
+    p.per = plan.per;
+    std::copy_n(plan.first_tile, kFewTensors + 1, p.first_tile);
+    std::copy_n(plan.meta, plan.n, p.meta);
+    std::copy_n(plan.grad, plan.n, p.grad);
+    return p;
+}
+static WritePlanOf<kFewTensors> few(const WritePlan& plan) {
+    WritePlanOf<kFewTensors> p;
+    p.n = plan.n;
+    std::copy_n(plan.first_tile, kFewTensors + 1, p.first_tile);
+    std::copy_n(plan.meta, plan.n, p.meta);
+    std::copy_n(plan.grad, plan.n, p.grad);
+    std::copy_n(plan.out, plan.n, p.out);
+    return p;
+}
+
+hipError_t launch_norm_few(const NormPlan& plan, const NormEnd& end, double* tensor_norms, hipStream_t stream) {
+    return launch(end.kind == kMax ? k_norm_few<kMax> : k_norm_few<kSum>, 1, kGrBlock * kFewTiles, 0, stream, few(plan), end,
+                  tensor_norms);
+}
+
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream) {
-    return launch(k_clip, plan.first_tile[plan.n], kGrBlock, 0, stream, plan, scale, nonfinite);
+    const int64_t tiles = plan.first_tile[plan.n];
+    if (plan.n <= kFewTensors) return launch(k_clip<kFewTensors>, tiles, kGrBlock, 0, stream, few(plan), scale, nonfinite);
+    return launch(k_clip<kWriteTensors>, tiles, kGrBlock, 0, stream, plan, scale, nonfinite);
 }
 
 constexpr int64_t kManyTiles = 100000;      // 205M elements
 
 template <int OP>
 static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float factor, double* entries, hipStream_t stream) {
-    auto kernel = kind == 0 ? k_accumulate<OP, 0> : kind == kMax ? k_accumulate<OP, kMax> : k_accumulate<OP, kSum>;
     // LDS that is reserved and never used: five workgroups a CU instead of eight (six with the
     // sums, which keep a workgroup longer), as many streams as HBM takes best where a launch
     // reads and writes gigabytes (the 1.0B elements of a share of 291 tensors 1655 -> 1560 us,
@@ -603,6 +657,11 @@ static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float f
     // 54 us)
     const int64_t tiles = plan.first_tile[plan.n];
     const unsigned lds = OP == kAdd && tiles >= kManyTiles ? (kind == 0 ? 32 : 26) * 1024u : 0;
+    if (plan.n <= kFewTensors) {
+        auto kernel = kind == 0 ? k_accumulate<OP, 0, kFewTensors> : kind == kMax ? k_accumulate<OP, kMax, kFewTensors> : k_accumulate<OP, kSum, kFewTensors>;
+        return launch(kernel, tiles, kGrBlock, lds, stream, few(plan), factor, entries);
+    }
+    auto kernel = kind == 0 ? k_accumulate<OP, 0, kWriteTensors> : kind == kMax ? k_accumulate<OP, kMax, kWriteTensors> : k_accumulate<OP, kSum, kWriteTensors>;
     return launch(kernel, tiles, kGrBlock, lds, stream, plan, factor, entries);
 }
 

@@ -31,30 +31,38 @@ constexpr uint32_t gr_meta(int64_t last, int32_t dtype, int32_t out_dtype, bool 
            (shared ? 1u << 20 : 0u);
 }
 
-struct NormPlan {
+template <int N>
+struct NormPlanOf {
     int32_t n;
     int32_t per;            // tiles of a workgroup, one behind the other
-    int32_t first_tile[kNormTensors + 1];
-    uint32_t meta[kNormTensors];
-    const void* grad[kNormTensors];
+    int32_t first_tile[N + 1];
+    uint32_t meta[N];
+    const void* grad[N];
 };
+using NormPlan = NormPlanOf<kNormTensors>;
 static_assert(sizeof(NormPlan) <= 3840, "the plan has to fit the kernel arguments");
 
-struct WritePlan {
+template <int N>
+struct WritePlanOf {
     int32_t n;
-    int32_t first_tile[kWriteTensors + 1];
-    uint32_t meta[kWriteTensors];
-    const void* grad[kWriteTensors];
-    void* out[kWriteTensors];
+    int32_t first_tile[N + 1];
+    uint32_t meta[N];
+    const void* grad[N];
+    void* out[N];
 };
+using WritePlan = WritePlanOf<kWriteTensors>;
 static_assert(sizeof(WritePlan) <= 3840, "the plan has to fit the kernel arguments");
+
+// Tensors up to which a launch takes a plan of its own size: 4 KB of arguments cost the host 0.3 us
+// (the toy model's call 4.9 -> 4.6).
+constexpr int kFewTensors = 16;
 
 // Workgroups of a launch of the norm: each takes a run of tiles, so that there are
 // few partial results and the run's sum stays in registers.
 constexpr int kNormGroups = 2048;
-// Tiles up to which one workgroup takes the list: what it has joined then need not reach
-// another one (a tensor of 2,048 elements 5.3 -> 3.1 us, four tiles 5.4 -> 4.6, eight 5.6 -> 6.9).
-constexpr int64_t kAloneTiles = 4;
+// Tiles up to which one workgroup takes a list of few tensors, each tile by 256 threads of its
+// own, all at once (four tensors with their norms 6.1 -> FEWUS us on the GPU).
+constexpr int kFewTiles = 4;
 
 // Partial results in the workspace.  An entry is a sum of squares or a largest magnitude,
 // with a minus sign where its tensors are shared.  A launch of the norm leaves two a
@@ -99,6 +107,8 @@ struct NormEnd {
 };
 
 hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream);
+// The whole norm of a list of at most kFewTensors tensors and kFewTiles tiles (per is not read).
+hipError_t launch_norm_few(const NormPlan& plan, const NormEnd& end, double* tensor_norms, hipStream_t stream);
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream);
 // kind 0: without sums (entries may be null)
 hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, double* entries,

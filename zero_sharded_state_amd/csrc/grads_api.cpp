@@ -340,13 +340,17 @@ zs3_status zs3_grad_norm_tensors(int32_t n, const zs3_grad_tensor* tensors, cons
         bool ended = false;
         s = each_launch<NormPlan>(n, tensors, false, [&](NormPlan& plan, int32_t first, bool last) -> zs3_status {
             const int64_t tiles = plan.first_tile[plan.n];
-            plan.per = static_cast<int32_t>(std::max<int64_t>(1, tiles <= kAloneTiles ? tiles : (tiles + kNormGroups - 1) / kNormGroups));
+            double* each = a.tensor_norms != nullptr ? a.tensor_norms + first : nullptr;
+            if (plan.n == n && n <= kFewTensors && tiles <= kFewTiles) {
+                ended = true;
+                return launched(launch_norm_few(plan, end_of(a, a.finalize != 0), each, st), "norm kernel launch");
+            }
+            plan.per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + kNormGroups - 1) / kNormGroups));
             const int64_t here = 2 * ((tiles + plan.per - 1) / plan.per);
             const bool ends = last && tiles > 0 && used + here <= kLastEntries;
             bool few = ends;                    // its last workgroup joins the tensors' parts, too
             for (int32_t i = 0; i < plan.n && few; ++i)
                 few = plan.first_tile[i + 1] - plan.first_tile[i] <= int64_t(kFewParts - 1) * plan.per;
-            double* each = a.tensor_norms != nullptr ? a.tensor_norms + first : nullptr;
             if (tiles > 0) {
                 const NormParts to{entries, entries + used, each != nullptr ? parts : nullptr, ends ? counters : nullptr, few ? each : nullptr};
                 const zs3_status e = launched(launch_norm(a.kind, plan, to, end_of(a, a.finalize != 0), st), "norm kernel launch");

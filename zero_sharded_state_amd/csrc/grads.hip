@@ -647,16 +647,16 @@ hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t*
 }
 
 constexpr int64_t kManyTiles = 100000;      // 205M elements
+constexpr unsigned kManyLds = 32 * 1024;
 
 template <int OP>
 static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float factor, double* entries, hipStream_t stream) {
-    // LDS that is reserved and never used: five workgroups a CU instead of eight (six with the
-    // sums, which keep a workgroup longer), as many streams as HBM takes best where a launch
-    // reads and writes gigabytes (the 1.0B elements of a share of 291 tensors 1655 -> 1560 us,
-    // 1630 -> 1564 with the sums; equal on 400 of 1M; smaller launches lose: 27M elements 50 ->
-    // 54 us)
+    // LDS that is reserved and never used: five workgroups a CU instead of eight, as many
+    // streams as HBM takes best where a launch reads and writes gigabytes (the 1.0B elements
+    // of a share of 291 tensors 1655 -> 1560 us, with the sums 1625 -> 1573; equal on 400
+    // of 1M; smaller launches lose: 27M elements 50 -> 54 us)
     const int64_t tiles = plan.first_tile[plan.n];
-    const unsigned lds = OP == kAdd && tiles >= kManyTiles ? (kind == 0 ? 32 : 26) * 1024u : 0;
+    const unsigned lds = OP == kAdd && tiles >= kManyTiles ? kManyLds : 0;
     if (plan.n <= kFewTensors) {
         auto kernel = kind == 0 ? k_accumulate<OP, 0, kFewTensors> : kind == kMax ? k_accumulate<OP, kMax, kFewTensors> : k_accumulate<OP, kSum, kFewTensors>;
         return launch(kernel, tiles, kGrBlock, lds, stream, few(plan), factor, entries);

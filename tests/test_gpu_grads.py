@@ -488,6 +488,29 @@ def test_same_bits_again_and_in_a_workspace_of_other_lists():
     assert all(len(s) == 2 for s in seen)
 
 
+def test_every_call_sees_its_own_partial_results():
+    """Calls in a row on one workspace, the gradients a power of two larger each time:
+    norm, sums and single norms are the first call's times that, bit for bit, so no partial result of an earlier call is read."""
+    import torch
+    require_gpu()
+    note("200 calls in a row")
+    rng = np.random.default_rng(34)
+    ts = [Tensor(rng, n, "fp32", i, shared=i == 1) for i, n in enumerate((3_000_001, 300, 40_000, 250_000))]
+    entries = zs.zs3_grad_tensor_list([t.entry() for t in ts])
+    n = Norm([t.entry() for t in ts], max_norm=math.inf)
+    got = []
+    for k in range(200):
+        zs.zs3_grad_norm_tensors(entries, n.args)
+        got.append([x.clone() for x in (n.norm, n.sums, n.each)])
+        for t in ts:
+            t.g.view.mul_(2.0 if k % 20 < 10 else 0.5)
+    torch.cuda.synchronize()
+    for k, (norm, sums, each) in enumerate(got):
+        f = 2.0 ** (k % 20 if k % 20 <= 10 else 20 - k % 20)
+        assert torch.equal(norm, got[0][0] * f) and torch.equal(each, got[0][2] * f), k
+        assert torch.equal(sums, got[0][1] * f * f), k
+
+
 def test_captured_and_replayed():
     """Accumulation with the norm, the clip and the per-tensor norms in one graph, replayed on new values between eager calls."""
     import torch

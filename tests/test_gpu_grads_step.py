@@ -154,6 +154,38 @@ def test_accumulated_steps_against_the_oracle(dtype, world, rank, path, fuse, K)
         step.destroy()
 
 
+def test_accumulation_over_the_4_bit_wire():
+    """Every micro-batch's average crosses the 4-bit wire with words of its own, and its flat gradient is what is accumulated."""
+    note("4-bit gradients, three micro-batches")
+    rng = np.random.default_rng(6)
+    step = _make(4, 2, "bf16", reduce_path="coalesced", reduce_bits=4, gather_bits=4, state_bits=8, fuse_norm=True, accumulate=3, seed=2)
+    try:
+        _start(step, rng)
+        for p in step.params:
+            x = oracle.from_f32((rng.standard_normal(p["numel"]) * 1e-1).astype(np.float32), "bf16").view(np.int16)
+            t = step.torch.from_numpy(x).cuda()
+            if p["persistent"]:
+                for v in range(4):
+                    i = step.recv_index(v, p["ds_id"])
+                    step.recv[i:i + p["numel"]] = t
+            else:
+                step.own_grads[step.grad_off[p["ds_id"]]:step.grad_off[p["ds_id"]] + p["numel"]] = t
+        want, flats = np.zeros(step.S, np.float32), []
+        for k in range(3):
+            (step.step if k == 2 else step.micro_step)()
+            sync()
+            flats.append(_h16(step.grad))
+            for p in step.params:
+                lo, hi = p["shard_offset"], p["shard_offset"] + p["own"][1] - p["own"][0]
+                want[lo:hi] = og.accumulate(want[lo:hi], oracle.to_f32(flats[k][lo:hi], "bf16"), 1 / 3, k == 0)
+                assert np.array_equal(step.acc[lo:hi].cpu().numpy(), want[lo:hi])
+        # the same gradients, rounded by other words: the own chunk's part of the averages differs
+        assert not np.array_equal(flats[0], flats[1]) and not np.array_equal(flats[1], flats[2])
+        assert int(step.outs.view(step.torch.int32)[3]) == 0 and float(step.outs[0]) > 0
+    finally:
+        step.destroy()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_one_micro_batch_accumulated_is_the_sum_of_its_halves(bits):
     """Two equal micro-batches accumulate to their gradient itself (halving is exact): the norm is

@@ -1,8 +1,8 @@
 """Python binding of libzs3, the ZeRO-3 shard-step library for MI355X.
 
 Argument marshalling only: every function below has the name of a C entry
-point in ``include/zs3.h``, ``include/zs3_lowbit.h`` or ``include/zs3_grads.h`` and forwards to it
-through ctypes.  Device
+point in ``include/zs3.h``, ``include/zs3_lowbit.h`` or ``include/zs3_grads.h``
+and forwards to it through ctypes.  Device
 buffers may be given as torch tensors (their data pointers are passed) or as
 raw integer device addresses; ``stream`` may be a ``torch.cuda.Stream``, a
 raw ``hipStream_t`` integer, or ``None`` for torch's current stream.  A
@@ -597,7 +597,7 @@ def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, d
 def zs3_grad_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
     """The list that the norm, the clip and the accumulation take: one dict a
     tensor with numel, grad, dtype and, where they differ from these, out=None,
-    out_dtype=None (dtype, or "fp32" for an accumulator), shared=False.  It holds
+    out_dtype=dtype ("fp32" where out is an accumulator), shared=False.  It holds
     addresses only: a caller keeps it for as long as its buffers stay where they are."""
     out = (zs3_grad_tensor * max(1, len(tensors)))()
     for o, t in zip(out, tensors):
@@ -625,7 +625,9 @@ def zs3_norm_args_of(*, sums, workspace=None, workspace_bytes: Optional[int] = N
                      world: int = 1, finalize: bool = True, max_norm: float = 1.0, loss_scale: float = 1.0, norm=None,
                      scale=None, nonfinite=None, tensor_norms=None) -> zs3_norm_args:
     """What a norm is told and where it goes.  Addresses only, as
-    ``zs3_grad_tensor_list``; a tensor given as the workspace brings its bytes."""
+    ``zs3_grad_tensor_list``; a tensor given as the workspace brings its bytes (it
+    is zeros before its first use: ``torch.zeros(zs3_norm_workspace_bytes(tensors),
+    dtype=torch.uint8, device="cuda")``)."""
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "data_ptr") else 0
     return zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale), _ptr(sums),

@@ -20,7 +20,8 @@ namespace zs3 {
 // A launch: its tensors as its kernel takes them.
 struct Launch {
     bool written;
-    int32_t kind, n, per;
+    int32_t kind, n, more;  // more: tiles behind a tensor's last that hold nothing
+    Runs runs;
     std::vector<int32_t> first_tile;
     std::vector<uint32_t> meta;
     std::vector<const void*> grad;
@@ -32,7 +33,8 @@ struct Launch {
 };
 std::vector<Launch> launches;
 struct TensorNorms {
-    int32_t kind, n, per, skew;
+    int32_t kind, n, skew;
+    Runs runs;
     std::vector<int32_t> first_tile;
     const double* parts;
     double* out;
@@ -52,8 +54,8 @@ struct End {
 std::vector<End> ends;
 
 template <class PLAN>
-Launch copy(const PLAN& p, bool written, int32_t kind, int32_t per, double* entries, double* tensors) {
-    Launch l{written, kind, p.n, per, {}, {}, {}, {}, entries, tensors, nullptr, nullptr};
+Launch copy(const PLAN& p, bool written, int32_t kind, int32_t more, const Runs& runs, double* entries, double* tensors) {
+    Launch l{written, kind, p.n, more, runs, {}, {}, {}, {}, entries, tensors, nullptr, nullptr};
     l.first_tile.assign(p.first_tile, p.first_tile + p.n + 1);
     l.meta.assign(p.meta, p.meta + p.n);
     l.grad.assign(p.grad, p.grad + p.n);
@@ -62,33 +64,33 @@ Launch copy(const PLAN& p, bool written, int32_t kind, int32_t per, double* entr
     return l;
 }
 hipError_t launch_norm(int32_t kind, const NormPlan& p, const NormParts& parts, const NormEnd& end, hipStream_t) {
-    launches.push_back(copy(p, false, kind, p.per, parts.entries, parts.tensors));
+    launches.push_back(copy(p, false, kind, 1, p.runs, parts.entries, parts.tensors));
     launches.back().counters = parts.counters;
     launches.back().tensor_norms = parts.tensor_norms;
     if (parts.counters != nullptr)      // its last workgroup ends the norm
-        ends.push_back({parts.all, parts.entries - parts.all + 2 * ((int64_t(p.first_tile[p.n]) + p.per - 1) / p.per), end});
+        ends.push_back({parts.all, parts.entries - parts.all + 2 * (int64_t(p.runs.of_tile(p.first_tile[p.n] - 1)) + 1), end});
     return hipSuccess;
 }
 bool few = false;
 hipError_t launch_norm_few(const NormPlan& p, const NormEnd& end, double* each, hipStream_t) {
     few = true;
-    launches.push_back(copy(p, false, end.kind, 1, nullptr, nullptr));
+    launches.push_back(copy(p, false, end.kind, 0, p.runs, nullptr, nullptr));
     launches.back().tensor_norms = each;
     return hipSuccess;
 }
 hipError_t launch_clip(const WritePlan& p, const float*, const int32_t*, hipStream_t) {
-    launches.push_back(copy(p, true, 0, 1, nullptr, nullptr));
+    launches.push_back(copy(p, true, 0, 0, Runs{1, 0}, nullptr, nullptr));
     launches.back().out.assign(p.out, p.out + p.n);
     return hipSuccess;
 }
 hipError_t launch_accumulate(int32_t kind, const WritePlan& p, float, bool, double* entries, hipStream_t) {
-    launches.push_back(copy(p, true, kind, 1, entries, nullptr));
+    launches.push_back(copy(p, true, kind, 0, Runs{1, 0}, entries, nullptr));
     launches.back().out.assign(p.out, p.out + p.n);
     return hipSuccess;
 }
-hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, int32_t skew, const double* parts,
-                               double* out, hipStream_t) {
-    tensor_norms.push_back({kind, n, per, skew, {first_tile, first_tile + n + 1}, parts, out});
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, const Runs& runs, int32_t skew,
+                               const double* parts, double* out, hipStream_t) {
+    tensor_norms.push_back({kind, n, skew, runs, {first_tile, first_tile + n + 1}, parts, out});
     return hipSuccess;
 }
 hipError_t launch_join(int32_t, const double* entries, int64_t n, int64_t per, double* to, hipStream_t) {
@@ -148,11 +150,18 @@ std::vector<zs3_grad_tensor> list(Rng& r, int32_t n, int64_t most, bool acc) {
 void hold(const std::vector<zs3_grad_tensor>& want, bool written) {
     size_t i = 0;
     for (const Launch& L : launches) {
-        EXPECT(L.written == written && L.per >= 1 && L.n >= 1);
+        EXPECT(L.written == written && L.runs.per >= 1 && L.n >= 1);
         EXPECT(L.first_tile[0] == 0);
-        const int64_t all = L.first_tile[L.n], groups = (all + L.per - 1) / L.per;
-        EXPECT(all > 0 && groups < (int64_t(1) << 24));
-        EXPECT(written ? L.per == 1 : groups <= kNormGroups);
+        const int32_t all = L.first_tile[L.n];
+        EXPECT(all > 0 && all < (1 << 24));
+        const int32_t groups = L.runs.of_tile(all - 1) + 1;
+        EXPECT(written ? L.runs.per == 1 && L.runs.rest == 0 : groups <= kNormGroups);
+        // runs follow each other, none is empty, and a tile's run holds it
+        EXPECT(L.runs.start(0) == 0 && L.runs.start(groups) == all);
+        for (int32_t b = 0; b < groups; b += 1 + groups / 3000) {
+            EXPECT(L.runs.start(b) < L.runs.start(b + 1));
+            EXPECT(L.runs.of_tile(L.runs.start(b)) == b && L.runs.of_tile(L.runs.start(b + 1) - 1) == b);
+        }
         for (int32_t s = 0; s < L.n; ++s, ++i) {
             if (i >= want.size()) {
                 EXPECT(false);
@@ -165,7 +174,8 @@ void hold(const std::vector<zs3_grad_tensor>& want, bool written) {
             const uint32_t m = L.meta[s];
             EXPECT((m >> 16 & 3) == static_cast<uint32_t>(t.dtype) && (m >> 20 & 1) == static_cast<uint32_t>(t.shared));
             EXPECT(!written || (m >> 18 & 3) == static_cast<uint32_t>(od));
-            const int64_t size = size_of(written ? od : t.dtype), T = gr_tile(size), tiles = L.first_tile[s + 1] - L.first_tile[s];
+            const int64_t size = size_of(written ? od : t.dtype), T = gr_tile(size);
+            const int64_t tiles = L.first_tile[s + 1] - L.first_tile[s] - (t.numel > 0 ? L.more : 0);
             const uintptr_t main = reinterpret_cast<uintptr_t>(written ? out : t.grad);
             const int64_t head = static_cast<int64_t>(main & (kGrLine - 1)) / size;
             int64_t next = 0;
@@ -211,7 +221,7 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
     for (const Launch& L : launches) {
         EXPECT(L.counters == nullptr || (L.counters == a.workspace && &L == &launches.back()));
         EXPECT(L.tensor_norms == nullptr || L.counters != nullptr);
-        const int64_t all = L.first_tile[L.n], groups = (all + L.per - 1) / L.per, entries = written ? all : 2 * groups;
+        const int64_t all = L.first_tile[L.n], groups = L.runs.of_tile(L.first_tile[L.n] - 1) + 1, entries = written ? all : 2 * groups;
         EXPECT(L.kind == a.kind && L.entries == lo + used);
         put(L.entries, entries);
         used += entries;
@@ -219,7 +229,7 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
         if (L.tensors == nullptr) continue;
         for (int32_t s = 0; s < L.n; ++s) {
             const int32_t f0 = L.first_tile[s], f1 = L.first_tile[s + 1];
-            if (f1 > f0) put(L.tensors + f0 / L.per + s, (f1 - 1) / L.per - f0 / L.per + 1);
+            if (f1 > f0) put(L.tensors + L.runs.of_tile(f0) + s, L.runs.of_tile(f1 - 1) - L.runs.of_tile(f0) + 1);
         }
     }
     if (joins.empty()) {
@@ -239,10 +249,10 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
     for (const Launch& L : launches) {      // those that a launch's last workgroup does
         if (L.tensor_norms == nullptr) continue;
         EXPECT(L.tensor_norms + L.n == a.tensor_norms + want.size());
-        tensor_norms.push_back({L.kind, L.n, L.per, 1, L.first_tile, L.tensors, L.tensor_norms});
+        tensor_norms.push_back({L.kind, L.n, 1, L.runs, L.first_tile, L.tensors, L.tensor_norms});
         for (int32_t s = 0; s < L.n; ++s)
             EXPECT(L.first_tile[s + 1] == L.first_tile[s] ||
-                   (L.first_tile[s + 1] - 1) / L.per - L.first_tile[s] / L.per < kFewParts);
+                   L.runs.of_tile(L.first_tile[s + 1] - 1) - L.runs.of_tile(L.first_tile[s]) < kFewParts);
     }
     for (const TensorNorms& t : tensor_norms) {
         EXPECT(t.out == a.tensor_norms + done && t.skew == (written ? 0 : 1));
@@ -250,7 +260,7 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
         if (t.first_tile[t.n] == 0) continue;
         EXPECT(seen < launches.size());
         const Launch& L = launches[seen++];
-        EXPECT(t.parts == (written ? L.entries : L.tensors) && t.n == L.n && t.per == L.per && t.first_tile == L.first_tile);
+        EXPECT(t.parts == (written ? L.entries : L.tensors) && t.n == L.n && t.runs.per == L.runs.per && t.runs.rest == L.runs.rest && t.first_tile == L.first_tile);
     }
     EXPECT(done == want.size() && seen == launches.size());
 }

@@ -390,10 +390,11 @@ __device__ __forceinline__ void join_entries(const double* entries, int64_t i0, 
     group_join2<KIND, BLOCK>(own, shared, sh);
 }
 
+// Tile t of the launch, one of tensor s's n.
 template <int KIND, class PLAN>
-__device__ __forceinline__ void norm_tile(const PLAN& plan, int s, int32_t t, Part<KIND>& part) {
+__device__ __forceinline__ void norm_tile(const PLAN& plan, int s, int32_t t, int32_t n, Part<KIND>& part) {
     const uint32_t meta = plan.meta[s], last = meta & 0xffffu;
-    const int32_t f0 = plan.first_tile[s], n = plan.first_tile[s + 1] - f0;
+    const int32_t f0 = plan.first_tile[s];
     const int g = meta >> 16 & 3;
     const void* grad = plan.grad[s];
     if (g == kFP16) typed_tile<kNorm, KIND, kFP16, kFP16>(grad, nullptr, t - f0, n, last, 1.0f, part);
@@ -405,8 +406,7 @@ template <int KIND>
 __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) void k_norm(const NormPlan plan, const NormParts parts, const NormEnd e) {
     __shared__ double sh[2 * (kGrBlock / 64)];
     __shared__ uint32_t last;
-    const int32_t b = static_cast<int32_t>(blockIdx.x), all = plan.first_tile[plan.n];
-    const int32_t t0 = b * plan.per, t1 = t0 + plan.per < all ? t0 + plan.per : all;
+    const int32_t b = static_cast<int32_t>(blockIdx.x), t0 = plan.runs.start(b), t1 = plan.runs.start(b + 1);
     int s = find_tensor(plan, t0, threadIdx.x & 63);
     double own = 0.0, shared = 0.0;
     Part<KIND> part;
@@ -426,7 +426,8 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
             do ++s;
             while (t >= plan.first_tile[s + 1]);
         }
-        norm_tile<KIND>(plan, s, t, part);
+        const int32_t past = plan.first_tile[s + 1] - 1;        // the tile that holds nothing
+        if (t < past) norm_tile<KIND>(plan, s, t, past - plan.first_tile[s], part);
     }
     close();
     group_join2<KIND, kGrBlock>(own, shared, sh);
@@ -450,9 +451,9 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
             const int32_t f0 = plan.first_tile[i], f1 = plan.first_tile[i + 1];
             double x = 0.0;
             if (f1 > f0) {
-                const int32_t end = (f1 - 1) / plan.per;
+                const int32_t end = plan.runs.of_tile(f1 - 1);
                 constexpr int kBatch = 8;
-                for (int32_t k = f0 / plan.per; k <= end; k += kBatch) {
+                for (int32_t k = plan.runs.of_tile(f0); k <= end; k += kBatch) {
                     double y[kBatch];
 #pragma unroll
                     for (int j = 0; j < kBatch; ++j) y[j] = k + j <= end ? get<true>(parts.tensors + k + j + i) : 0.0;
@@ -475,7 +476,10 @@ __global__ __launch_bounds__(kGrBlock* kFewTiles) void k_norm_few(const NormPlan
     const int32_t t = wave / kWaves;
     const double peers = peers_of<KIND>(e);
     Part<KIND> part;
-    if (t < plan.first_tile[plan.n]) norm_tile<KIND>(plan, find_tensor(plan, t, lane), t, part);
+    if (t < plan.first_tile[plan.n]) {
+        const int s = find_tensor(plan, t, lane);
+        norm_tile<KIND>(plan, s, t, plan.first_tile[s + 1] - plan.first_tile[s], part);
+    }
     const double x = wave_join<KIND>(part.value());
     if (lane == 0) sh[wave] = x;
     __syncthreads();
@@ -548,11 +552,12 @@ __global__ __launch_bounds__(kGrBlock) void k_accumulate(const WritePlanOf<N> pl
 // ------------------------------------------------------------ ends
 
 struct TensorTiles {
-    int32_t n, per, skew;
+    int32_t skew;
+    Runs runs;
     int32_t first_tile[kNormTensors + 1];
 };
 
-// A workgroup a tensor: its entries are [f0 / per, (f1 - 1) / per], moved by skew * s.
+// A workgroup a tensor.
 __global__ __launch_bounds__(kGrBlock) void k_tensor_norms(const TensorTiles p, int32_t kind, const double* __restrict__ parts,
                                                            double* __restrict__ tensor_norms) {
     __shared__ double sh[kGrBlock / 64];
@@ -561,9 +566,9 @@ __global__ __launch_bounds__(kGrBlock) void k_tensor_norms(const TensorTiles p, 
     double x = 0.0;
     if (f1 > f0) {
         const double* at = parts + int64_t(p.skew) * s;
-        const int32_t end = (f1 - 1) / p.per + 1;
+        const int32_t end = p.runs.of_tile(f1 - 1);
 #pragma unroll 4
-        for (int32_t i = f0 / p.per + static_cast<int32_t>(threadIdx.x); i < end; i += kGrBlock)
+        for (int32_t i = p.runs.of_tile(f0) + static_cast<int32_t>(threadIdx.x); i <= end; i += kGrBlock)
             x = join(kind, x, __builtin_fabs(at[i]));
     }
     x = kind == kMax ? group_join<kMax, kGrBlock>(x, sh) : group_join<kSum, kGrBlock>(x, sh);
@@ -617,7 +622,7 @@ static hipError_t launch(void (*kernel)(A...), int64_t groups, int threads, unsi
 }
 
 hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
-    const int64_t groups = (int64_t(plan.first_tile[plan.n]) + plan.per - 1) / plan.per;
+    const int32_t groups = plan.runs.of_tile(plan.first_tile[plan.n] - 1) + 1;
     return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, 0, stream, plan, parts, end);
 }
 
@@ -626,7 +631,7 @@ hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& part
 static NormPlanOf<kFewTensors> few(const NormPlan& plan) {
     NormPlanOf<kFewTensors> p;
     p.n = plan.n;
-    p.per = plan.per;
+    p.runs = plan.runs;
     std::copy_n(plan.first_tile, kFewTensors + 1, p.first_tile);
     std::copy_n(plan.meta, plan.n, p.meta);
     std::copy_n(plan.grad, plan.n, p.grad);
@@ -677,12 +682,11 @@ hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, 
                  : accumulate_launch<kAdd>(kind, plan, factor, entries, stream);
 }
 
-hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, int32_t per, int32_t skew, const double* parts,
-                               double* tensor_norms, hipStream_t stream) {
+hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, const Runs& runs, int32_t skew,
+                               const double* parts, double* tensor_norms, hipStream_t stream) {
     TensorTiles p;
-    p.n = n;
-    p.per = per;
     p.skew = skew;
+    p.runs = runs;
     for (int32_t i = 0; i <= n; ++i) p.first_tile[i] = first_tile[i];
     return launch(k_tensor_norms, n, kGrBlock, 0, stream, p, kind, parts, tensor_norms);
 }

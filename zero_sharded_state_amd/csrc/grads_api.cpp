@@ -60,7 +60,7 @@ int64_t size_of(int32_t d) { return d == ZS3_FP32 ? 4 : 2; }
 // Tiles of one launch: a grid of 256 threads each has to fit 32 bits.
 constexpr int64_t kMaxTiles = (int64_t(1) << 24) - 1;
 constexpr int64_t kMaxNumel = int64_t(1) << 34;
-static_assert(kMaxNumel / gr_tile(4) + 2 <= kMaxTiles, "the largest tensor fits a launch");
+static_assert(kMaxNumel / gr_tile(4) + 3 <= kMaxTiles, "the largest tensor fits a launch");
 
 // The byte ranges of a call: no written one may overlap another.  Lists are mostly
 // in the order of their addresses: what is sorted already is not sorted again.
@@ -161,7 +161,7 @@ zs3_status check_grad(int32_t i, const zs3_grad_tensor& t) {
 // ------------------------------------------------------------- the norm
 
 // What a list takes at most, whichever call takes it: launches, and tiles of all of them (an
-// address adds up to one a tensor).
+// address adds up to one a tensor, the norm counts another).
 struct Extent {
     int64_t launches = 1, tiles = 0;
 };
@@ -171,7 +171,7 @@ Extent extent_of(int32_t n, const zs3_grad_tensor* tensors) {
     int64_t here = 0;
     int32_t held = 0;
     for (int32_t i = 0; i < n; ++i) {
-        const int64_t t = tensors[i].numel == 0 ? 0 : tensors[i].numel / gr_tile(4) + 2;
+        const int64_t t = tensors[i].numel == 0 ? 0 : tensors[i].numel / gr_tile(4) + 3;
         if (held == std::min(kNormTensors, kWriteTensors) || here + t > kMaxTiles) {
             ++e.launches;
             here = held = 0;
@@ -249,10 +249,10 @@ void set_out(NormPlan&, int32_t, void*) {}
 void set_out(WritePlan& p, int32_t i, void* out) { p.out[i] = out; }
 
 // Cuts a list into launches.  `written`: tiles are those of out (grad where NULL),
-// otherwise grad's.  `emit(plan, first tensor, whether it is the last)` launches one plan; a
+// otherwise grad's; a tensor that is not empty gets `more` of them.  `emit(plan, first tensor, whether it is the last)` launches one plan; a
 // plan may hold empty tensors alone.
 template <class PLAN, class EMIT>
-zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, EMIT emit) {
+zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, int32_t more, EMIT emit) {
     constexpr int32_t kMost = sizeof(PLAN::meta) / sizeof(uint32_t);
     PLAN plan;
     plan.n = 0;
@@ -276,6 +276,7 @@ zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, 
             const int64_t head = static_cast<int64_t>(reinterpret_cast<uintptr_t>(written ? out : t.grad) % kGrLine) / size;
             tiles = (head + t.numel + tile - 1) / tile;
             last = head + t.numel - (tiles - 1) * tile;
+            tiles += more;
         }
         if (plan.n == kMost || plan.first_tile[plan.n] + tiles > kMaxTiles) {
             const zs3_status s = flush(i);
@@ -336,31 +337,36 @@ zs3_status zs3_grad_norm_tensors(int32_t n, const zs3_grad_tensor* tensors, cons
         double* entries = static_cast<double*>(a.workspace) + w.entries;
         double* parts = static_cast<double*>(a.workspace) + w.tensors;
         uint32_t* counters = static_cast<uint32_t*>(a.workspace);
+        const NormEnd end = end_of(a, a.finalize != 0);
+        constexpr const char* kWhat = "norm kernel launch";
         int64_t used = 0;
         bool ended = false;
-        s = each_launch<NormPlan>(n, tensors, false, [&](NormPlan& plan, int32_t first, bool last) -> zs3_status {
-            const int64_t tiles = plan.first_tile[plan.n];
-            double* each = a.tensor_norms != nullptr ? a.tensor_norms + first : nullptr;
-            if (plan.n == n && n <= kFewTensors && tiles <= kFewTiles) {
+        if (n <= kFewTensors) {
+            s = each_launch<NormPlan>(n, tensors, false, 0, [&](NormPlan& plan, int32_t, bool) -> zs3_status {
+                if (plan.n != n || plan.first_tile[n] > kFewTiles) return ZS3_OK;
                 ended = true;
-                return launched(launch_norm_few(plan, end_of(a, a.finalize != 0), each, st), "norm kernel launch");
-            }
-            plan.per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + kNormGroups - 1) / kNormGroups));
-            const int64_t here = 2 * ((tiles + plan.per - 1) / plan.per);
-            const bool ends = last && tiles > 0 && used + here <= kLastEntries;
+                plan.runs = Runs{1, 0};
+                return launched(launch_norm_few(plan, end, a.tensor_norms, st), kWhat);
+            });
+            if (s != ZS3_OK || ended) return s != ZS3_OK ? s : ok();
+        }
+        s = each_launch<NormPlan>(n, tensors, false, 1, [&](NormPlan& plan, int32_t first, bool last) -> zs3_status {
+            const int32_t tiles = plan.first_tile[plan.n], groups = std::min<int32_t>(kNormGroups, tiles);
+            plan.runs = groups > 0 ? Runs{tiles / groups, tiles % groups} : Runs{1, 0};
+            const bool ends = last && tiles > 0 && used + 2 * groups <= kLastEntries;
             bool few = ends;                    // its last workgroup joins the tensors' parts, too
             for (int32_t i = 0; i < plan.n && few; ++i)
-                few = plan.first_tile[i + 1] - plan.first_tile[i] <= int64_t(kFewParts - 1) * plan.per;
+                few = plan.first_tile[i + 1] - plan.first_tile[i] <= int64_t(kFewParts - 1) * plan.runs.per;
+            double* each = a.tensor_norms != nullptr ? a.tensor_norms + first : nullptr;
             if (tiles > 0) {
                 const NormParts to{entries, entries + used, each != nullptr ? parts : nullptr, ends ? counters : nullptr, few ? each : nullptr};
-                const zs3_status e = launched(launch_norm(a.kind, plan, to, end_of(a, a.finalize != 0), st), "norm kernel launch");
+                const zs3_status e = launched(launch_norm(a.kind, plan, to, end, st), kWhat);
                 if (e != ZS3_OK) return e;
-                used += here;
+                used += 2 * groups;
                 ended = ends;
             }
             if (each == nullptr || few) return ZS3_OK;
-            const zs3_status e = launched(launch_tensor_norms(a.kind, plan.first_tile, plan.n, plan.per, 1, parts, each, st),
-                                          "norm kernel launch");
+            const zs3_status e = launched(launch_tensor_norms(a.kind, plan.first_tile, plan.n, plan.runs, 1, parts, each, st), kWhat);
             parts += kNormGroups + kNormTensors;
             return e;
         });
@@ -407,7 +413,7 @@ zs3_status zs3_clip_tensors(int32_t n, const zs3_grad_tensor* tensors, const flo
             ranges.written(t.out, size_of(t.out_dtype) * t.numel, i);
         }
         if ((s = check_overlaps(ranges)) != ZS3_OK) return s;
-        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t, bool) -> zs3_status {
+        s = each_launch<WritePlan>(n, tensors, true, 0, [&](const WritePlan& plan, int32_t, bool) -> zs3_status {
             if (plan.first_tile[plan.n] == 0) return ZS3_OK;
             return launched(launch_clip(plan, scale, nonfinite, static_cast<hipStream_t>(stream)), "clip kernel launch");
         });
@@ -437,7 +443,7 @@ zs3_status zs3_accumulate_tensors(int32_t n, const zs3_grad_tensor* tensors, dou
         const hipStream_t st = static_cast<hipStream_t>(stream);
         double* entries = norm != nullptr ? static_cast<double*>(norm->workspace) + Workspace::entries : nullptr;
         int64_t used = 0;
-        s = each_launch<WritePlan>(n, tensors, true, [&](const WritePlan& plan, int32_t at, bool) -> zs3_status {
+        s = each_launch<WritePlan>(n, tensors, true, 0, [&](const WritePlan& plan, int32_t at, bool) -> zs3_status {
             const int64_t tiles = plan.first_tile[plan.n];
             double* to = entries != nullptr ? entries + used : nullptr;
             used += tiles;
@@ -447,7 +453,7 @@ zs3_status zs3_accumulate_tensors(int32_t n, const zs3_grad_tensor* tensors, dou
                 if (e != ZS3_OK) return e;
             }
             if (norm == nullptr || norm->tensor_norms == nullptr) return ZS3_OK;
-            return launched(launch_tensor_norms(norm->kind, plan.first_tile, plan.n, 1, 0, to, norm->tensor_norms + at, st),
+            return launched(launch_tensor_norms(norm->kind, plan.first_tile, plan.n, Runs{1, 0}, 0, to, norm->tensor_norms + at, st),
                             "norm kernel launch");
         });
         if (s != ZS3_OK || norm == nullptr) return s != ZS3_OK ? s : ok();

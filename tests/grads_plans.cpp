@@ -44,6 +44,7 @@ struct Join {
     const double* entries;
     int64_t n, per;
     double* to;
+    uint32_t* counters;
 };
 std::vector<Join> joins;
 struct End {
@@ -93,8 +94,10 @@ hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t 
     tensor_norms.push_back({kind, n, skew, runs, {first_tile, first_tile + n + 1}, parts, out});
     return hipSuccess;
 }
-hipError_t launch_join(int32_t, const double* entries, int64_t n, int64_t per, double* to, hipStream_t) {
-    joins.push_back({entries, n, per, to});
+hipError_t launch_join(const double* entries, int64_t n, int64_t per, double* to, uint32_t* counters, const NormEnd& end,
+                       hipStream_t) {
+    joins.push_back({entries, n, per, to, counters});
+    ends.push_back({entries, n, end});
     return hipSuccess;
 }
 hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end, hipStream_t) {
@@ -232,13 +235,13 @@ void hold_norm(const std::vector<zs3_grad_tensor>& want, const zs3_norm_args& a,
             if (f1 > f0) put(L.tensors + L.runs.of_tile(f0) + s, L.runs.of_tile(f1 - 1) - L.runs.of_tile(f0) + 1);
         }
     }
+    EXPECT(ends[0].entries == lo && ends[0].n == used);
     if (joins.empty()) {
-        EXPECT((!written || used <= kEndEntries) && ends[0].entries == lo && ends[0].n == used);
+        EXPECT(used <= kEndEntries);
     } else {
         const Join& j = joins[0];
         const int64_t groups = (used + j.per - 1) / j.per;
-        EXPECT(used > kEndEntries && j.entries == lo && j.n == used && groups <= kJoinGroups);
-        EXPECT(ends[0].entries == j.to && ends[0].n == 2 * groups && 2 * groups <= kEndEntries);
+        EXPECT(used > kEndEntries && j.counters == a.workspace && groups > 1 && groups <= kJoinGroups);
         put(j.to, 2 * groups);
     }
     if (a.tensor_norms == nullptr) {

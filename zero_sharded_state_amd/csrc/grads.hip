@@ -197,6 +197,16 @@ __device__ __forceinline__ void end_of_norm(const NormEnd& e, double peers, doub
     *e.scale = bad ? __builtin_nanf("") : static_cast<float>(coef / e.loss_scale);
 }
 
+// The sums and the end of the norm, by the threads of one workgroup.
+template <int KIND>
+__device__ __forceinline__ void write_sums(const NormEnd& e, double peers, double own, double shared) {
+    if (threadIdx.x == 0) {
+        e.sums[e.rank] = own;
+        e.sums[e.world] = shared;
+    }
+    if (e.finalize && threadIdx.x < 64) end_of_norm<KIND>(e, peers, own, shared);
+}
+
 // ------------------------------------------------------------ tiles
 
 enum Op { kNorm = 1, kClip = 2, kSet = 3, kAdd = 4 };
@@ -441,11 +451,7 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
     if (last == 0) return;
     const double peers = peers_of<KIND>(e);
     join_entries<KIND, kGrBlock, true>(parts.all, 0, mine - parts.all + 2 * int64_t(static_cast<int32_t>(gridDim.x) - b), sh, own, shared);
-    if (threadIdx.x == 0) {
-        e.sums[e.rank] = own;
-        e.sums[e.world] = shared;
-    }
-    if (e.finalize && threadIdx.x < 64) end_of_norm<KIND>(e, peers, own, shared);
+    write_sums<KIND>(e, peers, own, shared);
     if (parts.tensor_norms != nullptr) {
         for (int i = static_cast<int>(threadIdx.x); i < plan.n; i += kGrBlock) {
             const int32_t f0 = plan.first_tile[i], f1 = plan.first_tile[i + 1];
@@ -492,11 +498,7 @@ __global__ __launch_bounds__(kGrBlock* kFewTiles) void k_norm_few(const NormPlan
     if (tensor_norms != nullptr && lane < plan.n) tensor_norms[lane] = root<KIND>(mine);
     const bool second = lane < plan.n && (plan.meta[s] >> 20 & 1) != 0;
     const double own = wave_join<KIND>(second ? 0.0 : mine), shared = wave_join<KIND>(second ? mine : 0.0);
-    if (lane == 0) {
-        e.sums[e.rank] = own;
-        e.sums[e.world] = shared;
-    }
-    if (e.finalize) end_of_norm<KIND>(e, peers, own, shared);
+    write_sums<KIND>(e, peers, own, shared);
 }
 
 // ------------------------------------------------------------ writing
@@ -575,18 +577,25 @@ __global__ __launch_bounds__(kGrBlock) void k_tensor_norms(const TensorTiles p, 
     if (threadIdx.x == 0) tensor_norms[s] = kind == kMax ? x : root<kSum>(x);
 }
 
-// Workgroup b joins `per` entries into two.
+// Workgroup b joins `per` entries into two, and the last one those.
 template <int KIND>
-__global__ __launch_bounds__(kGrBlock) void k_join(const double* __restrict__ entries, int64_t n, int64_t per,
-                                                   double* __restrict__ to) {
+__global__ __launch_bounds__(kGrBlock) void k_join(const double* __restrict__ entries, int64_t n, int64_t per, double* to,
+                                                   uint32_t* counters, const NormEnd e) {
     __shared__ double sh[2 * (kGrBlock / 64)];
+    __shared__ uint32_t last;
     const int64_t i0 = blockIdx.x * per, i1 = i0 + per < n ? i0 + per : n;
     double own, shared;
+    const double peers = peers_of<KIND>(e);
     join_entries<KIND, kGrBlock, false>(entries, i0, i1, sh, own, shared);
     if (threadIdx.x == 0) {
-        to[2 * blockIdx.x] = entry(own, false);
-        to[2 * blockIdx.x + 1] = entry(shared, true);
+        put(to + 2 * blockIdx.x, entry(own, false));
+        put(to + 2 * blockIdx.x + 1, entry(shared, true));
+        last = ends_last(counters, static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(gridDim.x)) ? 1u : 0u;
     }
+    __syncthreads();
+    if (last == 0) return;
+    join_entries<KIND, kGrBlock, true>(to, 0, 2 * int64_t(gridDim.x), sh, own, shared);
+    write_sums<KIND>(e, peers, own, shared);
 }
 
 constexpr int kEndBlock = 1024;
@@ -597,11 +606,7 @@ __global__ __launch_bounds__(kEndBlock) void k_norm_end(const double* __restrict
     double own, shared;
     const double peers = peers_of<KIND>(e);
     join_entries<KIND, kEndBlock, false>(entries, 0, n, sh, own, shared);
-    if (threadIdx.x == 0) {
-        e.sums[e.rank] = own;
-        e.sums[e.world] = shared;
-    }
-    if (e.finalize && threadIdx.x < 64) end_of_norm<KIND>(e, peers, own, shared);
+    write_sums<KIND>(e, peers, own, shared);
 }
 
 template <int KIND>
@@ -691,8 +696,10 @@ hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t 
     return launch(k_tensor_norms, n, kGrBlock, 0, stream, p, kind, parts, tensor_norms);
 }
 
-hipError_t launch_join(int32_t kind, const double* entries, int64_t n, int64_t per, double* to, hipStream_t stream) {
-    return launch(kind == kMax ? k_join<kMax> : k_join<kSum>, (n + per - 1) / per, kGrBlock, 0, stream, entries, n, per, to);
+hipError_t launch_join(const double* entries, int64_t n, int64_t per, double* to, uint32_t* counters, const NormEnd& end,
+                       hipStream_t stream) {
+    return launch(end.kind == kMax ? k_join<kMax> : k_join<kSum>, (n + per - 1) / per, kGrBlock, 0, stream, entries, n, per, to,
+                  counters, end);
 }
 
 hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end, hipStream_t stream) {

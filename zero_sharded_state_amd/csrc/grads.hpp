@@ -110,8 +110,9 @@ constexpr int kFewParts = 32;
 constexpr int64_t kLastEntries = 4 * kNormGroups;
 
 // Entries that one workgroup ends the norm from; more are joined by kJoinGroups at
-// most first.
+// most, kJoinEntries each at least, whose last one ends it.
 constexpr int64_t kEndEntries = 16384;
+constexpr int64_t kJoinEntries = 2048;
 constexpr int64_t kJoinGroups = 512;
 
 struct NormEnd {
@@ -135,9 +136,11 @@ hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, 
 // are in, moved by skew * s.
 hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, const Runs& runs, int32_t skew,
                                const double* parts, double* tensor_norms, hipStream_t stream);
-// to[2 * b], to[2 * b + 1]: entries [b * per, (b + 1) * per) joined.
-hipError_t launch_join(int32_t kind, const double* entries, int64_t n, int64_t per, double* to, hipStream_t stream);
-// n entries into the sums, and the end of the norm where asked.
+// n entries into the sums by workgroups of `per` (their results in `to`), and the end of the norm
+// where asked.
+hipError_t launch_join(const double* entries, int64_t n, int64_t per, double* to, uint32_t* counters, const NormEnd& end,
+                       hipStream_t stream);
+// The same by one workgroup.
 hipError_t launch_norm_end(const double* entries, int64_t n, const NormEnd& end, hipStream_t stream);
 // The end of the norm from the sums alone.
 hipError_t launch_norm_finalize(const NormEnd& end, hipStream_t stream);

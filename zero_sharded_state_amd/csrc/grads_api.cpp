@@ -293,16 +293,16 @@ zs3_status each_launch(int32_t n, const zs3_grad_tensor* tensors, bool written, 
 
 // The end of a norm from the first `used` entries.
 zs3_status end_norm(int64_t used, const Workspace& w, const zs3_norm_args& a, hipStream_t stream) {
-    const double* entries = static_cast<const double*>(a.workspace) + w.entries;
-    zs3_status s;
+    double* at = static_cast<double*>(a.workspace);
+    const NormEnd end = end_of(a, a.finalize != 0);
+    hipError_t e;
     if (used > kEndEntries) {
-        double* to = static_cast<double*>(a.workspace) + w.joined;
-        const int64_t per = (used + kJoinGroups - 1) / kJoinGroups;
-        if ((s = launched(launch_join(a.kind, entries, used, per, to, stream), "norm kernel launch")) != ZS3_OK) return s;
-        entries = to;
-        used = 2 * ((used + per - 1) / per);
+        const int64_t per = std::max(kJoinEntries, (used + kJoinGroups - 1) / kJoinGroups);
+        e = launch_join(at + w.entries, used, per, at + w.joined, static_cast<uint32_t*>(a.workspace), end, stream);
+    } else {
+        e = launch_norm_end(at + w.entries, used, end, stream);
     }
-    s = launched(launch_norm_end(entries, used, end_of(a, a.finalize != 0), stream), "norm kernel launch");
+    const zs3_status s = launched(e, "norm kernel launch");
     return s != ZS3_OK ? s : ok();
 }
 

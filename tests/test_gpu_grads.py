@@ -511,13 +511,14 @@ def test_every_call_sees_its_own_partial_results():
         assert torch.equal(sums, got[0][1] * f * f), k
 
 
-def test_captured_and_replayed():
+@pytest.mark.parametrize("sizes", [(200_001, 300, 4000), (700,) * 330, (9, 5)], ids=["few", "many", "tiny"])
+def test_captured_and_replayed(sizes):
     """Accumulation with the norm, the clip and the per-tensor norms in one graph, replayed on new values between eager calls."""
     import torch
     require_gpu()
-    note("graph")
+    note(f"graph of {len(sizes)} tensors")
     rng = np.random.default_rng(32)
-    ts = [Tensor(rng, n, "bf16", i, out="acc", shared=i == 2) for i, n in enumerate((200_001, 300, 4000))]
+    ts = [Tensor(rng, n, "bf16", i % 9, out="acc", shared=i == 2) for i, n in enumerate(sizes)]
     entries = [t.entry() for t in ts]
     outs = [Buf16(t.n, 1) for t in ts]
     held = zs.zs3_grad_tensor_list([dict(numel=t.n, grad=t.o.ptr(), dtype="fp32", out=o.ptr(), out_dtype="bf16") for t, o in zip(ts, outs)])

@@ -352,8 +352,8 @@ __device__ __forceinline__ bool ends_last(uint32_t* counters, int32_t b, int32_t
 // registers; 2048 workgroups, all that fit on the chip at once (half as many: 309 -> 392 us on the
 // share below; twice as many 316; a workgroup a tile 567).  Issuing the next tile's loads
 // before the last one's values are added changes nothing (308): eight workgroups a CU have
-// 64 KB in flight.  Measured: a share of 1.0B elements in two types 304 us (6.6 TB/s), 117M of
-// 221 odd tensors 43 us (5.4 TB/s), 27M 14 us, of which 5 are the start, the last
+// 64 KB in flight.  Measured: a share of 1.0B elements in two types 299 us (6.7 TB/s), 117M of
+// 221 odd tensors 41 us (5.7 TB/s), 27M 14 us, of which 5 are the start, the last
 // workgroup's turn and its joins.
 
 // Joins two values over the workgroup of BLOCK threads; every thread gets them.
@@ -412,8 +412,8 @@ __device__ __forceinline__ void norm_tile(const PLAN& plan, int s, int32_t t, in
     else typed_tile<kNorm, KIND, kFP32, kFP32>(grad, nullptr, t - f0, n, last, 1.0f, part);
 }
 
-template <int KIND>
-__global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) void k_norm(const NormPlan plan, const NormParts parts, const NormEnd e) {
+template <int KIND, int N>
+__global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) void k_norm(const NormPlanOf<N> plan, const NormParts parts, const NormEnd e) {
     __shared__ double sh[2 * (kGrBlock / 64)];
     __shared__ uint32_t last;
     const int32_t b = static_cast<int32_t>(blockIdx.x), t0 = plan.runs.start(b), t1 = plan.runs.start(b + 1);
@@ -506,8 +506,8 @@ __global__ __launch_bounds__(kGrBlock* kFewTiles) void k_norm_few(const NormPlan
 // workgroups that follow the arrays' order stream fastest (runs of tiles as in the norm: 1595 ->
 // 1955 us for the accumulation of a 1.0B share; tiles of 4 or 16 KB 1780 and 1680; plain
 // instead of non-temporal loads 1820, stores 1906).  Measured: 117M elements of 221
-// odd tensors clipped in place 77 us (6.0 TB/s), accumulated 182 us (6.4 TB/s), for the first
-// time 117 us (6.0 TB/s); a share of 1.0B 1560 us (6.4 TB/s), with the norm 1578.
+// odd tensors clipped in place 74 us (6.3 TB/s), accumulated 181 us (6.5 TB/s), for the first
+// time 115 us (6.1 TB/s); a share of 1.0B 1570 us (6.4 TB/s), with the norm 1590.
 
 template <int OP, int KIND, int O, class PLAN>
 __device__ __forceinline__ void write_tile(const PLAN& plan, int s, int32_t t, float f, Part<KIND>& part) {
@@ -626,65 +626,80 @@ static hipError_t launch(void (*kernel)(A...), int64_t groups, int threads, unsi
     return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<uint32_t>(groups)), dim3(threads), list, lds, stream);
 }
 
-hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
-    const int32_t groups = plan.runs.of_tile(plan.first_tile[plan.n] - 1) + 1;
-    return launch(kind == kMax ? k_norm<kMax> : k_norm<kSum>, groups, kGrBlock, 0, stream, plan, parts, end);
-}
-
-// A plan of at most kFewTensors in a smaller one (the places past its end are copied, too: the
-// search counts on them).
-static NormPlanOf<kFewTensors> few(const NormPlan& plan) {
-    NormPlanOf<kFewTensors> p;
+// A plan in a smaller one (the places past its end are copied, too: the search counts on them).
+template <int N>
+static NormPlanOf<N> smaller(const NormPlan& plan) {
+    NormPlanOf<N> p;
     p.n = plan.n;
     p.runs = plan.runs;
-    std::copy_n(plan.first_tile, kFewTensors + 1, p.first_tile);
+    std::copy_n(plan.first_tile, N + 1, p.first_tile);
     std::copy_n(plan.meta, plan.n, p.meta);
     std::copy_n(plan.grad, plan.n, p.grad);
     return p;
 }
-static WritePlanOf<kFewTensors> few(const WritePlan& plan) {
-    WritePlanOf<kFewTensors> p;
+template <int N>
+static WritePlanOf<N> smaller(const WritePlan& plan) {
+    WritePlanOf<N> p;
     p.n = plan.n;
-    std::copy_n(plan.first_tile, kFewTensors + 1, p.first_tile);
+    std::copy_n(plan.first_tile, N + 1, p.first_tile);
     std::copy_n(plan.meta, plan.n, p.meta);
     std::copy_n(plan.grad, plan.n, p.grad);
     std::copy_n(plan.out, plan.n, p.out);
     return p;
 }
 
+template <int KIND>
+static hipError_t norm_launch(const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
+    const int32_t groups = plan.runs.of_tile(plan.first_tile[plan.n] - 1) + 1;
+    if (plan.n <= kNormMid) return launch(k_norm<KIND, kNormMid>, groups, kGrBlock, 0, stream, smaller<kNormMid>(plan), parts, end);
+    return launch(k_norm<KIND, kNormTensors>, groups, kGrBlock, 0, stream, plan, parts, end);
+}
+
+hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
+    return kind == kMax ? norm_launch<kMax>(plan, parts, end, stream) : norm_launch<kSum>(plan, parts, end, stream);
+}
+
 hipError_t launch_norm_few(const NormPlan& plan, const NormEnd& end, double* tensor_norms, hipStream_t stream) {
-    return launch(end.kind == kMax ? k_norm_few<kMax> : k_norm_few<kSum>, 1, kGrBlock * kFewTiles, 0, stream, few(plan), end,
-                  tensor_norms);
+    return launch(end.kind == kMax ? k_norm_few<kMax> : k_norm_few<kSum>, 1, kGrBlock * kFewTiles, 0, stream,
+                  smaller<kFewTensors>(plan), end, tensor_norms);
+}
+
+// go(the plan, in the smallest size that holds it).
+template <class F>
+static hipError_t by_size(const WritePlan& plan, F go) {
+    if (plan.n <= kFewTensors) return go(smaller<kFewTensors>(plan));
+    if (plan.n <= kWriteMid) return go(smaller<kWriteMid>(plan));
+    return go(plan);
+}
+
+template <int N>
+static hipError_t clip_launch(const WritePlanOf<N>& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream) {
+    return launch(k_clip<N>, plan.first_tile[plan.n], kGrBlock, 0, stream, plan, scale, nonfinite);
 }
 
 hipError_t launch_clip(const WritePlan& plan, const float* scale, const int32_t* nonfinite, hipStream_t stream) {
-    const int64_t tiles = plan.first_tile[plan.n];
-    if (plan.n <= kFewTensors) return launch(k_clip<kFewTensors>, tiles, kGrBlock, 0, stream, few(plan), scale, nonfinite);
-    return launch(k_clip<kWriteTensors>, tiles, kGrBlock, 0, stream, plan, scale, nonfinite);
+    return by_size(plan, [&](const auto& p) { return clip_launch(p, scale, nonfinite, stream); });
 }
 
 constexpr int64_t kManyTiles = 100000;      // 205M elements
 constexpr unsigned kManyLds = 32 * 1024;
 
-template <int OP>
-static hipError_t accumulate_launch(int32_t kind, const WritePlan& plan, float factor, double* entries, hipStream_t stream) {
+template <int OP, int N>
+static hipError_t accumulate_launch(int32_t kind, const WritePlanOf<N>& plan, float factor, double* entries, hipStream_t stream) {
     // LDS that is reserved and never used: five workgroups a CU instead of eight, as many
     // streams as HBM takes best where a launch reads and writes gigabytes (the 1.0B elements
     // of a share of 291 tensors 1655 -> 1560 us, with the sums 1625 -> 1573; equal on 400
     // of 1M; smaller launches lose: 27M elements 50 -> 54 us)
     const int64_t tiles = plan.first_tile[plan.n];
     const unsigned lds = OP == kAdd && tiles >= kManyTiles ? kManyLds : 0;
-    if (plan.n <= kFewTensors) {
-        auto kernel = kind == 0 ? k_accumulate<OP, 0, kFewTensors> : kind == kMax ? k_accumulate<OP, kMax, kFewTensors> : k_accumulate<OP, kSum, kFewTensors>;
-        return launch(kernel, tiles, kGrBlock, lds, stream, few(plan), factor, entries);
-    }
-    auto kernel = kind == 0 ? k_accumulate<OP, 0, kWriteTensors> : kind == kMax ? k_accumulate<OP, kMax, kWriteTensors> : k_accumulate<OP, kSum, kWriteTensors>;
+    auto kernel = kind == 0 ? k_accumulate<OP, 0, N> : kind == kMax ? k_accumulate<OP, kMax, N> : k_accumulate<OP, kSum, N>;
     return launch(kernel, tiles, kGrBlock, lds, stream, plan, factor, entries);
 }
 
 hipError_t launch_accumulate(int32_t kind, const WritePlan& plan, float factor, bool first, double* entries, hipStream_t stream) {
-    return first ? accumulate_launch<kSet>(kind, plan, factor, entries, stream)
-                 : accumulate_launch<kAdd>(kind, plan, factor, entries, stream);
+    return by_size(plan, [&](const auto& p) {
+        return first ? accumulate_launch<kSet>(kind, p, factor, entries, stream) : accumulate_launch<kAdd>(kind, p, factor, entries, stream);
+    });
 }
 
 hipError_t launch_tensor_norms(int32_t kind, const int32_t* first_tile, int32_t n, const Runs& runs, int32_t skew,

@@ -1,7 +1,7 @@
 // Internal declarations of the gradient-list operators: the global norm over a
 // list of tensors, clipping it, and accumulating it in fp32.  As with the low-bit
-// operators a call's description travels in the kernel arguments (under 4 KB, longer
-// lists split over launches): nothing is allocated, uploaded or kept.
+// operators a call's description travels in the kernel arguments (longer lists split
+// over launches): nothing is allocated, uploaded or kept.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -21,9 +21,13 @@ constexpr int64_t kGrLine = 128;           // bytes of a cache line: tiles start
 // head + i, head elements after the line that the array starts in.
 constexpr int64_t gr_tile(int64_t bytes_of_element) { return kGrTileBytes / bytes_of_element; }
 
-// Tensors of one launch: as many as 4 KB of kernel arguments hold.
-constexpr int kNormTensors = 224;
-constexpr int kWriteTensors = 152;
+// Tensors that a launch's plan has room for.  The host writes the arguments into device memory, so
+// their size is its time: 2.5 us a launch with few bytes, 3.3 with 4 KB, 6.1 with 8. A launch
+// more costs the GPU about 4.5 (its start and end): lists past the middle size take the large one
+// (221 tensors clipped in place 77.7 -> 74.4 us, 1500 of 33,555 65.5 -> 50.5).
+constexpr int kFewTensors = 16;
+constexpr int kNormMid = 224, kNormTensors = 480;
+constexpr int kWriteMid = 152, kWriteTensors = 320;
 
 // meta: positions of the last tile that are the tensor's (1 .. gr_tile), and types.
 constexpr uint32_t gr_meta(int64_t last, int32_t dtype, int32_t out_dtype, bool shared) {
@@ -53,7 +57,7 @@ struct NormPlanOf {
     const void* grad[N];
 };
 using NormPlan = NormPlanOf<kNormTensors>;
-static_assert(sizeof(NormPlan) <= 3840, "the plan has to fit the kernel arguments");
+static_assert(sizeof(NormPlanOf<kNormMid>) <= 3840 && sizeof(NormPlan) <= 7936, "what the sizes are chosen by");
 
 template <int N>
 struct WritePlanOf {
@@ -64,11 +68,7 @@ struct WritePlanOf {
     void* out[N];
 };
 using WritePlan = WritePlanOf<kWriteTensors>;
-static_assert(sizeof(WritePlan) <= 3840, "the plan has to fit the kernel arguments");
-
-// Tensors up to which a launch takes a plan of its own size: 4 KB of arguments cost the host 0.3 us
-// (the toy model's call 4.9 -> 4.6).
-constexpr int kFewTensors = 16;
+static_assert(sizeof(WritePlanOf<kWriteMid>) <= 3840 && sizeof(WritePlan) <= 7936, "what the sizes are chosen by");
 
 // Workgroups of a launch of the norm: each takes a run of tiles, so that there are
 // few partial results and the run's sum stays in registers.  (Runs that differ by one tile
@@ -100,8 +100,8 @@ constexpr int kCounters = 32;
 constexpr int64_t kCounterBytes = (1 + kCounters) * kGrLine;
 
 // Parts of one tensor up to which the norm's last workgroup joins them, a thread a tensor;
-// otherwise a launch of its own does, a workgroup a tensor (221 tensors of at most 28 parts 55 ->
-// 47 us, one of 2048 would take 200).
+// otherwise a launch of its own does, a workgroup a tensor (200 tensors of 10 parts: 36.0 us
+// without their norms, 37.7 with; the 57 parts of the largest of 221: 44.6 so, 43.7 by a launch).
 constexpr int kFewParts = 32;
 
 // Entries up to which the norm's last workgroup joins them: those of two launches

@@ -111,8 +111,8 @@ ZS3_API const char* zs3_last_error(void);
  * created by the caller, either may be NULL), as hipExtLaunchKernel does; no
  * extra commands are enqueued.  The setting applies to exactly one launch
  * (calls that launch two kernels time the first).  The calls of
- * zs3_lowbit.h do not take part: they leave the setting for the next other
- * launch.  Always returns ZS3_OK. */
+ * zs3_lowbit.h and zs3_grads.h do not take part: they leave the setting for
+ * the next other launch.  Always returns ZS3_OK. */
 ZS3_API zs3_status zs3_time_next_launch(void* start_event, void* stop_event);
 
 /* ------------------------------------------------------------- layout

@@ -246,6 +246,35 @@ def test_norm_finalize_alone_and_measured_only(kind):
     assert torch.cuda.current_stream() is not None
 
 
+@pytest.mark.parametrize("kind", ["2", "inf"])
+@pytest.mark.parametrize("world", [64, 65, 300])
+def test_norm_of_many_ranks(kind, world):
+    """More peers than a wave has lanes; one whose sum is not finite."""
+    require_gpu()
+    note(f"{world} ranks, {kind}")
+    rng = np.random.default_rng(world)
+    for sizes in ((500, 40), (30_000, 7, 9000)):
+        ts = [Tensor(rng, n, "fp32", i, shared=i == 1) for i, n in enumerate(sizes)]
+        peers = list(rng.random(world + 1) * 1e-3)
+        for rank in (0, world - 1, 17):
+            _norm(ts, kind=kind, rank=rank, world=world, peers=peers)
+        assert _norm(ts, kind=kind, rank=1, world=world, peers=[math.inf if v == 20 else p for v, p in enumerate(peers)]).got()["flag"] == 1
+        assert _norm(ts, kind=kind, rank=1, world=world, peers=[math.nan if v == 33 else p for v, p in enumerate(peers)]).got()["flag"] == 1
+
+
+def test_norm_counts_a_tensor_twice_where_the_list_does():
+    require_gpu()
+    note("a tensor twice, and parts of one")
+    rng = np.random.default_rng(9)
+    for n in (700, 50_000):
+        t = Tensor(rng, n, "bf16", 3)
+        parts = [t.entry(), t.entry(), dict(numel=n // 2, grad=t.g.ptr(), dtype="bf16", shared=True)]
+        nm = Norm(parts)
+        zs.zs3_grad_norm_tensors(parts, nm.args)
+        sync()
+        nm.check([(t.x, False), (t.x, False), (t.x[:n // 2], True)])
+
+
 def test_norm_agrees_with_the_flat_norm():
     """One flat gradient of a layout, by the layout's call and as a list."""
     import torch
@@ -556,14 +585,19 @@ def test_two_streams_at_once():
     rng = np.random.default_rng(33)
     sets = [[Tensor(rng, n, d, out="acc") for n in (900_000, 33, 70_000)] for d in ("bf16", "fp16")]
     streams = [torch.cuda.Stream() for _ in sets]
-    norms = [Norm([t.entry() for t in ts]) for ts in sets]
+    norms, alone = ([Norm([t.entry() for t in ts]) for ts in sets] for _ in range(2))
     torch.cuda.synchronize()
     for _ in range(10):
         for ts, n, s in zip(sets, norms, streams):
             zs.zs3_accumulate_tensors([t.entry() for t in ts], 0.5, False, norm=n.args, stream=s)
             for t in ts:
                 t.acc = og.accumulate(t.acc, t.x, 0.5, False)
+        # and the lists' own norms, on the other stream each: workspaces of their own
+        for ts, n, s in zip(sets, alone, reversed(streams)):
+            zs.zs3_grad_norm_tensors([t.entry() for t in ts], n.args, stream=s)
     torch.cuda.synchronize()
+    for ts, n in zip(sets, alone):
+        n.check([(t.x, t.shared) for t in ts])
     for ts, n in zip(sets, norms):
         n.check([(t.acc, t.shared) for t in ts])
         for t in ts:

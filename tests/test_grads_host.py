@@ -214,6 +214,26 @@ def test_overlaps_are_found_in_any_order():
             _refused(zs.ZS3_EALIAS, "overlap", _acc, ts)
 
 
+def test_tensors_have_to_fit_what_is_said_of_them():
+    """Lists and arguments made of torch tensors (never read here)."""
+    import torch
+    g, a = torch.zeros(10, dtype=torch.bfloat16), torch.zeros(10)
+    ok = zs.zs3_grad_tensor_list([dict(numel=10, grad=g, dtype="bf16", out=a, out_dtype="fp32"), dict(numel=9, grad=g, dtype="bf16")])
+    assert (ok[0].grad, ok[0].out, ok[1].out, ok[1].out_dtype) == (g.data_ptr(), a.data_ptr(), None, zs.ZS3_BF16)
+    for bad, text in ((dict(numel=10, grad=a, dtype="bf16"), "grad has 4-byte"), (dict(numel=11, grad=g, dtype="bf16"), "11 elements"),
+                      (dict(numel=10, grad=g, dtype="bf16", out=a), "out has 4-byte"),
+                      (dict(numel=5, grad=g[::2], dtype="bf16"), "one behind the other"),
+                      (dict(numel=10, grad=g, dtype="bf16", out=a[:9], out_dtype="fp32"), "10 elements")):
+        with pytest.raises(ValueError, match=text):
+            zs.zs3_grad_tensor_list([bad])
+    d, f, i = torch.zeros(4, dtype=torch.float64), torch.zeros(1), torch.zeros(1, dtype=torch.int32)
+    args = dict(sums=d[:3], world=2, norm=d[3:], scale=f, nonfinite=i, workspace=torch.zeros(64, dtype=torch.uint8))
+    assert zs.zs3_norm_args_of(**args).workspace_bytes == 64
+    for k, bad in (("sums", d[:2]), ("sums", f), ("norm", f), ("scale", d), ("nonfinite", d), ("tensor_norms", f)):
+        with pytest.raises(ValueError, match=k):
+            zs.zs3_norm_args_of(**dict(args, **{k: bad}))
+
+
 # --------------------------------------------------------------- ShardStep
 
 def _host_step(**k):

@@ -594,17 +594,28 @@ def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, d
 
 # ------------------------------------------------ gradients over a tensor list
 
+def _sized(x, name: str, item: int, numel: int) -> Optional[int]:
+    """The address of x; a torch tensor has to hold numel elements of `item` bytes, one behind the other."""
+    if hasattr(x, "data_ptr"):
+        if x.element_size() != item:
+            raise ValueError(f"{name} has {x.element_size()}-byte elements, not {item}-byte ones")
+        if not x.is_contiguous() or x.numel() < numel:
+            raise ValueError(f"{name} is not {numel} elements one behind the other")
+    return _ptr(x)
+
+
 def zs3_grad_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
     """The list that the norm, the clip and the accumulation take: one dict a
     tensor with numel, grad, dtype and, where they differ from these, out=None,
     out_dtype=dtype ("fp32" where out is an accumulator), shared=False.  It holds
     addresses only: a caller keeps it for as long as its buffers stay where they are."""
     out = (zs3_grad_tensor * max(1, len(tensors)))()
-    for o, t in zip(out, tensors):
-        o.numel, o.grad, o.out = int(t["numel"]), _ptr(t["grad"]), _ptr(t.get("out"))
-        o.dtype = _dtype_lowbit(t["dtype"])
+    for i, (o, t) in enumerate(zip(out, tensors)):
+        o.numel, o.dtype = int(t["numel"]), _dtype_lowbit(t["dtype"])
         o.out_dtype = o.dtype if t.get("out_dtype") is None else _dtype_lowbit(t["out_dtype"])
         o.shared = int(bool(t.get("shared", False)))
+        o.grad = _sized(t["grad"], f"tensor {i}: grad", 4 if o.dtype == ZS3_FP32 else 2, o.numel)
+        o.out = _sized(t.get("out"), f"tensor {i}: out", 4 if o.out_dtype == ZS3_FP32 else 2, o.numel)
     out.count = len(tensors)
     return out
 
@@ -630,8 +641,10 @@ def zs3_norm_args_of(*, sums, workspace=None, workspace_bytes: Optional[int] = N
     dtype=torch.uint8, device="cuda")``)."""
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "data_ptr") else 0
-    return zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale), _ptr(sums),
-                         _ptr(norm), _ptr(scale), _ptr(nonfinite), _ptr(tensor_norms), _ptr(workspace), int(workspace_bytes))
+    return zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale),
+                         _sized(sums, "sums", 8, int(world) + 1), _sized(norm, "norm", 8, 1), _sized(scale, "scale", 4, 1),
+                         _sized(nonfinite, "nonfinite", 4, 1), _sized(tensor_norms, "tensor_norms", 8, 0), _ptr(workspace),
+                         int(workspace_bytes))
 
 
 def _norm_args(a) -> zs3_norm_args:

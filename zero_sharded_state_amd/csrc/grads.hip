@@ -648,15 +648,18 @@ static WritePlanOf<N> smaller(const WritePlan& plan) {
     return p;
 }
 
-template <int KIND>
-static hipError_t norm_launch(const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
-    const int32_t groups = plan.runs.of_tile(plan.first_tile[plan.n] - 1) + 1;
-    if (plan.n <= kNormMid) return launch(k_norm<KIND, kNormMid>, groups, kGrBlock, 0, stream, smaller<kNormMid>(plan), parts, end);
-    return launch(k_norm<KIND, kNormTensors>, groups, kGrBlock, 0, stream, plan, parts, end);
+template <int KIND, int N>
+static hipError_t norm_launch(const NormPlanOf<N>& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
+    return launch(k_norm<KIND, N>, plan.runs.of_tile(plan.first_tile[plan.n] - 1) + 1, kGrBlock, 0, stream, plan, parts, end);
 }
 
 hipError_t launch_norm(int32_t kind, const NormPlan& plan, const NormParts& parts, const NormEnd& end, hipStream_t stream) {
-    return kind == kMax ? norm_launch<kMax>(plan, parts, end, stream) : norm_launch<kSum>(plan, parts, end, stream);
+    const auto go = [&](const auto& p) {
+        return kind == kMax ? norm_launch<kMax>(p, parts, end, stream) : norm_launch<kSum>(p, parts, end, stream);
+    };
+    if (plan.n <= kFewTensors) return go(smaller<kFewTensors>(plan));
+    if (plan.n <= kNormMid) return go(smaller<kNormMid>(plan));
+    return go(plan);
 }
 
 hipError_t launch_norm_few(const NormPlan& plan, const NormEnd& end, double* tensor_norms, hipStream_t stream) {

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import operator
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libzs3.so")
@@ -594,6 +595,11 @@ def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, d
 
 # ------------------------------------------------ gradients over a tensor list
 
+# A zs3_grad_tensor as bytes: a list of them made so takes half the time
+# of one filled field by field.
+_GRAD_ROW = struct.Struct("=qQQiiii")
+
+
 def _sized(x, name: str, item: int, numel: int) -> Optional[int]:
     """The address of x; a torch tensor has to hold numel elements of `item` bytes, one behind the other."""
     if hasattr(x, "data_ptr"):
@@ -609,15 +615,20 @@ def zs3_grad_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
     tensor with numel, grad, dtype and, where they differ from these, out=None,
     out_dtype=dtype ("fp32" where out is an accumulator), shared=False.  It holds
     addresses only: a caller keeps it for as long as its buffers stay where they are."""
-    out = (zs3_grad_tensor * max(1, len(tensors)))()
-    for i, (o, t) in enumerate(zip(out, tensors)):
-        o.numel, o.dtype = int(t["numel"]), _dtype_lowbit(t["dtype"])
-        o.out_dtype = o.dtype if t.get("out_dtype") is None else _dtype_lowbit(t["out_dtype"])
-        o.shared = int(bool(t.get("shared", False)))
-        o.grad = _sized(t["grad"], f"tensor {i}: grad", 4 if o.dtype == ZS3_FP32 else 2, o.numel)
-        o.out = _sized(t.get("out"), f"tensor {i}: out", 4 if o.out_dtype == ZS3_FP32 else 2, o.numel)
-    out.count = len(tensors)
-    return out
+    pack, codes, rows = _GRAD_ROW.pack, _DTYPES_LOWBIT, []
+    for i, t in enumerate(tensors):
+        get = t.get
+        numel, dtype, grad, out, out_dtype = t["numel"], t["dtype"], t["grad"], get("out"), get("out_dtype")
+        dtype = codes[dtype] if type(dtype) is str else int(dtype)
+        out_dtype = codes[out_dtype] if type(out_dtype) is str else dtype if out_dtype is None else int(out_dtype)
+        if type(grad) is not int:
+            grad = _sized(grad, f"tensor {i}: grad", 4 if dtype == ZS3_FP32 else 2, numel)
+        if type(out) is not int and out is not None:
+            out = _sized(out, f"tensor {i}: out", 4 if out_dtype == ZS3_FP32 else 2, numel)
+        rows.append(pack(numel, grad or 0, out or 0, dtype, out_dtype, 1 if get("shared") else 0, 0))
+    arr = (zs3_grad_tensor * len(rows)).from_buffer_copy(b"".join(rows)) if rows else (zs3_grad_tensor * 1)()
+    arr.count = len(rows)
+    return arr
 
 
 def _grad_list(tensors):

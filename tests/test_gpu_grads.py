@@ -181,6 +181,43 @@ def test_norm_of_large_tensors(dtype):
     _norm([Tensor(rng, n, dtype, i % 3) for i, n in enumerate(sizes)], kind="inf")
 
 
+@pytest.mark.parametrize("count,numel", [(1, 40_000_000), (700, 20_001), (1500, 20_001), (3000, 20_001)])
+@pytest.mark.parametrize("kind", ["2", "inf"])
+def test_joins_of_many_partial_sums(kind, count, numel):
+    """Lists past what the last workgroup and what one workgroup join, over several launches.
+    Small whole numbers: every sum of their squares is exact, in any order."""
+    import torch
+    require_gpu()
+    note(f"{count} tensors of {numel}, {kind}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(count)
+    flat = torch.randint(-8, 9, (count * numel,), device="cuda", generator=g).to(torch.bfloat16)
+    flat[-1] = 15.0
+    acc = torch.full((count * numel,), math.nan, device="cuda")
+    entries = [dict(numel=numel, grad=flat.data_ptr() + 2 * numel * i, dtype="bf16", out=acc.data_ptr() + 4 * numel * i,
+                    out_dtype="fp32", shared=i % 3 == 1) for i in range(count)]
+    x = flat.view(count, numel).double()
+    each = x.square().sum(1) if kind == "2" else x.abs().amax(1)
+    shared = torch.arange(count, device="cuda") % 3 == 1
+    join = (lambda v: float(v.sum())) if kind == "2" else (lambda v: float(v.max()) if v.numel() else 0.0)
+    want = [join(each[~shared]), join(each[shared])]
+    total = sum(want) if kind == "2" else max(want)
+    arr = zs.zs3_grad_tensor_list(entries)
+    for f in (1.0, 2.0):                # acc = x, then 2 x + x
+        n = Norm(entries, kind=kind, max_norm=math.inf)
+        zs.zs3_grad_norm_tensors(arr, n.args)
+        fused = Norm(entries, kind=kind, max_norm=math.inf)
+        zs.zs3_accumulate_tensors(arr, f, first=f == 1.0, norm=fused.args)
+        torch.cuda.synchronize()
+        for got, k in ((n.got(), 1), (fused.got(), 1 if f == 1.0 else 3)):
+            power = k * k if kind == "2" else k
+            assert got["sums"].tolist() == [power * w for w in want] and got["flag"] == 0
+            assert got["norm"] == (math.sqrt(power * total) if kind == "2" else power * total)
+            root = torch.sqrt(power * each) if kind == "2" else power * each
+            np.testing.assert_allclose(got["each"], root.cpu().numpy(), rtol=2.0 ** -52 if kind == "2" else 0.0)
+    assert torch.equal(acc, 3 * flat.float())
+
+
 def test_norm_without_elements():
     require_gpu()
     note("empty lists")

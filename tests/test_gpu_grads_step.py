@@ -257,3 +257,85 @@ def test_a_trace_scheduled_step_over_micro_batches():
     finally:
         step.destroy()
     assert zs.zs3_abi_version() == 3
+
+
+def _values(step, rng):
+    """Random contents of the gradient that the step holds, and each parameter's real elements of it."""
+    import torch
+    x = (rng.standard_normal(step.S) * 1e-1).astype(np.float32)
+    if step.acc is None:
+        bits = oracle.from_f32(x, step.dtype)
+        step.grad.copy_(torch.from_numpy(bits.view(np.int16)))
+        x = oracle.to_f32(bits, step.dtype)
+    else:
+        step.acc.copy_(torch.from_numpy(x))
+    return [x[p["shard_offset"]:p["shard_offset"] + p["own"][1] - p["own"][0]] for p in step.params]
+
+
+def _check_each(each, parts, kind="2"):
+    # sums of n positive terms in binary64, then a root
+    tol = (sum(SIZES) * 2.0 ** -53 + 2.0 ** -51) if kind == "2" else 0.0
+    want = [math.sqrt(og.part(x, kind)) if kind == "2" else og.part(x, kind) for x in parts]
+    np.testing.assert_allclose(each.cpu().numpy(), want, rtol=tol, atol=0)
+
+
+@pytest.mark.parametrize("accumulate", [1, 2])
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_single_norms_and_clip_on_another_stream(accumulate, handle):
+    """The step's first such calls, on a stream that is behind: their results, and that what is allocated
+    and written on the current stream meanwhile stays as it was."""
+    import torch
+    note(f"norms and clip on another stream, accumulate={accumulate}")
+    rng = np.random.default_rng(12)
+    step = _make(4, 1, "bf16", accumulate=accumulate)
+    try:
+        s = torch.cuda.Stream()
+        on = int(s.cuda_stream) if handle else s
+        for k in range(4):
+            parts = _values(step, rng)
+            step.outs.zero_()
+            step.outs.view(torch.float32)[2] = 0.75
+            torch.cuda.synchronize()
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(20_000_000)       # about 10 ms
+            each, top = step.grad_norms(stream=on), step.grad_norms(inf=True, stream=on)
+            step.clip_grads(stream=on)
+            mine = [torch.full((2,), -7.0, dtype=torch.float64, device="cuda") for _ in range(200)]
+            s.synchronize()
+            _check_each(each, parts)
+            _check_each(top, parts, "inf")
+            assert all(bool((x == -7.0).all()) for x in mine)
+            for x, p in zip(parts, step.params):
+                o = p["shard_offset"]
+                if accumulate == 1:
+                    assert np.array_equal(_h16(step.grad[o:o + len(x)]), og.clip(x, 0.75, "bf16"))
+                else:
+                    assert np.array_equal(step.acc[o:o + len(x)].cpu().numpy(), og.clip(x, 0.75, "fp32"))
+    finally:
+        step.destroy()
+
+
+@pytest.mark.parametrize("accumulate", [1, 2])
+def test_single_norms_captured_at_once(accumulate):
+    """A step's first call of them is captured, then replayed between eager ones."""
+    import torch
+    note(f"norms captured first, accumulate={accumulate}")
+    rng = np.random.default_rng(13)
+    step = _make(4, 1, "fp16", accumulate=accumulate)
+    try:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            each = step.grad_norms()
+        for k in range(4):
+            eager = step.grad_norms()
+            parts = _values(step, rng)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            _check_each(each, parts)
+            eager = step.grad_norms()
+            torch.cuda.synchronize()
+            assert torch.equal(eager, each)
+    finally:
+        step.destroy()

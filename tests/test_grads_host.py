@@ -304,3 +304,41 @@ def test_shard_step_counts_the_bytes_of_every_micro_batch():
     assert b["accumulate"] == 4 * (2 + 4) * own + 3 * 4 * own
     assert b["grad_norm"] == 4 * own and b["adam"] == a["adam"] + 2 * own
     one.destroy(), four.destroy()
+
+
+class _Recorder:
+    """Takes the library's place: what each call of a gradient list carries."""
+
+    def __init__(self):
+        self.calls, self.real = [], zs.lib()
+
+    def __getattr__(self, name):
+        if name not in ("zs3_grad_norm_tensors", "zs3_clip_tensors", "zs3_accumulate_tensors", "zs3_norm_finalize", "zs3_adamw_tensors"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return zs.ZS3_OK
+        return call
+
+
+@pytest.mark.parametrize("accumulate", [1, 3])
+def test_single_norms_use_buffers_that_the_step_keeps(accumulate, monkeypatch):
+    """Sums and workspace of ``grad_norms`` are the step's own from its start (a buffer made or
+    dropped at the call belongs to another stream than the kernel's)."""
+    import torch
+    st = _host_step(accumulate=accumulate)
+    held = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in vars(st).values() if torch.is_tensor(t)]
+    rec = _Recorder()
+    with monkeypatch.context() as m:
+        m.setattr(zs, "lib", lambda: rec)
+        for inf in (False, True):
+            each = st.grad_norms(inf=inf, stream=0)
+    for name, (n, _, args, _) in rec.calls:
+        a = args._obj
+        assert name == "zs3_grad_norm_tensors" and n == each.numel() == 2
+        for p, size in ((a.sums, 16), (a.workspace, a.workspace_bytes)):
+            assert any(lo <= p and p + size <= hi for lo, hi in held)
+    assert a.tensor_norms == each.data_ptr() and len(rec.calls) == 2
+    assert a.sums != st.sumsq.data_ptr()
+    st.destroy()

@@ -44,11 +44,14 @@ sum (with ``fuse_norm`` in the same pass) and steps on the sum.
 for an optimizer of the caller's own.
 
 No call synchronises; nothing is copied to the host.  All buffers are torch
-tensors owned by this object; all arithmetic runs in libzs3's kernels.
+tensors owned by this object, made and cleared on the stream that is current when it is
+made (a caller who goes on with another stream lets that one wait for it); all arithmetic
+runs in libzs3's kernels.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import hashlib
 import operator
@@ -240,6 +243,7 @@ class ShardStep:
             self.exp_avg_sq = self.state[2 * sa:2 * sa + max(1, self.S)]
         self.acc = torch.zeros(max(1, self.S), dtype=f32, device=dev) if accumulate > 1 else None
         self.sumsq = torch.zeros(self.N + 1, dtype=torch.float64, device=dev)
+        self.each_sums = torch.zeros(2, dtype=torch.float64, device=dev)      # of grad_norms, looked at by nobody
         self.n_slots, _ = zs.zs3_layout_norm_slots(self.h)
         self.partials = torch.zeros(max(1, self.n_slots), dtype=torch.float64, device=dev)
         if reduce_path == "coalesced":
@@ -393,12 +397,14 @@ class ShardStep:
             self._listed_decay = self.adam.weight_decay
             self._lists = [zs.zs3_adamw_tensor_list([self._tensor(p) for p in self.params if b <= p["shard_offset"] < e])
                            for b, e in self.sub_groups]
-        self._grad_list = None
+        # the gradient that the norm and the clip see: the sum, or the flat gradient
+        held, kind = (self.grad, self.dtype) if self.acc is None else (self.acc, "fp32")
+        self._grad_list = zs.zs3_grad_tensor_list([self._gradient(p, held, kind) for p in self.params])
+        self.norm_workspace = self.torch.zeros(zs.zs3_norm_workspace_bytes(self._grad_list), dtype=self.torch.uint8, device=self.device)
         if self.accumulate > 1:
             self._acc_list = zs.zs3_grad_tensor_list([
                 dict(self._gradient(p, self.grad, self.dtype), out=self.acc.data_ptr() + 4 * p["shard_offset"], out_dtype="fp32")
                 for p in self.params])
-            self._held()
         all_ids = [p["ds_id"] for p in self.params]
         self._p = (len(all_ids), (I64 * len(all_ids))(*all_ids),
                    (P * len(all_ids))(*[self.full_param_ptr(d) for d in all_ids]))
@@ -566,15 +572,6 @@ class ShardStep:
         self._ok(zs.lib().zs3_partition(self.h, self.rank, self.dcode, n, ids, ptrs, out.data_ptr(),
                                         stream if stream is not None else self._stream()))
 
-    def _held(self):
-        """The gradient that the norm and the clip see, as a list: the sum, or the flat gradient."""
-        if self._grad_list is None:
-            held, kind = (self.grad, self.dtype) if self.acc is None else (self.acc, "fp32")
-            self._grad_list = zs.zs3_grad_tensor_list([self._gradient(p, held, kind) for p in self.params])
-            self.norm_workspace = self.torch.zeros(zs.zs3_norm_workspace_bytes(self._grad_list), dtype=self.torch.uint8,
-                                                   device=self.device)
-        return self._grad_list
-
     def _norm_args(self, finalize: bool, **over):
         return zs.zs3_norm_args_of(**dict(
             dict(rank=self.rank, world=self.N, finalize=finalize, max_norm=self.max_norm, sums=self.sumsq, norm=self.norm_ptr,
@@ -589,28 +586,38 @@ class ShardStep:
         zs.zs3_accumulate_tensors(self._acc_list, 1.0 / self.accumulate, first=self.micro == 0, norm=args,
                                   stream=stream if stream is not None else self._stream())
 
+    def _allocating_on(self, stream):
+        """torch's allocations as those of ``stream`` (a Stream or its handle): memory that earlier
+        work of another stream may still use is not given out, nor is it taken back before ``stream`` is done."""
+        cuda = self.torch.cuda
+        if stream is None or self.device.type != "cuda":
+            return contextlib.nullcontext()
+        if isinstance(stream, int):
+            stream = cuda.ExternalStream(stream, device=self.device) if stream else cuda.default_stream(self.device)
+        return cuda.stream(stream)
+
     def grad_norms(self, inf: bool = False, stream=None):
         """The norm of each parameter's real elements of the gradient that the step
         holds (the sum of the micro-batches so far, if it accumulates), as doubles in the
         order of ``params``; with ``inf`` the largest magnitude.  The clip norm and its
-        sums are left alone.  On the step's own stream, whose workspace it uses."""
-        torch = self.torch
-        held = self._held()
-        each = torch.empty(len(self.params), dtype=torch.float64, device=self.device)
-        sums = torch.empty(2, dtype=torch.float64, device=self.device)
-        args = self._norm_args(False, rank=0, world=1, sums=sums, tensor_norms=each, kind=zs.ZS3_NORM_INF if inf else zs.ZS3_NORM_2)
-        zs.zs3_grad_norm_tensors(held, args, stream=stream if stream is not None else self._stream())
+        sums are left alone.  The result is a new tensor of ``stream``'s, which the step's
+        norms run on too (they share a workspace): a reader elsewhere waits for it."""
+        with self._allocating_on(stream):
+            each = self.torch.empty(len(self.params), dtype=self.torch.float64, device=self.device)
+        args = self._norm_args(False, rank=0, world=1, sums=self.each_sums, tensor_norms=each,
+                               kind=zs.ZS3_NORM_INF if inf else zs.ZS3_NORM_2)
+        zs.zs3_grad_norm_tensors(self._grad_list, args, stream=stream if stream is not None else self._stream())
         return each
 
     def clip_grads(self, stream=None):
         """Multiplies the gradient that the step holds by the clip scale of the last norm, in place
         (nothing, where the norm was not finite): for an optimizer of the caller's own in
         place of ``adam_step``, which takes the scale itself."""
-        zs.zs3_clip_tensors(self._held(), self.scale_ptr, self.flag_ptr, stream=stream if stream is not None else self._stream())
+        zs.zs3_clip_tensors(self._grad_list, self.scale_ptr, self.flag_ptr, stream=stream if stream is not None else self._stream())
 
     def grad_norm(self, finalize: bool = True, stream=None):
         if self.acc is not None:
-            zs.zs3_grad_norm_tensors(self._held(), self._norm_args(finalize),
+            zs.zs3_grad_norm_tensors(self._grad_list, self._norm_args(finalize),
                                      stream=stream if stream is not None else self._stream())
             return
         if self.fuse_norm:

@@ -339,3 +339,65 @@ def test_single_norms_captured_at_once(accumulate):
             assert torch.equal(eager, each)
     finally:
         step.destroy()
+
+
+@pytest.mark.parametrize("fuse,phases", [(True, False), (False, False), (True, True)], ids=["fused", "norm alone", "phase by phase"])
+@pytest.mark.parametrize("K", [1, 3])
+def test_an_optimizer_of_the_callers_own(K, fuse, phases):
+    """Two steps in a row that stop before AdamW: the clipped sum of each, nothing of the step before in it,
+    master and moments as they were, and parameters that the caller has written to the shard gathered next."""
+    import torch
+    if K == 1 and phases:
+        pytest.skip("no accumulators")
+    note(f"own optimizer, K={K} fuse_norm={fuse} phases={phases}")
+    world, rank, rng = 4, 1, np.random.default_rng(21)
+    step = _make(world, rank, "bf16", fuse_norm=fuse, accumulate=K)
+    try:
+        L = oracle.make_layout(world, 100, IDS, SIZES)
+        _start(step, rng)
+        own = [(p.shard_offset, p.shard_offset + L.own_range(p, rank)[1] - L.own_range(p, rank)[0]) for p in L.params]
+        before = [x.clone() for x in (step.master, step.exp_avg, step.exp_avg_sq)]
+        for t in (1, 2):
+            acc = np.full(L.shard_numel, np.nan, np.float32)
+            for k in range(K):
+                grads = [{p.ds_id: oracle.from_f32(rng.standard_normal(p.numel).astype(np.float32), "bf16") for p in L.params}
+                         for _ in range(world)]
+                flat = np.zeros(L.shard_numel, np.uint16)
+                oracle.reduce_scatter(L, rank, "bf16", IDS, grads, flat)
+                _send(step, grads, rank)
+                step.sumsq.zero_()
+                if phases:
+                    step.gather_pass()
+                    step.reduce_scatter()
+                    step.accumulate_grads(norm=k == K - 1)
+                else:
+                    (step.gradient_step if k == K - 1 else step.micro_step)()
+                for lo, hi in own:
+                    x = oracle.to_f32(flat[lo:hi], "bf16")
+                    acc[lo:hi] = x if K == 1 else og.accumulate(acc[lo:hi], x, 1.0 / K, k == 0)
+            step.clip_grads()
+            sync()
+            assert (step.t, step.micro) == (t, 0)
+            scale = float(step.outs.view(torch.float32)[2])
+            s = og.sums([(acc[lo:hi], p.persistent) for (lo, hi), p in zip(own, L.params)], "2", [0.0] * (world + 1), rank)
+            # sums of positive terms in binary64, a root, and the rounding to fp32
+            want = og.finalize(s, "2", 1.0, 1.0)[1]
+            assert scale < 1.0 and abs(scale - want) <= (2.0 ** -24 + (sum(SIZES) + 6) * 2.0 ** -53 + 2.0 ** -50) * want
+            for lo, hi in own:
+                if K == 1:
+                    assert np.array_equal(_h16(step.grad[lo:hi]), og.clip(acc[lo:hi], scale, "bf16"))
+                else:
+                    assert np.array_equal(step.acc[lo:hi].cpu().numpy(), og.clip(acc[lo:hi], scale, "fp32"))
+            for a, b in zip(before, (step.master, step.exp_avg, step.exp_avg_sq)):
+                assert torch.equal(a, b)
+            # the caller's own update
+            held = step.grad.view(torch.bfloat16) if K == 1 else step.acc
+            step.shard.view(torch.bfloat16).sub_(held, alpha=0.5)
+            step.gather_pass()
+            sync()
+            for p in step.params:
+                if not p["persistent"]:
+                    o, (lo, hi) = step.full_off[p["ds_id"]], p["own"]
+                    assert torch.equal(step.full[o + lo:o + hi], step.shard[p["shard_offset"]:p["shard_offset"] + hi - lo])
+    finally:
+        step.destroy()

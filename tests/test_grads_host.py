@@ -313,7 +313,7 @@ class _Recorder:
         self.calls, self.real = [], zs.lib()
 
     def __getattr__(self, name):
-        if name not in ("zs3_grad_norm_tensors", "zs3_clip_tensors", "zs3_accumulate_tensors", "zs3_norm_finalize", "zs3_adamw_tensors"):
+        if name.startswith("zs3_layout") or name in ("zs3_norm_workspace_bytes", "zs3_last_error"):
             return getattr(self.real, name)
 
         def call(*args):
@@ -341,4 +341,72 @@ def test_single_norms_use_buffers_that_the_step_keeps(accumulate, monkeypatch):
             assert any(lo <= p and p + size <= hi for lo, hi in held)
     assert a.tensor_norms == each.data_ptr() and len(rec.calls) == 2
     assert a.sums != st.sumsq.data_ptr()
+    st.destroy()
+
+
+class _NoStream:
+    """What the recorder's calls run on."""
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("path", ["phases", "micro_step", "mixed"])
+def test_every_way_through_a_step_counts_its_micro_batches(path, monkeypatch):
+    """Two steps without AdamW, by phases, by ``micro_step`` and ``gradient_step``, and
+    by both in turn: the first micro-batch of each overwrites, the others add, the norm comes once, seeds
+    of the 4-bit wire do not repeat, and what takes the whole sum waits for it."""
+    from zero_sharded_state_amd.shard_step import ShardStep
+    st = ShardStep(world_size=2, rank=1, threshold=0, ds_ids=[0, 1], numels=[64, 65], dtype="bf16", prefetch_bucket_size=1000,
+                   reduce_bucket_size=1000, sub_group_size=1000, device="cpu", reduce_path="coalesced", reduce_bits=4, accumulate=3,
+                   fuse_norm=True)
+    on = _NoStream()
+    rec = _Recorder()
+
+    def by_phases(last):
+        st.gather_pass(on)
+        st.reduce_scatter(on)
+        st.accumulate_grads(on, norm=last)
+    with monkeypatch.context() as m:
+        m.setattr(zs, "lib", lambda: rec)
+        for t in (1, 2, 3, 4):
+            for k in range(3):
+                if path == "phases" or path == "mixed" and (t + k) % 2:
+                    by_phases(k == 2)
+                else:
+                    (st.gradient_step if k == 2 else st.micro_step)(on)
+                assert (st.t, st.micro) == (t, (k + 1) % 3)
+                if k < 2:
+                    for call in (st.clip_grads, lambda **a: st.adam_step(1, **a)):
+                        with pytest.raises(ValueError, match=f"{k + 1} of 3 micro-batches"):
+                            call(stream=0)
+            st.clip_grads(stream=0)
+        st.micro_step(on)
+        with pytest.raises(ValueError, match="1 of 2 micro-batches before"):
+            st.gradient_step(on)
+        st.micro_step(on)
+        with pytest.raises(ValueError, match="micro-batch 3 of 3"):
+            st.micro_step(on)
+        st.step(on)
+        assert (st.t, st.micro) == (5, 0)
+    acc = [a for name, a in rec.calls if name == "zs3_accumulate_tensors"]
+    assert [a[3] for a in acc] == [1, 0, 0] * 5 and all(a[2] == 1 / 3 for a in acc)
+    assert [a[4] is not None for a in acc] == [False, False, True] * 5
+    seeds = [a[-2] for name, a in rec.calls if name == "zs3_reduce_scatter_coalesced_mx4"]
+    assert len(seeds) == len(set(seeds)) == 15 * len(st._x)
+    order = [name for name, _ in rec.calls if name in ("zs3_clip_tensors", "zs3_adamw_tensors")]
+    assert order == ["zs3_clip_tensors"] * 4 + ["zs3_adamw_tensors"] * len(st._lists)
+    st.destroy()
+
+
+def test_a_step_without_accumulators_stops_before_adamw(monkeypatch):
+    st, rec = _host_step(), _Recorder()
+    phases = []
+    with monkeypatch.context() as m:
+        m.setattr(zs, "lib", lambda: rec)
+        st.gradient_step(_NoStream(), on_phase=phases.append)
+        st.clip_grads(stream=0)
+        st.step(_NoStream())
+    assert phases == ["gather_fwd", "gather_bwd", "reduce_scatter", "grad_norm", None] and st.t == 2
+    names = [name for name, _ in rec.calls]
+    assert names.count("zs3_grad_norm") == 2 and names.count("zs3_adam_step") == len(st.sub_groups)
+    assert names.index("zs3_clip_tensors") < names.index("zs3_adam_step")
     st.destroy()

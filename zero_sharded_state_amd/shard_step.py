@@ -40,8 +40,10 @@ Several micro-batches a step (``accumulate=K``): ``micro_step`` runs 1 to 3 for
 each of the first K-1 and adds their averaged gradients, over K, to fp32
 accumulators; ``step`` does the same with the last one, takes the norm of the
 sum (with ``fuse_norm`` in the same pass) and steps on the sum.
-``grad_norms`` looks at each parameter's gradient, ``clip_grads`` scales them
-for an optimizer of the caller's own.
+``grad_norms`` looks at each parameter's gradient.  For an optimizer of the
+caller's own ``gradient_step`` stands in ``step``'s place and stops before AdamW;
+``clip_grads`` then scales the gradient.  Called phase by phase,
+``accumulate_grads`` counts the micro-batches.
 
 No call synchronises; nothing is copied to the host.  All buffers are torch
 tensors owned by this object, made and cleared on the stream that is current when it is
@@ -97,7 +99,9 @@ class ShardStep:
         self.listed = state_bits == 8 or bool(no_decay) or accumulate > 1
         if self.listed and offload:
             raise ValueError("offloaded state has 32 bits and one weight decay, and steps on 16-bit gradients")
-        self.accumulate, self.micro = accumulate, 0     # micro: accumulated in the step under way
+        # micro: accumulated in the step under way (0 again once its sum is whole);
+        # _begun: t counts that step already
+        self.accumulate, self.micro, self._begun = accumulate, 0, False
         unknown = no_decay - set(ds_ids)
         if unknown:
             raise ValueError(f"no_decay names ds_ids that are not there: {sorted(unknown)}")
@@ -528,6 +532,8 @@ class ShardStep:
         """Every gradient bucket, fanned out over the main and auxiliary
         streams and joined back into the main stream."""
         lib = zs.lib()
+        if self.acc is not None:
+            self._begin()
         # with accumulators it is their sum that has a norm
         partials = self.partials.data_ptr() if self.fuse_norm and self.acc is None else None
         if self.single_reduce:
@@ -577,14 +583,28 @@ class ShardStep:
             dict(rank=self.rank, world=self.N, finalize=finalize, max_norm=self.max_norm, sums=self.sumsq, norm=self.norm_ptr,
                  scale=self.scale_ptr, nonfinite=self.flag_ptr, workspace=self.norm_workspace), **over))
 
+    def _begin(self):
+        """Counts the step that a first micro-batch begins, once: seeds and AdamW go by it."""
+        if not self._begun:
+            self.t += 1
+            self._begun = True
+
+    def _whole(self, what: str):
+        if self.micro != 0:
+            raise ValueError(f"{what} takes the whole sum, of which {self.micro} of {self.accumulate} micro-batches are there")
+
     def accumulate_grads(self, stream=None, norm: bool = False):
         """Adds the flat gradient, over the number of micro-batches, to the
-        accumulators (the first of a step overwrites them), with the norm of the sum where asked."""
+        accumulators and counts it (the first of a step overwrites them, the last one makes the
+        sum whole), with the norm of the sum so far where asked."""
         if self.acc is None:
             raise ValueError("accumulate is 1: there are no accumulators")
         args = self._norm_args(True) if norm else None
+        self._begin()
         zs.zs3_accumulate_tensors(self._acc_list, 1.0 / self.accumulate, first=self.micro == 0, norm=args,
                                   stream=stream if stream is not None else self._stream())
+        self.micro = (self.micro + 1) % self.accumulate
+        self._begun = self.micro != 0
 
     def _allocating_on(self, stream):
         """torch's allocations as those of ``stream`` (a Stream or its handle): memory that earlier
@@ -611,8 +631,9 @@ class ShardStep:
 
     def clip_grads(self, stream=None):
         """Multiplies the gradient that the step holds by the clip scale of the last norm, in place
-        (nothing, where the norm was not finite): for an optimizer of the caller's own in
-        place of ``adam_step``, which takes the scale itself."""
+        (nothing, where the norm was not finite): for an optimizer of the caller's own, after
+        ``gradient_step``, in place of ``adam_step``, which takes the scale itself."""
+        self._whole("clip_grads")
         zs.zs3_clip_tensors(self._grad_list, self.scale_ptr, self.flag_ptr, stream=stream if stream is not None else self._stream())
 
     def grad_norm(self, finalize: bool = True, stream=None):
@@ -631,6 +652,7 @@ class ShardStep:
                                         self.flag_ptr, stream if stream is not None else self._stream()))
 
     def adam_step(self, t: int, stream=None):
+        self._whole("adam_step")
         a = self.adam
         hp = zs.zs3_adam_params(a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, int(t))
         s = stream if stream is not None else self._stream()
@@ -685,13 +707,21 @@ class ShardStep:
         if self.micro >= self.accumulate - 1:
             raise ValueError(f"micro-batch {self.micro + 1} of {self.accumulate} is step()'s")
         self._check_wire(gather_timer, trace_pass)
-        if self.micro == 0:
-            self.t += 1
+        self._begin()
         mark = on_phase or (lambda name: None)
         self._gather_and_reduce(stream, mark, gather_timer, trace_pass)
         mark("accumulate")
         self.accumulate_grads(stream)
-        self.micro += 1
+        mark(None)
+
+    def gradient_step(self, stream=None, on_phase=None, gather_timer=None, trace_pass=None):
+        """``step`` without its AdamW, and with its arguments: the (last) micro-batch's gathers,
+        reduce-scatter and accumulation, the norm and the clip scale.  What follows is
+        ``adam_step(self.t)``, or ``clip_grads`` and an optimizer of the caller's own on the flat
+        gradient (``grad``, with accumulators ``acc``), which leaves its 16-bit
+        parameters in ``shard``."""
+        mark = on_phase or (lambda name: None)
+        self._to_the_norm(stream, mark, gather_timer, trace_pass)
         mark(None)
 
     def step(self, stream=None, on_phase=None, gather_timer=None, trace_pass=None):
@@ -700,25 +730,29 @@ class ShardStep:
         and with None at the end (for event timing).  With ``trace_pass`` (a
         TraceGatherPass) the forward and backward gathers follow the
         fetch/release coordinator instead of the static gather buckets."""
+        mark = on_phase or (lambda name: None)
+        self._to_the_norm(stream, mark, gather_timer, trace_pass)
+        mark("adam")
+        self.adam_step(self.t, stream)
+        mark(None)
+
+    def _to_the_norm(self, stream, mark, gather_timer, trace_pass):
         self._check_wire(gather_timer, trace_pass)
         if self.micro != self.accumulate - 1:
             raise ValueError(f"{self.micro} of {self.accumulate - 1} micro-batches before step()")
-        if self.micro == 0:
+        if self.acc is None:
             self.t += 1
-        mark = on_phase or (lambda name: None)
+        else:
+            self._begin()
         self._gather_and_reduce(stream, mark, gather_timer, trace_pass)
         if self.acc is not None:
             mark("accumulate")
             self.accumulate_grads(stream, norm=self.fuse_norm)
-            self.micro = 0
         # the pre-step pass ([codex] 6.3): the gathered views are dropped;
         # the shard already is the partitioned form, so nothing moves
         if self.acc is None or not self.fuse_norm:
             mark("grad_norm")
             self.grad_norm(True, stream)
-        mark("adam")
-        self.adam_step(self.t, stream)
-        mark(None)
 
     # ------------------------------------------------------------ set-up
     def init_from_full(self):

@@ -410,3 +410,25 @@ def test_a_step_without_accumulators_stops_before_adamw(monkeypatch):
     assert names.count("zs3_grad_norm") == 2 and names.count("zs3_adam_step") == len(st.sub_groups)
     assert names.index("zs3_clip_tensors") < names.index("zs3_adam_step")
     st.destroy()
+
+
+def test_what_a_norm_writes_has_to_hold_it(monkeypatch):
+    """One place for each tensor's norm, and a workspace of the bytes it counts (the library is not reached)."""
+    import torch
+    rec = _Recorder()
+    monkeypatch.setattr(zs, "lib", lambda: rec)
+    each = torch.zeros(3, dtype=torch.float64)
+    for made in (lambda d: d, lambda d: zs.zs3_norm_args_of(**d)):
+        for call in (zs.zs3_grad_norm_tensors, lambda ts, a, stream: zs.zs3_accumulate_tensors(ts, norm=a, stream=stream)):
+            for ts in ([_t()] * 4, zs.zs3_grad_tensor_list([_t()] * 4)):
+                with pytest.raises(ValueError, match="tensor_norms has 3 elements, the list 4"):
+                    call(ts, made(_args(tensor_norms=each)), stream=0)
+            with pytest.raises(ValueError, match="tensor_norms has 0 elements"):
+                call([_t()], made(_args(tensor_norms=each[:0])), stream=0)
+    assert not rec.calls
+    zs.zs3_grad_norm_tensors([_t()] * 3, _args(tensor_norms=each), stream=0)
+    zs.zs3_norm_finalize(_args(tensor_norms=each[:0]), stream=0)
+    assert len(rec.calls) == 2
+    for bad in (torch.zeros(64, dtype=torch.uint8)[::2], torch.zeros(1, dtype=torch.uint8).expand(1 << 20)):
+        with pytest.raises(ValueError, match="workspace"):
+            zs.zs3_norm_args_of(**dict(_args(workspace=bad), workspace_bytes=None))

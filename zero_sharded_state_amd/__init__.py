@@ -650,23 +650,32 @@ def zs3_norm_args_of(*, sums, workspace=None, workspace_bytes: Optional[int] = N
     ``zs3_grad_tensor_list``; a tensor given as the workspace brings its bytes (it
     is zeros before its first use: ``torch.zeros(zs3_norm_workspace_bytes(tensors),
     dtype=torch.uint8, device="cuda")``)."""
+    if hasattr(workspace, "data_ptr") and not workspace.is_contiguous():
+        raise ValueError("workspace is not bytes one behind the other")
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "data_ptr") else 0
-    return zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale),
+    args = zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale),
                          _sized(sums, "sums", 8, int(world) + 1), _sized(norm, "norm", 8, 1), _sized(scale, "scale", 4, 1),
                          _sized(nonfinite, "nonfinite", 4, 1), _sized(tensor_norms, "tensor_norms", 8, 0), _ptr(workspace),
                          int(workspace_bytes))
+    args.room = tensor_norms.numel() if hasattr(tensor_norms, "data_ptr") else None      # of an address the caller knows
+    return args
 
 
-def _norm_args(a) -> zs3_norm_args:
-    return a if isinstance(a, zs3_norm_args) else zs3_norm_args_of(**a)
+def _norm_args(a, n: int = 0) -> zs3_norm_args:
+    """The arguments of a norm over a list of n."""
+    a = a if isinstance(a, zs3_norm_args) else zs3_norm_args_of(**a)
+    room = getattr(a, "room", None)
+    if room is not None and room < n:
+        raise ValueError(f"tensor_norms has {room} elements, the list {n} tensors")
+    return a
 
 
 def zs3_grad_norm_tensors(tensors, norm, stream=None) -> None:
     """``tensors``: what ``zs3_grad_tensor_list`` gives, or the dicts; ``norm``:
     what ``zs3_norm_args_of`` gives, or a dict of its arguments."""
     n, arr = _grad_list(tensors)
-    _check(lib().zs3_grad_norm_tensors(n, arr, ctypes.byref(_norm_args(norm)), _stream(stream)))
+    _check(lib().zs3_grad_norm_tensors(n, arr, ctypes.byref(_norm_args(norm, n)), _stream(stream)))
 
 
 def zs3_norm_finalize(norm, stream=None) -> None:
@@ -681,7 +690,7 @@ def zs3_clip_tensors(tensors, scale, nonfinite=None, stream=None) -> None:
 def zs3_accumulate_tensors(tensors, factor: float = 1.0, first: bool = False, norm=None, stream=None) -> None:
     n, arr = _grad_list(tensors)
     _check(lib().zs3_accumulate_tensors(n, arr, float(factor), int(bool(first)),
-                                        ctypes.byref(_norm_args(norm)) if norm is not None else None, _stream(stream)))
+                                        ctypes.byref(_norm_args(norm, n)) if norm is not None else None, _stream(stream)))
 
 
 # ------------------------------------------------------------- coordinator

@@ -432,3 +432,32 @@ def test_what_a_norm_writes_has_to_hold_it(monkeypatch):
     for bad in (torch.zeros(64, dtype=torch.uint8)[::2], torch.zeros(1, dtype=torch.uint8).expand(1 << 20)):
         with pytest.raises(ValueError, match="workspace"):
             zs.zs3_norm_args_of(**dict(_args(workspace=bad), workspace_bytes=None))
+
+
+def test_tensors_have_to_be_of_the_type_that_is_said(monkeypatch):
+    """A type of the same width is another one; 16-bit values may come as their bits."""
+    import torch
+    rec = _Recorder()
+    monkeypatch.setattr(zs, "lib", lambda: rec)
+    t = {d: torch.zeros(8, dtype=getattr(torch, d)) for d in ("float16", "bfloat16", "float32", "float64", "int16", "int32", "int64", "bool")}
+    for said, good in (("fp16", ("float16", "int16")), ("bf16", ("bfloat16", "int16")), ("fp32", ("float32",))):
+        for name, x in t.items():
+            for d, what in ((dict(numel=8, grad=x, dtype=said), "tensor 1: grad"), (dict(_t(), out=x, numel=8, out_dtype=said), "tensor 1: out")):
+                if name in good:
+                    zs.zs3_grad_tensor_list([_t(), d])
+                    continue
+                with pytest.raises(ValueError, match=what):
+                    zs.zs3_grad_tensor_list([_t(), d])
+    for k, good in (("sums", "float64"), ("norm", "float64"), ("tensor_norms", "float64"), ("scale", "float32"), ("nonfinite", "int32")):
+        for name, x in t.items():
+            if name == good:
+                zs.zs3_norm_args_of(**_args(**{k: x}))
+                continue
+            with pytest.raises(ValueError, match=k):
+                zs.zs3_norm_args_of(**_args(**{k: x}))
+    # a norm's own double as the scale, a flag of one byte, and neither
+    for scale, flag, what in ((t["float64"], None, "scale"), (t["bfloat16"], None, "scale"), (BASE, t["bool"], "nonfinite"),
+                              (BASE, t["float32"], "nonfinite"), (t["float32"][:0], None, "scale"), (BASE, t["int32"][:0], "nonfinite")):
+        with pytest.raises(ValueError, match=what):
+            zs.zs3_clip_tensors([_t()], scale, flag, stream=0)
+    assert not rec.calls

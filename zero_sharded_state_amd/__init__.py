@@ -600,11 +600,27 @@ def zs3_reduce_scatter_coalesced_mx4(layout: int, rank: int, dtype, mode: int, d
 _GRAD_ROW = struct.Struct("=qQQiiii")
 
 
-def _sized(x, name: str, item: int, numel: int) -> Optional[int]:
-    """The address of x; a torch tensor has to hold numel elements of `item` bytes, one behind the other."""
+_KINDS: dict = {}
+
+
+def _kind(name):
+    """The torch types of a buffer of a list's type code, or of "double", "float", "int32"."""
+    if not _KINDS:
+        import torch
+        raw = (torch.int16, torch.uint16)       # 16-bit values as their bits, as ShardStep holds them
+        _KINDS.update({ZS3_FP16: (torch.float16, *raw), ZS3_BF16: (torch.bfloat16, *raw), ZS3_FP32: (torch.float32,),
+                       "double": (torch.float64,), "float": (torch.float32,), "int32": (torch.int32,)})
+    return _KINDS.get(name)
+
+
+def _sized(x, name: str, kind, numel: int) -> Optional[int]:
+    """The address of x; a torch tensor has to hold numel elements of that kind, one behind the other."""
+    if x is None or type(x) is int:
+        return x
     if hasattr(x, "data_ptr"):
-        if x.element_size() != item:
-            raise ValueError(f"{name} has {x.element_size()}-byte elements, not {item}-byte ones")
+        types = _kind(kind)             # None: a code that the call refuses
+        if types is not None and x.dtype not in types:
+            raise ValueError(f"{name} has {x.element_size()}-byte elements of {x.dtype}, not of {types[0]}")
         if not x.is_contiguous() or x.numel() < numel:
             raise ValueError(f"{name} is not {numel} elements one behind the other")
     return _ptr(x)
@@ -622,9 +638,9 @@ def zs3_grad_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
         dtype = codes[dtype] if type(dtype) is str else int(dtype)
         out_dtype = codes[out_dtype] if type(out_dtype) is str else dtype if out_dtype is None else int(out_dtype)
         if type(grad) is not int:
-            grad = _sized(grad, f"tensor {i}: grad", 4 if dtype == ZS3_FP32 else 2, numel)
+            grad = _sized(grad, f"tensor {i}: grad", dtype, numel)
         if type(out) is not int and out is not None:
-            out = _sized(out, f"tensor {i}: out", 4 if out_dtype == ZS3_FP32 else 2, numel)
+            out = _sized(out, f"tensor {i}: out", out_dtype, numel)
         rows.append(pack(numel, grad or 0, out or 0, dtype, out_dtype, 1 if get("shared") else 0, 0))
     arr = (zs3_grad_tensor * len(rows)).from_buffer_copy(b"".join(rows)) if rows else (zs3_grad_tensor * 1)()
     arr.count = len(rows)
@@ -655,9 +671,9 @@ def zs3_norm_args_of(*, sums, workspace=None, workspace_bytes: Optional[int] = N
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "data_ptr") else 0
     args = zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale),
-                         _sized(sums, "sums", 8, int(world) + 1), _sized(norm, "norm", 8, 1), _sized(scale, "scale", 4, 1),
-                         _sized(nonfinite, "nonfinite", 4, 1), _sized(tensor_norms, "tensor_norms", 8, 0), _ptr(workspace),
-                         int(workspace_bytes))
+                         _sized(sums, "sums", "double", int(world) + 1), _sized(norm, "norm", "double", 1),
+                         _sized(scale, "scale", "float", 1), _sized(nonfinite, "nonfinite", "int32", 1),
+                         _sized(tensor_norms, "tensor_norms", "double", 0), _ptr(workspace), int(workspace_bytes))
     args.room = tensor_norms.numel() if hasattr(tensor_norms, "data_ptr") else None      # of an address the caller knows
     return args
 
@@ -684,7 +700,8 @@ def zs3_norm_finalize(norm, stream=None) -> None:
 
 def zs3_clip_tensors(tensors, scale, nonfinite=None, stream=None) -> None:
     n, arr = _grad_list(tensors)
-    _check(lib().zs3_clip_tensors(n, arr, _ptr(scale), _ptr(nonfinite), _stream(stream)))
+    scale, nonfinite = _sized(scale, "scale", "float", 1), _sized(nonfinite, "nonfinite", "int32", 1)
+    _check(lib().zs3_clip_tensors(n, arr, scale, nonfinite, _stream(stream)))
 
 
 def zs3_accumulate_tensors(tensors, factor: float = 1.0, first: bool = False, norm=None, stream=None) -> None:

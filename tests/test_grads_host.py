@@ -426,9 +426,9 @@ def test_what_a_norm_writes_has_to_hold_it(monkeypatch):
             with pytest.raises(ValueError, match="tensor_norms has 0 elements"):
                 call([_t()], made(_args(tensor_norms=each[:0])), stream=0)
     assert not rec.calls
-    zs.zs3_grad_norm_tensors([_t()] * 3, _args(tensor_norms=each), stream=0)
-    zs.zs3_norm_finalize(_args(tensor_norms=each[:0]), stream=0)
-    assert len(rec.calls) == 2
+    for call, a in ((lambda a: zs.zs3_grad_norm_tensors([_t()] * 3, a, stream=0), each), (lambda a: zs.zs3_norm_finalize(a, stream=0), each[:0])):
+        with pytest.raises(ValueError, match="host memory"):        # long enough
+            call(_args(tensor_norms=a))
     for bad in (torch.zeros(64, dtype=torch.uint8)[::2], torch.zeros(1, dtype=torch.uint8).expand(1 << 20)):
         with pytest.raises(ValueError, match="workspace"):
             zs.zs3_norm_args_of(**dict(_args(workspace=bad), workspace_bytes=None))
@@ -461,3 +461,63 @@ def test_tensors_have_to_be_of_the_type_that_is_said(monkeypatch):
         with pytest.raises(ValueError, match=what):
             zs.zs3_clip_tensors([_t()], scale, flag, stream=0)
     assert not rec.calls
+
+
+class _On:
+    """A tensor's face, on a device that is not there."""
+
+    def __init__(self, device, dtype, pinned=False, n=16):
+        import torch
+        self.device, self.dtype, self.pinned, self.n = device, getattr(torch, dtype), pinned, n
+
+    def get_device(self):
+        return self.device
+
+    def is_pinned(self):
+        return self.pinned
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return BASE + 64 * (self.device + 2) + (1 << 30) * id(self) % (1 << 36) // 64 * 64
+
+
+def test_tensors_have_to_be_on_the_device_of_the_call(monkeypatch):
+    """Host memory and another GPU's do not reach a launch; addresses and pinned memory are the caller's word."""
+    rec = _Recorder()
+    monkeypatch.setattr(zs, "lib", lambda: rec)
+    monkeypatch.setattr(zs, "_device", lambda: 1, raising=False)
+    calls = (lambda ts, **a: zs.zs3_grad_norm_tensors(ts, _args(**a), stream=0),
+             lambda ts, **a: zs.zs3_accumulate_tensors(ts, norm=_args(**a), stream=0),
+             lambda ts, scale=BASE, nonfinite=None, **a: zs.zs3_clip_tensors(ts, scale, nonfinite, stream=0))
+    made = dict(sums="float64", norm="float64", scale="float32", nonfinite="int32", tensor_norms="float64", workspace="uint8")
+    for device, text in ((-1, "host memory in a call on the GPU"), (0, "cuda:0 in a call on cuda:1")):
+        g, a = _On(device, "bfloat16"), _On(device, "float32")
+        for call in calls:
+            for d in (dict(grad=g), dict(out=a)):
+                for ts in ([_t(numel=16, **d)], zs.zs3_grad_tensor_list([_t(), _t(numel=16, **d)])):
+                    with pytest.raises(ValueError, match=text):
+                        call(ts)
+            for k, dtype in made.items():
+                if call is calls[2] and k not in ("scale", "nonfinite"):
+                    continue
+                with pytest.raises(ValueError, match=text):
+                    call([_t()], **dict({k: _On(device, dtype)}, **({"workspace_bytes": 64} if k == "workspace" else {})))
+        with pytest.raises(ValueError, match=text):
+            zs.zs3_norm_finalize(_args(scale=_On(device, "float32")), stream=0)
+    assert not rec.calls
+    with pytest.raises(ValueError, match="more than one device: host memory, cuda:1"):
+        zs.zs3_grad_tensor_list([_t(numel=16, grad=_On(1, "bfloat16")), _t(numel=16, grad=_On(-1, "bfloat16"))])
+    with pytest.raises(ValueError, match="more than one device: cuda:0, cuda:1"):
+        zs.zs3_norm_args_of(**_args(sums=_On(0, "float64"), scale=_On(1, "float32")))
+    for call in calls:
+        call([_t(numel=16, grad=_On(1, "bfloat16"), out=_On(-1, "float32", pinned=True))], scale=_On(1, "float32"), nonfinite=_On(-1, "int32", True))
+        call([_t()])
+    assert len(rec.calls) == 6

@@ -261,6 +261,18 @@ def _ptr(x) -> Optional[int]:
     return operator.index(x)       # an address: any integer type
 
 
+def _current_device() -> int:
+    global _device
+    if _device is None:
+        import torch
+        torch.cuda.current_device()                 # makes torch ready for its devices, once
+        _device = torch._C._cuda_getDevice
+    return _device()
+
+
+_device = None
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
         global _raw_stream
@@ -269,7 +281,8 @@ def _stream(s) -> Optional[int]:
             # the current stream's handle without a Stream object around it:
             # 0.3 us a call where torch.cuda.current_stream() takes 2.5, a
             # quarter of a small call's time
-            get, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            _current_device()
+            get, device = torch._C._cuda_getCurrentRawStream, _device
             _raw_stream = lambda: get(device())     # noqa: E731
         return _raw_stream()
     if isinstance(s, int):
@@ -613,8 +626,27 @@ def _kind(name):
     return _KINDS.get(name)
 
 
-def _sized(x, name: str, kind, numel: int) -> Optional[int]:
-    """The address of x; a torch tensor has to hold numel elements of that kind, one behind the other."""
+def _one_device(places: set) -> Optional[int]:
+    """The device that tensors lie on: None where all are addresses, -1 for host memory."""
+    if len(places) > 1:
+        raise ValueError("tensors on more than one device: " + ", ".join(_device_name(d) for d in sorted(places)))
+    return next(iter(places), None)
+
+
+def _device_name(d: int) -> str:
+    return f"cuda:{d}" if d >= 0 else "host memory"
+
+
+def _on_current(*devices: Optional[int]) -> None:
+    """Nothing but the current device's memory goes to a kernel."""
+    for d in devices:
+        if d is not None and (d < 0 or d != _current_device()):
+            raise ValueError(f"tensors on {_device_name(d)} in a call on " + (f"cuda:{_current_device()}" if d >= 0 else "the GPU"))
+
+
+def _sized(x, name: str, kind, numel: int, places: set) -> Optional[int]:
+    """The address of x; a torch tensor has to hold numel elements of that kind, one behind the
+    other.  Its device is added to places (pinned host memory is any device's)."""
     if x is None or type(x) is int:
         return x
     if hasattr(x, "data_ptr"):
@@ -623,6 +655,9 @@ def _sized(x, name: str, kind, numel: int) -> Optional[int]:
             raise ValueError(f"{name} has {x.element_size()}-byte elements of {x.dtype}, not of {types[0]}")
         if not x.is_contiguous() or x.numel() < numel:
             raise ValueError(f"{name} is not {numel} elements one behind the other")
+        device = x.get_device()
+        if device >= 0 or not x.is_pinned():
+            places.add(device)
     return _ptr(x)
 
 
@@ -631,25 +666,31 @@ def zs3_grad_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
     tensor with numel, grad, dtype and, where they differ from these, out=None,
     out_dtype=dtype ("fp32" where out is an accumulator), shared=False.  It holds
     addresses only: a caller keeps it for as long as its buffers stay where they are."""
-    pack, codes, rows = _GRAD_ROW.pack, _DTYPES_LOWBIT, []
+    pack, codes, rows, places = _GRAD_ROW.pack, _DTYPES_LOWBIT, [], set()
     for i, t in enumerate(tensors):
         get = t.get
         numel, dtype, grad, out, out_dtype = t["numel"], t["dtype"], t["grad"], get("out"), get("out_dtype")
         dtype = codes[dtype] if type(dtype) is str else int(dtype)
         out_dtype = codes[out_dtype] if type(out_dtype) is str else dtype if out_dtype is None else int(out_dtype)
         if type(grad) is not int:
-            grad = _sized(grad, f"tensor {i}: grad", dtype, numel)
+            grad = _sized(grad, f"tensor {i}: grad", dtype, numel, places)
         if type(out) is not int and out is not None:
-            out = _sized(out, f"tensor {i}: out", out_dtype, numel)
+            out = _sized(out, f"tensor {i}: out", out_dtype, numel, places)
         rows.append(pack(numel, grad or 0, out or 0, dtype, out_dtype, 1 if get("shared") else 0, 0))
     arr = (zs3_grad_tensor * len(rows)).from_buffer_copy(b"".join(rows)) if rows else (zs3_grad_tensor * 1)()
-    arr.count = len(rows)
+    arr.count, arr.device = len(rows), _one_device(places)
     return arr
 
 
 def _grad_list(tensors):
     arr = tensors if isinstance(tensors, ctypes.Array) else zs3_grad_tensor_list(tensors)
     return getattr(arr, "count", len(arr)), arr
+
+
+def _grad_list_here(tensors):
+    n, arr = _grad_list(tensors)
+    _on_current(getattr(arr, "device", None))
+    return n, arr
 
 
 def zs3_norm_workspace_bytes(tensors) -> int:
@@ -666,15 +707,17 @@ def zs3_norm_args_of(*, sums, workspace=None, workspace_bytes: Optional[int] = N
     ``zs3_grad_tensor_list``; a tensor given as the workspace brings its bytes (it
     is zeros before its first use: ``torch.zeros(zs3_norm_workspace_bytes(tensors),
     dtype=torch.uint8, device="cuda")``)."""
-    if hasattr(workspace, "data_ptr") and not workspace.is_contiguous():
-        raise ValueError("workspace is not bytes one behind the other")
+    places: set = set()
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "data_ptr") else 0
     args = zs3_norm_args(int(kind), int(rank), int(world), int(bool(finalize)), float(max_norm), float(loss_scale),
-                         _sized(sums, "sums", "double", int(world) + 1), _sized(norm, "norm", "double", 1),
-                         _sized(scale, "scale", "float", 1), _sized(nonfinite, "nonfinite", "int32", 1),
-                         _sized(tensor_norms, "tensor_norms", "double", 0), _ptr(workspace), int(workspace_bytes))
-    args.room = tensor_norms.numel() if hasattr(tensor_norms, "data_ptr") else None      # of an address the caller knows
+                         _sized(sums, "sums", "double", int(world) + 1, places), _sized(norm, "norm", "double", 1, places),
+                         _sized(scale, "scale", "float", 1, places), _sized(nonfinite, "nonfinite", "int32", 1, places),
+                         _sized(tensor_norms, "tensor_norms", "double", 0, places), _sized(workspace, "workspace", "bytes", 0, places),
+                         int(workspace_bytes))
+    if hasattr(tensor_norms, "data_ptr"):       # what there is room for at that address
+        args.room = args.tensor_norms, tensor_norms.numel()
+    args.device = _one_device(places)
     return args
 
 
@@ -682,15 +725,16 @@ def _norm_args(a, n: int = 0) -> zs3_norm_args:
     """The arguments of a norm over a list of n."""
     a = a if isinstance(a, zs3_norm_args) else zs3_norm_args_of(**a)
     room = getattr(a, "room", None)
-    if room is not None and room < n:
-        raise ValueError(f"tensor_norms has {room} elements, the list {n} tensors")
+    if room is not None and room[0] == a.tensor_norms and room[1] < n:
+        raise ValueError(f"tensor_norms has {room[1]} elements, the list {n} tensors")
+    _on_current(getattr(a, "device", None))
     return a
 
 
 def zs3_grad_norm_tensors(tensors, norm, stream=None) -> None:
     """``tensors``: what ``zs3_grad_tensor_list`` gives, or the dicts; ``norm``:
     what ``zs3_norm_args_of`` gives, or a dict of its arguments."""
-    n, arr = _grad_list(tensors)
+    n, arr = _grad_list_here(tensors)
     _check(lib().zs3_grad_norm_tensors(n, arr, ctypes.byref(_norm_args(norm, n)), _stream(stream)))
 
 
@@ -699,13 +743,15 @@ def zs3_norm_finalize(norm, stream=None) -> None:
 
 
 def zs3_clip_tensors(tensors, scale, nonfinite=None, stream=None) -> None:
-    n, arr = _grad_list(tensors)
-    scale, nonfinite = _sized(scale, "scale", "float", 1), _sized(nonfinite, "nonfinite", "int32", 1)
+    n, arr = _grad_list_here(tensors)
+    places: set = set()
+    scale, nonfinite = _sized(scale, "scale", "float", 1, places), _sized(nonfinite, "nonfinite", "int32", 1, places)
+    _on_current(_one_device(places))
     _check(lib().zs3_clip_tensors(n, arr, scale, nonfinite, _stream(stream)))
 
 
 def zs3_accumulate_tensors(tensors, factor: float = 1.0, first: bool = False, norm=None, stream=None) -> None:
-    n, arr = _grad_list(tensors)
+    n, arr = _grad_list_here(tensors)
     _check(lib().zs3_accumulate_tensors(n, arr, float(factor), int(bool(first)),
                                         ctypes.byref(_norm_args(norm, n)) if norm is not None else None, _stream(stream)))
 

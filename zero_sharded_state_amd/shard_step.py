@@ -580,8 +580,9 @@ class ShardStep:
 
     def _norm_args(self, finalize: bool, **over):
         return zs.zs3_norm_args_of(**dict(
-            dict(rank=self.rank, world=self.N, finalize=finalize, max_norm=self.max_norm, sums=self.sumsq, norm=self.norm_ptr,
-                 scale=self.scale_ptr, nonfinite=self.flag_ptr, workspace=self.norm_workspace), **over))
+            dict(rank=self.rank, world=self.N, finalize=finalize, max_norm=self.max_norm, sums=self.sumsq.data_ptr(),
+                 norm=self.norm_ptr, scale=self.scale_ptr, nonfinite=self.flag_ptr, workspace=self.norm_workspace.data_ptr(),
+                 workspace_bytes=self.norm_workspace.numel()), **over))
 
     def _begin(self):
         """Counts the step that a first micro-batch begins, once: seeds and AdamW go by it."""
@@ -624,7 +625,7 @@ class ShardStep:
         norms run on too (they share a workspace): a reader elsewhere waits for it."""
         with self._allocating_on(stream):
             each = self.torch.empty(len(self.params), dtype=self.torch.float64, device=self.device)
-        args = self._norm_args(False, rank=0, world=1, sums=self.each_sums, tensor_norms=each,
+        args = self._norm_args(False, rank=0, world=1, sums=self.each_sums.data_ptr(), tensor_norms=each.data_ptr(),
                                kind=zs.ZS3_NORM_INF if inf else zs.ZS3_NORM_2)
         zs.zs3_grad_norm_tensors(self._grad_list, args, stream=stream if stream is not None else self._stream())
         return each

@@ -644,6 +644,14 @@ def _on_current(*devices: Optional[int]) -> None:
             raise ValueError(f"tensors on {_device_name(d)} in a call on " + (f"cuda:{_current_device()}" if d >= 0 else "the GPU"))
 
 
+def _fits(x, types, numel: int, device: int) -> bool:
+    """Whether x is a tensor that ``_sized`` takes as it is, on that device."""
+    try:
+        return x.dtype in types and x.get_device() == device and x.numel() >= numel and x.is_contiguous()
+    except (AttributeError, TypeError):
+        return False
+
+
 def _sized(x, name: str, kind, numel: int, places: set) -> Optional[int]:
     """The address of x; a torch tensor has to hold numel elements of that kind, one behind the
     other.  Its device is added to places (pinned host memory is any device's)."""
@@ -666,16 +674,25 @@ def zs3_grad_tensor_list(tensors: Sequence[dict]) -> ctypes.Array:
     tensor with numel, grad, dtype and, where they differ from these, out=None,
     out_dtype=dtype ("fp32" where out is an accumulator), shared=False.  It holds
     addresses only: a caller keeps it for as long as its buffers stay where they are."""
-    pack, codes, rows, places = _GRAD_ROW.pack, _DTYPES_LOWBIT, [], set()
+    pack, codes, kinds, rows, places, here = _GRAD_ROW.pack, _DTYPES_LOWBIT, _KINDS, [], set(), None
     for i, t in enumerate(tensors):
         get = t.get
         numel, dtype, grad, out, out_dtype = t["numel"], t["dtype"], t["grad"], get("out"), get("out_dtype")
         dtype = codes[dtype] if type(dtype) is str else int(dtype)
         out_dtype = codes[out_dtype] if type(out_dtype) is str else dtype if out_dtype is None else int(out_dtype)
+        # tensors as the ones before them are taken at a glance
         if type(grad) is not int:
-            grad = _sized(grad, f"tensor {i}: grad", dtype, numel, places)
+            if here is not None and _fits(grad, kinds.get(dtype), numel, here):
+                grad = grad.data_ptr()
+            else:
+                grad = _sized(grad, f"tensor {i}: grad", dtype, numel, places)
+                here = next(iter(places), None)
         if type(out) is not int and out is not None:
-            out = _sized(out, f"tensor {i}: out", out_dtype, numel, places)
+            if here is not None and _fits(out, kinds.get(out_dtype), numel, here):
+                out = out.data_ptr()
+            else:
+                out = _sized(out, f"tensor {i}: out", out_dtype, numel, places)
+                here = next(iter(places), None)
         rows.append(pack(numel, grad or 0, out or 0, dtype, out_dtype, 1 if get("shared") else 0, 0))
     arr = (zs3_grad_tensor * len(rows)).from_buffer_copy(b"".join(rows)) if rows else (zs3_grad_tensor * 1)()
     arr.count, arr.device = len(rows), _one_device(places)
@@ -688,9 +705,26 @@ def _grad_list(tensors):
 
 
 def _grad_list_here(tensors):
-    n, arr = _grad_list(tensors)
-    _on_current(getattr(arr, "device", None))
-    return n, arr
+    arr = tensors if isinstance(tensors, ctypes.Array) else zs3_grad_tensor_list(tensors)
+    device = getattr(arr, "device", None)
+    if device is not None:
+        _on_current(device)
+    return getattr(arr, "count", len(arr)), arr
+
+
+def _scalar(x, name: str, kind: str) -> Optional[int]:
+    """The address of one value of that kind."""
+    try:                                # what it mostly is, at a glance
+        if x.dtype is _KINDS[kind][0] and x.get_device() == _device():
+            p = x.data_ptr()
+            if p:
+                return p
+    except (KeyError, AttributeError, TypeError):
+        pass
+    places: set = set()
+    p = _sized(x, name, kind, 1, places)
+    _on_current(_one_device(places))
+    return p
 
 
 def zs3_norm_workspace_bytes(tensors) -> int:
@@ -727,7 +761,9 @@ def _norm_args(a, n: int = 0) -> zs3_norm_args:
     room = getattr(a, "room", None)
     if room is not None and room[0] == a.tensor_norms and room[1] < n:
         raise ValueError(f"tensor_norms has {room[1]} elements, the list {n} tensors")
-    _on_current(getattr(a, "device", None))
+    device = getattr(a, "device", None)
+    if device is not None:
+        _on_current(device)
     return a
 
 
@@ -744,9 +780,10 @@ def zs3_norm_finalize(norm, stream=None) -> None:
 
 def zs3_clip_tensors(tensors, scale, nonfinite=None, stream=None) -> None:
     n, arr = _grad_list_here(tensors)
-    places: set = set()
-    scale, nonfinite = _sized(scale, "scale", "float", 1, places), _sized(nonfinite, "nonfinite", "int32", 1, places)
-    _on_current(_one_device(places))
+    if type(scale) is not int:
+        scale = _scalar(scale, "scale", "float")
+    if nonfinite is not None and type(nonfinite) is not int:
+        nonfinite = _scalar(nonfinite, "nonfinite", "int32")
     _check(lib().zs3_clip_tensors(n, arr, scale, nonfinite, _stream(stream)))
 
 

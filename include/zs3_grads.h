@@ -64,7 +64,7 @@ typedef struct {
     int32_t rank, world;     /* 0 <= rank < world */
     int32_t finalize;
     double max_norm;         /* > 0 (may be infinite: measured, not clipped) */
-    double loss_scale;       /* > 0, finite */
+    double loss_scale;       /* > 0, finite, as is 1 / loss_scale in fp32 */
     double* sums;            /* dev, world + 1 */
     double* norm;            /* dev; this and the next two may be NULL where finalize = 0 */
     float* scale;            /* dev */

@@ -521,3 +521,14 @@ def test_tensors_have_to_be_on_the_device_of_the_call(monkeypatch):
         call([_t(numel=16, grad=_On(1, "bfloat16"), out=_On(-1, "float32", pinned=True))], scale=_On(1, "float32"), nonfinite=_On(-1, "int32", True))
         call([_t()])
     assert len(rec.calls) == 6
+
+
+@pytest.mark.parametrize("call", [_norm, _fused, lambda t, **a: zs.zs3_norm_finalize(_args(**a), stream=0)])
+def test_a_loss_scale_whose_reciprocal_is_infinite_is_refused(call):
+    """The scale of finite gradients is finite wherever the flag is 0: 1 / loss_scale rounds to at most the largest float."""
+    for v in (5e-324, 1e-300, 1e-40, 2.0 ** -128 * (1 - 2.0 ** -20)):
+        assert 1.0 / v >= 2.0 ** 128
+        _refused(zs.ZS3_EINVAL, "loss_scale", call, [_t()], loss_scale=v)
+    # the next larger ones get as far as the argument that is wrong besides
+    for v in (2.0 ** -128 * (1 + 2.0 ** -20), 1e-30):
+        _refused(zs.ZS3_EINVAL, "sums", call, [_t()], loss_scale=v, sums=0)

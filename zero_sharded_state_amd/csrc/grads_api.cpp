@@ -202,7 +202,9 @@ zs3_status check_finalize(const zs3_norm_args& a) {
     if (a.world < 1) return fail(ZS3_EINVAL, "world %d < 1", a.world);
     if (a.rank < 0 || a.rank >= a.world) return fail(ZS3_EINVAL, "rank %d outside [0, %d)", a.rank, a.world);
     if (!(a.max_norm > 0.0)) return fail(ZS3_EINVAL, "max_norm must be > 0");
-    if (!(a.loss_scale > 0.0) || !std::isfinite(a.loss_scale)) return fail(ZS3_EINVAL, "loss_scale must be > 0 and finite");
+    // (below 2^-128 the scale of finite gradients would be infinite, with no flag set)
+    if (!(a.loss_scale > 0.0) || !std::isfinite(a.loss_scale) || !std::isfinite(static_cast<float>(1.0 / a.loss_scale)))
+        return fail(ZS3_EINVAL, "loss_scale must be > 0 and finite, and 1 / loss_scale finite in fp32");
     if (a.sums == nullptr || !aligned(a.sums, 8)) return fail(ZS3_EINVAL, "sums is NULL or not 8-byte aligned");
     return ZS3_OK;
 }

@@ -689,10 +689,15 @@ constexpr unsigned kManyLds = 32 * 1024;
 
 template <int OP, int N>
 static hipError_t accumulate_launch(int32_t kind, const WritePlanOf<N>& plan, float factor, double* entries, hipStream_t stream) {
-    // LDS that is reserved and never used: five workgroups a CU instead of eight, as many
-    // streams as HBM takes best where a launch reads and writes gigabytes (the 1.0B elements
-    // of a share of 291 tensors 1655 -> 1560 us, with the sums 1625 -> 1573; equal on 400
-    // of 1M; smaller launches lose: 27M elements 50 -> 54 us)
+    // LDS that is reserved and never used: four workgroups a CU instead of eight, as many streams
+    // as HBM takes best where a launch reads and writes gigabytes.  (LDS is given out by
+    // 1280 bytes: 33,280 a workgroup, with the sums' 32 or without, of 163,840.)  One
+    // tensor, 290 even ones, 290 odd ones, a mixed list, us at eight a CU and at four:
+    //     205M elements   331 313 312 302 -> 314 313 314 303    with the sums   339 331 327 312 -> 322 320 321 309
+    //     420M            699 668 657 628 -> 650 658 656 628                    699 701 687 657 -> 660 666 663 636
+    //     1.0B            1701 1629 1626 1564 -> 1576 1579 1585 1516            1680 1662 1662 1605 -> 1582 1592 1594 1529
+    // Five a CU: 320 313 311 304 at 205M, 1613 1595 1592 1531 at 1.0B.  50M to 150M gain or lose up to 2%,
+    // one tensor gains 4; 27M lose (50 -> 54).
     const int64_t tiles = plan.first_tile[plan.n];
     const unsigned lds = OP == kAdd && tiles >= kManyTiles ? kManyLds : 0;
     auto kernel = kind == 0 ? k_accumulate<OP, 0, N> : kind == kMax ? k_accumulate<OP, kMax, N> : k_accumulate<OP, kSum, N>;

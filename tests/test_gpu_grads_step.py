@@ -401,3 +401,42 @@ def test_an_optimizer_of_the_callers_own(K, fuse, phases):
                     assert torch.equal(step.full[o + lo:o + hi], step.shard[p["shard_offset"]:p["shard_offset"] + hi - lo])
     finally:
         step.destroy()
+
+
+@pytest.mark.parametrize("accumulate", [1, 2])
+def test_a_norm_that_waits_for_the_other_ranks(accumulate):
+    """The sums first, the end of the norm after the others' have come: the norm that has them at once, bit for bit
+    where the same kernel ends it."""
+    import torch
+    note(f"norm in two parts, accumulate={accumulate}")
+    rng = np.random.default_rng(31)
+    step = _make(4, 2, "bf16", accumulate=accumulate)
+    try:
+        _start(step, rng)
+        step.recv.copy_(torch.from_numpy(oracle.from_f32(rng.standard_normal(step.recv.numel()).astype(np.float32), "bf16").view(np.int16)))
+        peers = [0.5, 7.0, 0.0, 11.0, 0.0]
+        outs = []
+        for parts in (True, False):
+            step.outs.fill_(-1.0)
+            step.sumsq.copy_(torch.tensor([0.0] * 5 if parts else peers, dtype=torch.float64))
+            for k in range(accumulate):
+                step.reduce_scatter()
+                if accumulate > 1:
+                    step.accumulate_grads(norm=k == accumulate - 1, finalize=not parts)
+            if accumulate == 1:
+                step.grad_norm(finalize=not parts)
+            if parts:
+                sync()
+                assert bool((step.outs == -1.0).all())
+                for v in (0, 1, 3):
+                    step.sumsq[v] = peers[v]
+                step.finalize_norm()
+            sync()
+            outs.append((float(step.outs[0]), float(step.outs.view(torch.float32)[2]), int(step.outs.view(torch.int32)[3])))
+        (na, sa, fa), (nb, sb, fb) = outs
+        # two sums of the same world + 1 positive terms, a root; the scale rounded to fp32 from these
+        assert abs(na - nb) <= 8 * 2.0 ** -53 * nb and abs(sa - sb) <= 2.0 ** -23 * sb and fa == fb == 0
+        if accumulate > 1:
+            assert na == nb and sa == sb
+    finally:
+        step.destroy()

@@ -532,3 +532,18 @@ def test_a_loss_scale_whose_reciprocal_is_infinite_is_refused(call):
     # the next larger ones get as far as the argument that is wrong besides
     for v in (2.0 ** -128 * (1 + 2.0 ** -20), 1e-30):
         _refused(zs.ZS3_EINVAL, "sums", call, [_t()], loss_scale=v, sums=0)
+
+
+def test_the_norm_of_the_sum_can_wait_for_the_other_ranks(monkeypatch):
+    st, rec = _host_step(accumulate=2), _Recorder()
+    with monkeypatch.context() as m:
+        m.setattr(zs, "lib", lambda: rec)
+        st.accumulate_grads(stream=0)
+        st.accumulate_grads(stream=0, norm=True, finalize=False)
+        st.finalize_norm(stream=0)
+        st.accumulate_grads(stream=0, norm=True)
+    acc = [a[4] for name, a in rec.calls if name == "zs3_accumulate_tensors"]
+    assert acc[0] is None and [a._obj.finalize for a in acc[1:]] == [0, 1]
+    (end,) = [a[0]._obj for name, a in rec.calls if name == "zs3_norm_finalize"]
+    assert (end.sums, end.norm, end.rank, end.world) == (st.sumsq.data_ptr(), st.norm_ptr, 1, 2)
+    st.destroy()

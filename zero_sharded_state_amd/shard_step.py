@@ -594,13 +594,14 @@ class ShardStep:
         if self.micro != 0:
             raise ValueError(f"{what} takes the whole sum, of which {self.micro} of {self.accumulate} micro-batches are there")
 
-    def accumulate_grads(self, stream=None, norm: bool = False):
+    def accumulate_grads(self, stream=None, norm: bool = False, finalize: bool = True):
         """Adds the flat gradient, over the number of micro-batches, to the
         accumulators and counts it (the first of a step overwrites them, the last one makes the
-        sum whole), with the norm of the sum so far where asked."""
+        sum whole), with the norm of the sum so far where asked; without ``finalize`` only its
+        sums, which ``finalize_norm`` ends once the ranks have exchanged them."""
         if self.acc is None:
             raise ValueError("accumulate is 1: there are no accumulators")
-        args = self._norm_args(True) if norm else None
+        args = self._norm_args(finalize) if norm else None
         self._begin()
         zs.zs3_accumulate_tensors(self._acc_list, 1.0 / self.accumulate, first=self.micro == 0, norm=args,
                                   stream=stream if stream is not None else self._stream())
@@ -636,6 +637,11 @@ class ShardStep:
         ``gradient_step``, in place of ``adam_step``, which takes the scale itself."""
         self._whole("clip_grads")
         zs.zs3_clip_tensors(self._grad_list, self.scale_ptr, self.flag_ptr, stream=stream if stream is not None else self._stream())
+
+    def finalize_norm(self, stream=None):
+        """The norm, the clip scale and the flag from the ranks' sums in ``sumsq``, with nothing read again: after
+        ``grad_norm(finalize=False)`` or ``accumulate_grads(norm=True, finalize=False)`` and an exchange."""
+        zs.zs3_norm_finalize(self._norm_args(True), stream=stream if stream is not None else self._stream())
 
     def grad_norm(self, finalize: bool = True, stream=None):
         if self.acc is not None:

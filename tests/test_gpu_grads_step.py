@@ -440,3 +440,32 @@ def test_a_norm_that_waits_for_the_other_ranks(accumulate):
             assert na == nb and sa == sb
     finally:
         step.destroy()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_equal_halves_step_to_the_same_bits(bits, dtype):
+    """Two equal micro-batches accumulate to their gradient itself (halving is exact); with a clip norm that
+    is not reached both scales are 1, and master, moments and shard are those of the step that takes it at once."""
+    import torch
+    note(f"equal halves, {bits}-bit states, {dtype}")
+    rng = np.random.default_rng(41)
+    a = _make(4, 1, dtype, state_bits=bits, fuse_norm=True, accumulate=2, no_decay=[9], seed=3, max_norm=1e9)
+    b = _make(4, 1, dtype, state_bits=bits, fuse_norm=True, no_decay=[9], seed=3, max_norm=1e9)
+    try:
+        for st in (a, b):
+            _start(st, np.random.default_rng(9))
+        for _ in range(3):
+            grads = [{d: oracle.from_f32((rng.standard_normal(n) * 1e-1).astype(np.float32), dtype) for d, n in zip(IDS, SIZES)}
+                     for _ in range(4)]
+            for st in (a, b):
+                _send(st, grads, 1)
+            a.micro_step()
+            a.step()
+            b.step()
+            sync()
+            assert float(a.outs.view(torch.float32)[2]) == float(b.outs.view(torch.float32)[2]) == 1.0
+            for x, y in ((a.master, b.master), (a.exp_avg, b.exp_avg), (a.exp_avg_sq, b.exp_avg_sq), (a.shard, b.shard)):
+                assert torch.equal(x, y)
+    finally:
+        a.destroy(), b.destroy()

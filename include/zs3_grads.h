@@ -50,12 +50,15 @@ typedef struct {
  *   tensor_norms:  [t] = sqrt(S_t) or S_t: of this rank's part, not divided by
  *                  loss_scale.
  * The other entries of sums are the caller's: in a multi-GPU run every rank
- * calls with finalize = 0, the ranks exchange their sums[rank] (sums[world]
- * is the same on every rank already), and zs3_norm_finalize ends the norm.
+ * calls with finalize = 0, the ranks exchange their sums[rank], and
+ * zs3_norm_finalize ends the norm.  sums[world] is the same on every rank up
+ * to the rounding of its sum, whose order goes by the rank's whole list: taken
+ * from one rank with the exchange, it leaves every rank with the same sums, and
+ * from the same sums every rank ends with the same bits.
  * *norm is that of the gradients without their loss scale, and it is that norm
  * which max_norm bounds (zs3_grad_norm compares the scaled one: the two agree
- * where loss_scale = 1).  The order of every sum is fixed by the list: a call gives
- * the same bits again.
+ * where loss_scale = 1).  The order of every sum is fixed by the list (and the tensors'
+ * places in lines of 128 bytes): a call gives the same bits again.
  */
 enum { ZS3_NORM_2 = 1, ZS3_NORM_INF = 2 };
 

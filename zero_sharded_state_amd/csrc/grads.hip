@@ -172,21 +172,21 @@ __device__ __forceinline__ double group_join(double x, double* sh) {
     return x;
 }
 
-// The peers' sums, read by the lanes of a wave.
-template <int KIND>
+// The sums of the first 64 ranks, one a lane, read ahead of the end (the own one is not there yet).
 __device__ __forceinline__ double peers_of(const NormEnd& e) {
-    double x = 0.0;
-    if (e.finalize)
-        for (int v = static_cast<int>(threadIdx.x & 63); v < e.world; v += 64)
-            if (v != e.rank) x = join<KIND>(x, e.sums[v]);
-    return x;
+    const int lane = static_cast<int>(threadIdx.x & 63);
+    return e.finalize && lane < e.world && lane != e.rank ? e.sums[lane] : 0.0;
 }
 
-// The end of the norm (see the header's definition), by a wave whose lanes hold the
-// peers' sums.
+// The end of the norm (see the header's definition), by a wave whose lanes hold the first ranks'
+// sums.  Lane l joins those of ranks l, l + 64, ...: an order that is the same on every rank, so
+// that ranks that hold the same sums end with the same bits.
 template <int KIND>
 __device__ __forceinline__ void end_of_norm(const NormEnd& e, double peers, double own, double shared) {
-    const double total = join<KIND>(join<KIND>(wave_join<KIND>(peers), own), shared);
+    const int lane = static_cast<int>(threadIdx.x & 63);
+    double x = lane == e.rank ? own : peers;
+    for (int v = lane + 64; v < e.world; v += 64) x = join<KIND>(x, v == e.rank ? own : e.sums[v]);
+    const double total = join<KIND>(wave_join<KIND>(x), shared);
     const bool bad = !(__builtin_fabs(total) <= 1.7976931348623157e308);
     const double norm = root<KIND>(total) / e.loss_scale;
     double coef = e.max_norm / (norm + 1e-6);
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(kGrBlock) __attribute__((amdgpu_waves_per_eu(8))) v
     }
     __syncthreads();
     if (last == 0) return;
-    const double peers = peers_of<KIND>(e);
+    const double peers = peers_of(e);
     join_entries<KIND, kGrBlock, true>(parts.all, 0, mine - parts.all + 2 * int64_t(static_cast<int32_t>(gridDim.x) - b), sh, own, shared);
     write_sums<KIND>(e, peers, own, shared);
     if (parts.tensor_norms != nullptr) {
@@ -480,7 +480,7 @@ __global__ __launch_bounds__(kGrBlock* kFewTiles) void k_norm_few(const NormPlan
     __shared__ double sh[kFewTiles * kWaves];
     const int lane = static_cast<int>(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int32_t t = wave / kWaves;
-    const double peers = peers_of<KIND>(e);
+    const double peers = peers_of(e);
     Part<KIND> part;
     if (t < plan.first_tile[plan.n]) {
         const int s = find_tensor(plan, t, lane);
@@ -585,7 +585,7 @@ __global__ __launch_bounds__(kGrBlock) void k_join(const double* __restrict__ en
     __shared__ uint32_t last;
     const int64_t i0 = blockIdx.x * per, i1 = i0 + per < n ? i0 + per : n;
     double own, shared;
-    const double peers = peers_of<KIND>(e);
+    const double peers = peers_of(e);
     join_entries<KIND, kGrBlock, false>(entries, i0, i1, sh, own, shared);
     if (threadIdx.x == 0) {
         put(to + 2 * blockIdx.x, entry(own, false));
@@ -604,14 +604,14 @@ template <int KIND>
 __global__ __launch_bounds__(kEndBlock) void k_norm_end(const double* __restrict__ entries, int64_t n, const NormEnd e) {
     __shared__ double sh[2 * (kEndBlock / 64)];
     double own, shared;
-    const double peers = peers_of<KIND>(e);
+    const double peers = peers_of(e);
     join_entries<KIND, kEndBlock, false>(entries, 0, n, sh, own, shared);
     write_sums<KIND>(e, peers, own, shared);
 }
 
 template <int KIND>
 __global__ __launch_bounds__(64) void k_norm_finalize(const NormEnd e) {
-    end_of_norm<KIND>(e, peers_of<KIND>(e), e.sums[e.rank], e.sums[e.world]);
+    end_of_norm<KIND>(e, peers_of(e), e.sums[e.rank], e.sums[e.world]);
 }
 
 }  // namespace

@@ -79,7 +79,9 @@ typedef struct {
 
 /* Bytes of workspace that a list of these sizes and types needs (the
  * addresses in it are not looked at).  Fill a workspace with zeros once, before
- * its first use: it starts with counters that every call leaves at 0.  One
+ * its first use: it starts with counters that every call leaves at 0 (from others
+ * a norm ends too early or not at all: its outputs are wrong or not written,
+ * without an error).  One
  * workspace serves any lists it is large enough for, calls one after
  * the other; calls that may run at once (on two streams, in two graphs that are
  * replayed side by side) need one each, and outputs of their own. */

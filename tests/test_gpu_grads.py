@@ -670,3 +670,33 @@ def test_a_tensor_past_32_bits():
     assert float(acc[0]) == -3.0 and float(acc[n + 1]) == -3.0
     assert int(torch.count_nonzero(acc[1:1 + n])) == len(at)
     assert nm.got()["norm"] == math.sqrt(sum((i + 1) ** 2 for i in range(len(at))))
+
+
+def test_lists_made_of_tensors():
+    """Device tensors, their bits and pinned host memory; ordinary host memory is refused before a launch."""
+    import torch
+    require_gpu()
+    note("lists of tensors")
+    rng = np.random.default_rng(40)
+    x = rng.standard_normal(5000).astype(np.float32)
+    g = torch.from_numpy(x).cuda().bfloat16()
+    held = og.widened(g.view(torch.int16).cpu().numpy().view(np.uint16), "bf16")
+    scale, flag = _scalar(0.5, torch.float32), _scalar(0, torch.int32)
+    for grad in (g, g.view(torch.int16)):
+        for acc in (torch.zeros(5000, device="cuda"), torch.zeros(5000, pin_memory=True)):
+            arr = zs.zs3_grad_tensor_list([dict(numel=5000, grad=grad, dtype="bf16", out=acc, out_dtype="fp32")] * 1)
+            n = Norm(arr, max_norm=math.inf, per_tensor=False)
+            zs.zs3_accumulate_tensors(arr, 0.5, first=True, norm=n.args)
+            torch.cuda.synchronize()
+            want = og.accumulate(held, held, 0.5, True)
+            _same(acc.cpu().numpy(), want)
+            n.check([(want, False)])
+            zs.zs3_clip_tensors([dict(numel=5000, grad=acc, dtype="fp32")], scale, flag)
+            torch.cuda.synchronize()
+            _same(acc.cpu().numpy(), og.clip(want, 0.5, "fp32"))
+    for call in (lambda: zs.zs3_accumulate_tensors([dict(numel=9, grad=g, dtype="bf16", out=torch.zeros(9), out_dtype="fp32")]),
+                 lambda: zs.zs3_clip_tensors([dict(numel=9, grad=g.cpu(), dtype="bf16")], scale, flag),
+                 lambda: zs.zs3_clip_tensors([dict(numel=9, grad=g, dtype="bf16")], scale.cpu(), flag),
+                 lambda: zs.zs3_grad_norm_tensors([dict(numel=9, grad=g, dtype="bf16")], zs.zs3_norm_args_of(sums=torch.zeros(2, dtype=torch.float64)))):
+        with pytest.raises(ValueError, match="host memory"):
+            call()

@@ -530,7 +530,8 @@ class ShardStep:
 
     def reduce_scatter(self, stream=None):
         """Every gradient bucket, fanned out over the main and auxiliary
-        streams and joined back into the main stream."""
+        streams and joined back into the main stream.  With accumulators the first
+        one of a step advances ``t``, which the seeds of the 4-bit wire go by."""
         lib = zs.lib()
         if self.acc is not None:
             self._begin()
